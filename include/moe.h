@@ -64,17 +64,27 @@ typedef enum {
 
 typedef enum { MOE_GATE_SOFTMAX = 0, MOE_GATE_SIGMOID = 1 } moe_gating;
 
+/* Element types of the calls around the experts (norm, balance loss, e4m3 product). */
+typedef enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1 } moe_dtype;
+
 /* Device status word bits (moe_read_device_status). */
 #define MOE_DEV_BAD_ID 0x1u       /* an expert id outside [0, E): that slot was skipped     */
 #define MOE_DEV_DUP_ID 0x2u       /* an id repeated within one token: the repeat was skipped */
-#define MOE_DEV_TIMEOUT 0x4u      /* a bounded wait in moe_layer_forward gave up: y is invalid,
-                                     zero the workspace before the next call */
+#define MOE_DEV_TIMEOUT 0x4u      /* a bounded wait in moe_layer_forward or moe_fp8_matmul gave up:
+                                     y is invalid, zero the workspace before the next call */
+#define MOE_DEV_BAD_ROW 0x8u      /* moe_fp8_matmul: a row index outside x (that row of y is zero) or
+                                     offsets that fall or leave [0, M] (they are taken as the nearest
+                                     end of that range)                                         */
 
 /* Limits of this build. */
 #define MOE_MAX_TOKENS 16          /* T per call (small-batch decode)        */
 #define MOE_MAX_K 32               /* top-k                                  */
 #define MOE_MAX_EXPERTS 1024       /* E                                      */
 #define MOE_MAX_RANKS 64           /* partial outputs summed by moe_sum_partials */
+#define MOE_MAX_ROWS (1 << 24)     /* T, M, X of the calls around the experts  */
+#define MOE_MAX_PAIRS (1 << 22)    /* T*k of moe_expert_order                  */
+#define MOE_MAX_NORM_WIDTH 16384   /* n of moe_add_rmsnorm                     */
+#define MOE_FP8_GROUP 128          /* values that share a scale of an e4m3 row */
 
 /* ------------------------------------------------------------------ sizes */
 
@@ -351,9 +361,125 @@ size_t moe_layer_workspace_bytes(int T, int k, const moe_pool *pool, const moe_p
  */
 moe_status moe_sum_partials(const float *parts, int R, size_t n, float *y, cudaStream_t stream);
 
+/* --------------------------------------------------- around the experts */
+
+/*
+ * Residual addition, root-mean-square norm and the 8-bit rows that the
+ * products take, in one pass: per row of n values
+ *   s = x + residual                  (residual NULL: s = x)
+ *   v = s * (1 / sqrt(mean(s*s) + eps)) * weight
+ * in fp32, from the sum before its rounding to `dtype`.
+ *   x, residual  : device [T][n] of `dtype`; weight: device fp32 [n]
+ *   residual_out : device [T][n] of `dtype` out: s, or NULL.  May be x or residual.
+ *   y            : device [T][n] of `ydtype` out: v, or NULL (fp32 for an F32 router)
+ *   xq           : device out, T q8 records of v (moe_quantize_q8K's rule, bit for
+ *                  bit, of the fp32 v), or NULL; needs n % 32 == 0
+ *   x8, x8_scale : device out, e4m3 [T][n] and fp32 [T][ceil(n/128)], both or
+ *                  neither: per group of 128 values (the last one may be short)
+ *                  amax = max|v|, scale = amax/448, code = e4m3(v * (448/amax)),
+ *                  nearest, ties to even.  A group with amax < 2^-119 (the
+ *                  inverse would overflow) has scale 0 and codes 0.
+ * All outputs are written; apart from residual_out none may overlap an input.
+ * Limits: T in [0, MOE_MAX_ROWS] (0 is a no-op); n % 16 == 0, 16 <= n <=
+ * MOE_MAX_NORM_WIDTH; eps >= 0; |s| below 2^57 (squares are summed in fp32).
+ * Errors: MOE_ERR_INVALID_ARG for limits, types, no output at all, x8 without
+ * x8_scale or the reverse, a NULL input or a buffer that is not 16-byte aligned
+ * (x8_scale: 4); MOE_ERR_UNSUPPORTED for a width outside the rules above.
+ */
+moe_status moe_add_rmsnorm(const void *x, const void *residual, const float *weight, float eps, int T, int n,
+                           moe_dtype dtype, void *residual_out, void *y, moe_dtype ydtype, void *xq, void *x8,
+                           float *x8_scale, cudaStream_t stream);
+
+/*
+ * Per-expert counts and the order by expert of a routing (moe_route's ids, of
+ * any number of tokens): the (token, slot) pairs sorted by expert, and within
+ * an expert by token, then slot.
+ *   ids     : device int32 [T][k].  A pair whose id lies outside [0, E) takes
+ *             no part (-1: a padded token; another rank's expert).
+ *   counts  : device int32 [E] out: pairs per expert, or NULL
+ *   offsets : device int32 [E+1] out: expert e's pairs are the sorted places
+ *             [offsets[e], offsets[e+1]), or NULL
+ *   rows    : device int32 [T*k] out: the token of each sorted place, -1 in the
+ *             places from offsets[E] on, or NULL
+ *   pos     : device int32 [T][k] out: the sorted place of each pair, -1 for one
+ *             that takes no part, or NULL
+ *   ws      : device workspace of moe_expert_order_workspace_bytes(T, k, E)
+ *             bytes, 16-byte aligned; needs no preparation (0 bytes: may be NULL)
+ * Limits: T in [0, MOE_MAX_ROWS], 1 <= k <= MOE_MAX_K, T*k <= MOE_MAX_PAIRS,
+ * 1 <= E <= MOE_MAX_EXPERTS.  T == 0 writes zero counts and offsets.
+ * Errors: MOE_ERR_INVALID_ARG for limits, a NULL ids, a buffer that is not
+ * 4-byte aligned or no output; MOE_ERR_WORKSPACE for a missing, short or unaligned ws.
+ */
+moe_status moe_expert_order(const int32_t *ids, int T, int k, int E, int32_t *counts, int32_t *offsets,
+                            int32_t *rows, int32_t *pos, void *ws, size_t ws_bytes, cudaStream_t stream);
+size_t moe_expert_order_workspace_bytes(int T, int k, int E);
+
+/*
+ * The router's balance loss and its gradient, from the logits and the counts.
+ * With p[t][e] the gate probabilities over all E (softmax of the logits, or
+ * sigma(l) / sum sigma(l)), c = counts and N = sum c (N/k counted tokens):
+ *   loss = alpha * sum_e (E c_e / N) * (k/N * sum_t p[t][e])
+ * Even counts give alpha.  The counts carry no gradient:
+ *   dloss/dlogits[t][e] = alpha k/N * p[t][e] (f_e - sum_j f_j p[t][j])
+ * with f_e = E c_e / N, times (1 - sigma(l[t][e])) for sigmoid gating.
+ *   logits    : device [T][E] of `dtype`.  -inf marks an expert that a token may
+ *               not take (p = 0); a row of nothing but -inf adds nothing.
+ *   counts    : device int32 [E] >= 0 (moe_expert_order; with expert parallelism
+ *               or several micro-batches, of all of them)
+ *   valid     : device uint8 [T] or NULL: a token with 0 (padding) adds nothing
+ *               and has gradient 0; its logits are not looked at
+ *   grad_loss : device fp32 [1] that multiplies the gradient, or NULL (1)
+ *   loss      : device fp32 [1] out, or NULL
+ *   dlogits   : device [T][E] of `dtype` out, or NULL.  May be logits.
+ *   ws        : device workspace of moe_balance_loss_workspace_bytes(T, E) bytes,
+ *               16-byte aligned, zero-filled before its first use; every
+ *               completed call leaves it ready for the next one
+ * N == 0 gives loss 0 and gradient 0.  Sums run in a fixed order.
+ * Limits: T in [0, MOE_MAX_ROWS] (0: loss 0), 1 <= E <= MOE_MAX_EXPERTS,
+ * 1 <= k <= min(E, MOE_MAX_K).
+ * Errors: MOE_ERR_INVALID_ARG for limits, types, gating, a NULL input, no
+ * output, or logits, dlogits that are not 16-byte aligned (counts, loss,
+ * grad_loss: 4); MOE_ERR_WORKSPACE for a missing, short or unaligned ws.
+ */
+moe_status moe_balance_loss(const void *logits, moe_dtype dtype, const int32_t *counts, const uint8_t *valid, int T,
+                            int E, int k, moe_gating gating, float alpha, const float *grad_loss, float *loss,
+                            void *dlogits, void *ws, size_t ws_bytes, cudaStream_t stream);
+size_t moe_balance_loss_workspace_bytes(int T, int E);
+
+/*
+ * Products of e4m3 rows with e4m3 matrices that carry a scale for each block
+ * of 128 x 128 (rows: for each group of 128 values, as moe_add_rmsnorm makes
+ * them), on the tensor cores.  Grouped by expert, or one matrix for all rows:
+ *   y[i][n] = sum_b x_scale[r][b] * w_scale[g][n/128][b]
+ *             * sum_{j in block b} x8[r][j] * w[g][n][j],   r = rows ? rows[i] : i
+ * for the places i of each group g, offsets[g] <= i < offsets[g+1].
+ *   x8, x_scale : device e4m3 [X][K], fp32 [X][ceil(K/128)]
+ *   rows        : device int32 [M], values in [0, X), or NULL (needs X >= M)
+ *   offsets     : device int32 [G+1], rising, in [0, M], or NULL (G == 1, all M)
+ *   w, w_scale  : device e4m3 [G][N][K], fp32 [G][ceil(N/128)][ceil(K/128)]
+ *   y           : device [M][N] of `ydtype` out.  Rows of no group keep their values.
+ *   ws          : device workspace of moe_fp8_matmul_workspace_bytes() bytes
+ *                 (the status word, moe_read_device_status), zero-filled before
+ *                 its first use.  Calls that overlap on the GPU may share it.
+ * Products within a block of 128 are summed by the tensor cores in fp32, the
+ * scaled blocks in fp32, in one order for given sizes: equal calls give equal
+ * bits.  Other sizes (M, N, K, G) may split K in another way and round differently.
+ * Row indexes and offsets outside their ranges are never followed (MOE_DEV_BAD_ROW).
+ * Limits: X, M in [0, MOE_MAX_ROWS] (M == 0 is a no-op), 1 <= G <=
+ * MOE_MAX_EXPERTS, 1 <= N <= 2^20, K % 16 == 0, 16 <= K <= 2^20, G*N <= 2^30.
+ * Errors: MOE_ERR_INVALID_ARG for limits, types, a NULL buffer, X < M without
+ * rows, X == 0, offsets missing with G > 1, or x8, w, y not 16-byte aligned
+ * (scales, rows, offsets: 4); MOE_ERR_UNSUPPORTED for a K outside the rule
+ * above; MOE_ERR_WORKSPACE for a missing, short or unaligned ws.
+ */
+moe_status moe_fp8_matmul(const void *x8, const float *x_scale, int X, const int32_t *rows, int M,
+                          const int32_t *offsets, int G, const void *w, const float *w_scale, int N, int K,
+                          void *y, moe_dtype ydtype, void *ws, size_t ws_bytes, cudaStream_t stream);
+size_t moe_fp8_matmul_workspace_bytes(void);
+
 /*
  * Reads (and, if clear != 0, zeroes) the device status word at the start of
- * an FFN or layer workspace (both keep it in their first 4 bytes).
+ * an FFN, layer or e4m3 product workspace (all keep it in their first 4 bytes).
  * Synchronises `stream`.  *flags receives MOE_DEV_* bits.
  * Returns MOE_ERR_DEVICE_STATUS if any bit was set, MOE_OK otherwise.
  */

@@ -23,9 +23,13 @@ MAX_TOKENS, MAX_K, MAX_EXPERTS = 16, 32, 1024
 EXPORTS = ["moe_act_block", "moe_q8_row_bytes", "moe_packed_bytes", "moe_pack_weights", "moe_quantize_q8K",
            "moe_route", "moe_route_workspace_bytes", "moe_expert_ffn", "moe_ffn_workspace_bytes",
            "moe_read_device_status", "moe_debug_row_dots", "moe_status_str", "moe_expert_ffn_noalloc",
-           "moe_layer_forward", "moe_layer_workspace_bytes", "moe_sum_partials", "moe_debug_set_exchange_wait"]
+           "moe_layer_forward", "moe_layer_workspace_bytes", "moe_sum_partials", "moe_debug_set_exchange_wait",
+           "moe_add_rmsnorm", "moe_expert_order", "moe_expert_order_workspace_bytes", "moe_balance_loss",
+           "moe_balance_loss_workspace_bytes", "moe_fp8_matmul", "moe_fp8_matmul_workspace_bytes"]
 LAYER_OVERLAP_PREVIOUS = 0x1
-DEV_TIMEOUT = 0x4
+DEV_TIMEOUT, DEV_BAD_ROW = 0x4, 0x8
+DT_F32, DT_BF16 = 0, 1
+FP8_GROUP = 128          # values that share a scale of an e4m3 row
 
 _P = ctypes.c_void_p
 _lib_handle = None
@@ -91,6 +95,21 @@ def lib():
         L.moe_debug_row_dots.argtypes = [_P, i, i, i, i, _P, _P, _P]
         L.moe_sum_partials.restype = i
         L.moe_sum_partials.argtypes = [_P, i, sz, _P, _P]
+        f = ctypes.c_float
+        L.moe_add_rmsnorm.restype = i
+        L.moe_add_rmsnorm.argtypes = [_P, _P, _P, f, i, i, i, _P, _P, i, _P, _P, _P, _P]
+        L.moe_expert_order.restype = i
+        L.moe_expert_order.argtypes = [_P, i, i, i, _P, _P, _P, _P, _P, sz, _P]
+        L.moe_expert_order_workspace_bytes.restype = sz
+        L.moe_expert_order_workspace_bytes.argtypes = [i, i, i]
+        L.moe_balance_loss.restype = i
+        L.moe_balance_loss.argtypes = [_P, i, _P, _P, i, i, i, i, f, _P, _P, _P, _P, sz, _P]
+        L.moe_balance_loss_workspace_bytes.restype = sz
+        L.moe_balance_loss_workspace_bytes.argtypes = [i, i]
+        L.moe_fp8_matmul.restype = i
+        L.moe_fp8_matmul.argtypes = [_P, _P, i, _P, i, _P, i, _P, _P, i, i, _P, i, _P, sz, _P]
+        L.moe_fp8_matmul_workspace_bytes.restype = sz
+        L.moe_fp8_matmul_workspace_bytes.argtypes = []
         L.moe_debug_set_exchange_wait.restype = i
         L.moe_debug_set_exchange_wait.argtypes = [ctypes.c_longlong]
         L.moe_status_str.restype = ctypes.c_char_p
@@ -240,6 +259,149 @@ def moe_sum_partials(parts, y, stream=None):
     if parts.numel() != R * n:
         raise ValueError("parts must hold R partials of y's size")
     _check(lib().moe_sum_partials(_ptr(parts), R, n, _ptr(y), _stream(stream)), "moe_sum_partials")
+
+
+# --------------------------------------------------- around the experts
+#
+# These calls check shapes, types, devices and layouts here (ValueError) and run
+# on the device that holds the tensors, on its current stream unless one is given.
+
+_DT = {torch.float32: DT_F32, torch.bfloat16: DT_BF16}
+_E4M3 = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _expect(name: str, t, like, shape, dtypes):
+    """t is a contiguous CUDA tensor of this shape and one of these types, where `like` is; None passes."""
+    if t is None:
+        return
+    if t.shape != shape or t.dtype not in dtypes or not t.is_contiguous() or t.device != like.device:
+        raise ValueError(f"{name}: want a contiguous {' or '.join(map(str, dtypes))} tensor {tuple(shape)} on "
+                         f"{like.device}, got {t.dtype} {tuple(t.shape)} on {t.device}"
+                         f"{'' if t.is_contiguous() else ', not contiguous'}")
+
+
+def _ws(ws, like):
+    """(address, bytes) of a workspace; it lies where the inputs lie"""
+    if ws is None:
+        return None, 0
+    if ws.device != like.device or not ws.is_contiguous():
+        raise ValueError(f"ws: want a contiguous tensor on {like.device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _launch(call: str, fn, like, args, stream):
+    """fn(*args, stream) with the tensors' device current"""
+    if not like.is_cuda:
+        raise ValueError(f"{call}: tensors must be on a CUDA device")
+    index = like.device.index
+    if stream is None:
+        stream = torch.cuda.current_stream(index)
+    elif stream.device_index != index:
+        raise ValueError(f"{call}: the stream belongs to another device than the tensors")
+    if index == torch.cuda.current_device():
+        _check(fn(*args, stream.cuda_stream), call)
+    else:
+        with torch.cuda.device(index):
+            _check(fn(*args, stream.cuda_stream), call)
+
+
+def moe_add_rmsnorm(x, residual, weight, eps: float, residual_out=None, y=None, xq=None, x8=None, x8_scale=None,
+                    stream=None):
+    """s = x + residual (None: s = x), v = s / sqrt(mean(s^2) + eps) * weight, row by row.
+
+    x, residual, residual_out (s; may be x or residual): [T, n] fp32 or bf16.  y (v): [T, n] fp32 or bf16.
+    xq: q8 records of v (device_bytes(T * moe_q8_row_bytes(n))).  x8, x8_scale: e4m3 [T, n] and its fp32
+    scales [T, ceil(n / 128)].  Give the outputs that are wanted."""
+    if x.dim() != 2 or x.dtype not in _DT or not x.is_contiguous():
+        raise ValueError("x: want a contiguous fp32 or bf16 tensor [T, n]")
+    T, n = x.shape
+    shape = x.shape
+    _expect("residual", residual, x, shape, (x.dtype,))
+    _expect("weight", weight, x, (n,), (torch.float32,))
+    _expect("residual_out", residual_out, x, shape, (x.dtype,))
+    _expect("y", y, x, shape, (torch.float32, torch.bfloat16))
+    _expect("x8", x8, x, shape, _E4M3)
+    _expect("x8_scale", x8_scale, x, (T, -(-n // FP8_GROUP)), (torch.float32,))
+    if xq is not None and (xq.device != x.device or not xq.is_contiguous() or
+                           xq.numel() * xq.element_size() < T * moe_q8_row_bytes(n)):
+        raise ValueError(f"xq: want at least {T} x {moe_q8_row_bytes(n)} contiguous bytes on {x.device}")
+    _launch("moe_add_rmsnorm", lib().moe_add_rmsnorm, x,
+            (x.data_ptr(), _ptr(residual), _ptr(weight), eps, T, n, _DT[x.dtype], _ptr(residual_out), _ptr(y),
+             DT_F32 if y is None else _DT[y.dtype], _ptr(xq), _ptr(x8), _ptr(x8_scale)), stream)
+
+
+def moe_expert_order_workspace_bytes(T: int, k: int, E: int) -> int:
+    return lib().moe_expert_order_workspace_bytes(T, k, E)
+
+
+def moe_expert_order(ids, E: int, ws=None, counts=None, offsets=None, rows=None, pos=None, stream=None):
+    """The (token, slot) pairs of ids [T, k] sorted by expert: counts [E], offsets [E + 1], the token of each
+    sorted place rows [T * k] (-1 past the last) and the sorted place of each pair pos [T, k] (-1: takes no
+    part, its id is not in [0, E)).  All int32; give the outputs that are wanted."""
+    if ids.dim() != 2 or ids.dtype != torch.int32 or not ids.is_contiguous():
+        raise ValueError("ids: want a contiguous int32 tensor [T, k]")
+    T, k = ids.shape
+    i32 = (torch.int32,)
+    _expect("counts", counts, ids, (E,), i32)
+    _expect("offsets", offsets, ids, (E + 1,), i32)
+    _expect("rows", rows, ids, (T * k,), i32)
+    _expect("pos", pos, ids, ids.shape, i32)
+    _launch("moe_expert_order", lib().moe_expert_order, ids,
+            (ids.data_ptr(), T, k, E, _ptr(counts), _ptr(offsets), _ptr(rows), _ptr(pos), *_ws(ws, ids)), stream)
+
+
+def moe_balance_loss_workspace_bytes(T: int, E: int) -> int:
+    return lib().moe_balance_loss_workspace_bytes(T, E)
+
+
+def moe_balance_loss(logits, counts, k: int, gating: int, alpha: float, ws, loss=None, dlogits=None, valid=None,
+                     grad_loss=None, stream=None):
+    """The balance loss alpha * sum_e (E c_e / N)(mean p_e) of logits [T, E] (fp32 or bf16) and counts [E]
+    (moe_expert_order) into loss [1], and grad_loss [1] times its gradient into dlogits [T, E]; either may be
+    None.  valid: uint8 or bool [T], 0 for padded tokens."""
+    if logits.dim() != 2 or logits.dtype not in _DT or not logits.is_contiguous():
+        raise ValueError("logits: want a contiguous fp32 or bf16 tensor [T, E]")
+    T, E = logits.shape
+    f32 = (torch.float32,)
+    _expect("counts", counts, logits, (E,), (torch.int32,))
+    _expect("valid", valid, logits, (T,), (torch.uint8, torch.bool))
+    _expect("grad_loss", grad_loss, logits, (1,), f32)
+    _expect("loss", loss, logits, (1,), f32)
+    _expect("dlogits", dlogits, logits, logits.shape, (logits.dtype,))
+    _launch("moe_balance_loss", lib().moe_balance_loss, logits,
+            (logits.data_ptr(), _DT[logits.dtype], _ptr(counts), _ptr(valid), T, E, k, gating, alpha, _ptr(grad_loss),
+             _ptr(loss), _ptr(dlogits), *_ws(ws, logits)), stream)
+
+
+def moe_fp8_matmul_workspace_bytes() -> int:
+    return lib().moe_fp8_matmul_workspace_bytes()
+
+
+def moe_fp8_matmul(x8, x_scale, w, w_scale, y, ws, offsets=None, rows=None, stream=None):
+    """y = x8 @ w.T with the scales of both, dense or grouped by expert.
+
+    x8 [X, K] e4m3, x_scale [X, ceil(K/128)] fp32; w [N, K] or [G, N, K] e4m3, w_scale [ceil(N/128),
+    ceil(K/128)] or [G, ...] fp32; y [M, N] fp32 or bf16.  offsets int32 [G + 1]: the places of y of each
+    group (moe_expert_order); rows int32 [M]: the row of x8 of each place (None: the place itself)."""
+    if x8.dim() != 2 or x8.dtype not in _E4M3 or not x8.is_contiguous():
+        raise ValueError("x8: want a contiguous e4m3 tensor [X, K]")
+    if w.dim() not in (2, 3) or y.dim() != 2:
+        raise ValueError("w: want [N, K] or [G, N, K]; y: [M, N]")
+    X, K = x8.shape
+    N, M = w.shape[-2], y.shape[0]
+    kb, nb = -(-K // FP8_GROUP), -(-N // FP8_GROUP)
+    G = w.shape[0] if w.dim() == 3 else 1
+    lead = w.shape[:-2]
+    f32 = (torch.float32,)
+    _expect("x_scale", x_scale, x8, (X, kb), f32)
+    _expect("w", w, x8, (*lead, N, K), _E4M3)
+    _expect("w_scale", w_scale, x8, (*lead, nb, kb), f32)
+    _expect("y", y, x8, (M, N), (torch.float32, torch.bfloat16))
+    _expect("offsets", offsets, x8, (G + 1,), (torch.int32,))
+    _expect("rows", rows, x8, (M,), (torch.int32,))
+    _launch("moe_fp8_matmul", lib().moe_fp8_matmul, x8,
+            (x8.data_ptr(), x_scale.data_ptr(), X, _ptr(rows), M, _ptr(offsets), G, w.data_ptr(), w_scale.data_ptr(),
+             N, K, y.data_ptr(), _DT[y.dtype], *_ws(ws, x8)), stream)
 
 
 def moe_debug_set_exchange_wait(cycles: int):

@@ -1,6 +1,9 @@
 // moe_api.cu - the C ABI declared in include/moe.h: argument validation and
 // launches.  Every check happens before anything is enqueued.
+#include <math.h>
 #include <string.h>
+
+#include <initializer_list>
 
 #include "moe_common.cuh"
 #include "moe_launch.h"
@@ -10,6 +13,9 @@ using namespace moe;
 namespace {
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
+
+bool dtype_ok(int d) { return d == MOE_DT_F32 || d == MOE_DT_BF16; }
 
 bool expert_format(int q) {
     return q == MOE_Q8_0 || q == MOE_Q4_K || q == MOE_Q2_K || q == MOE_MXFP4 || q == MOE_Q6_K || q == MOE_Q3_K;
@@ -195,6 +201,84 @@ moe_status moe_sum_partials(const float *parts, int R, size_t n, float *y, cudaS
     if (n == 0) return MOE_OK;
     if (!parts || !y || !aligned16(parts) || !aligned16(y)) return MOE_ERR_INVALID_ARG;
     return cuda_status(launch_sum_partials(parts, R, n, y, stream));
+}
+
+moe_status moe_add_rmsnorm(const void *x, const void *residual, const float *weight, float eps, int T, int n,
+                           moe_dtype dtype, void *residual_out, void *y, moe_dtype ydtype, void *xq, void *x8,
+                           float *x8_scale, cudaStream_t stream) {
+    if (T < 0 || T > MOE_MAX_ROWS || !dtype_ok(dtype) || !dtype_ok(ydtype)) return MOE_ERR_INVALID_ARG;
+    if (!(eps >= 0.f) || isinf(eps)) return MOE_ERR_INVALID_ARG;
+    if (n < 16 || n > MOE_MAX_NORM_WIDTH || n % 16 || (xq && !act_block(n))) return MOE_ERR_UNSUPPORTED;
+    if (T == 0) return MOE_OK;
+    if ((x8 == nullptr) != (x8_scale == nullptr)) return MOE_ERR_INVALID_ARG;
+    if (!residual_out && !y && !xq && !x8) return MOE_ERR_INVALID_ARG;
+    if (!x || !weight) return MOE_ERR_INVALID_ARG;
+    for (const void *p : {x, residual, (const void *)weight, (const void *)residual_out, (const void *)y,
+                          (const void *)xq, (const void *)x8})
+        if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
+    if (!aligned4(x8_scale)) return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_norm(x, residual, weight, eps, T, n, dtype, residual_out, y, ydtype, (uint8_t *)xq,
+                                   (uint8_t *)x8, x8_scale, stream));
+}
+
+size_t moe_expert_order_workspace_bytes(int T, int k, int E) {
+    if (T <= 0 || k < 1 || E < 1) return 0;
+    return order_ws_bytes(T, k, E);
+}
+
+moe_status moe_expert_order(const int32_t *ids, int T, int k, int E, int32_t *counts, int32_t *offsets,
+                            int32_t *rows, int32_t *pos, void *ws, size_t ws_bytes, cudaStream_t stream) {
+    if (T < 0 || T > MOE_MAX_ROWS || k < 1 || k > MOE_MAX_K || E < 1 || E > MOE_MAX_EXPERTS)
+        return MOE_ERR_INVALID_ARG;
+    if ((long long)T * k > MOE_MAX_PAIRS) return MOE_ERR_INVALID_ARG;
+    if (!counts && !offsets && !rows && !pos) return T == 0 ? MOE_OK : MOE_ERR_INVALID_ARG;
+    if (T > 0 && !ids) return MOE_ERR_INVALID_ARG;
+    for (const void *p : {(const void *)ids, (const void *)counts, (const void *)offsets, (const void *)rows,
+                          (const void *)pos})
+        if (!aligned4(p)) return MOE_ERR_INVALID_ARG;
+    const size_t need = moe_expert_order_workspace_bytes(T, k, E);
+    if (need && (!ws || ws_bytes < need || !aligned16(ws))) return MOE_ERR_WORKSPACE;
+    return cuda_status(launch_order(ids, T, k, E, counts, offsets, rows, pos, ws, stream));
+}
+
+size_t moe_balance_loss_workspace_bytes(int T, int E) {
+    if (T < 0 || E < 1) return 0;
+    return balance_ws_bytes();
+}
+
+moe_status moe_balance_loss(const void *logits, moe_dtype dtype, const int32_t *counts, const uint8_t *valid, int T,
+                            int E, int k, moe_gating gating, float alpha, const float *grad_loss, float *loss,
+                            void *dlogits, void *ws, size_t ws_bytes, cudaStream_t stream) {
+    if (T < 0 || T > MOE_MAX_ROWS || E < 1 || E > MOE_MAX_EXPERTS || !dtype_ok(dtype)) return MOE_ERR_INVALID_ARG;
+    if (k < 1 || k > E || k > MOE_MAX_K) return MOE_ERR_INVALID_ARG;
+    if (gating != MOE_GATE_SOFTMAX && gating != MOE_GATE_SIGMOID) return MOE_ERR_INVALID_ARG;
+    if (!counts || !aligned4(counts) || !aligned4(grad_loss) || !aligned4(loss)) return MOE_ERR_INVALID_ARG;
+    if (!loss && !dlogits) return T == 0 ? MOE_OK : MOE_ERR_INVALID_ARG;
+    if (T > 0 && !logits) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(logits) || !aligned16(dlogits)) return MOE_ERR_INVALID_ARG;
+    if (!ws || ws_bytes < balance_ws_bytes() || !aligned16(ws)) return MOE_ERR_WORKSPACE;
+    return cuda_status(launch_balance(logits, dtype, counts, valid, T, E, k, gating, alpha, grad_loss, loss, dlogits,
+                                      ws, stream));
+}
+
+size_t moe_fp8_matmul_workspace_bytes(void) { return 256; }
+
+moe_status moe_fp8_matmul(const void *x8, const float *x_scale, int X, const int32_t *rows, int M,
+                          const int32_t *offsets, int G, const void *w, const float *w_scale, int N, int K,
+                          void *y, moe_dtype ydtype, void *ws, size_t ws_bytes, cudaStream_t stream) {
+    if (X < 0 || X > MOE_MAX_ROWS || M < 0 || M > MOE_MAX_ROWS || G < 1 || G > MOE_MAX_EXPERTS)
+        return MOE_ERR_INVALID_ARG;
+    if (N < 1 || N > (1 << 20) || (long long)G * N > (1ll << 30) || !dtype_ok(ydtype)) return MOE_ERR_INVALID_ARG;
+    if (K < 16 || K > (1 << 20) || K % 16) return MOE_ERR_UNSUPPORTED;
+    if (!offsets && G != 1) return MOE_ERR_INVALID_ARG;
+    if (M == 0) return MOE_OK;
+    if (X == 0 || (!rows && X < M)) return MOE_ERR_INVALID_ARG;
+    if (!x8 || !x_scale || !w || !w_scale || !y) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(x8) || !aligned16(w) || !aligned16(y)) return MOE_ERR_INVALID_ARG;
+    if (!aligned4(x_scale) || !aligned4(w_scale) || !aligned4(rows) || !aligned4(offsets)) return MOE_ERR_INVALID_ARG;
+    if (!ws || ws_bytes < moe_fp8_matmul_workspace_bytes() || !aligned16(ws)) return MOE_ERR_WORKSPACE;
+    return cuda_status(launch_fp8(x8, x_scale, X, rows, M, offsets, G, w, w_scale, N, K, y, ydtype, (unsigned *)ws,
+                                  stream));
 }
 
 moe_status moe_read_device_status(void *ws, int clear, uint32_t *flags, cudaStream_t stream) {

@@ -1,0 +1,285 @@
+"""moe_expert_order and moe_balance_loss against plain definitions.
+
+The order is whole numbers: equal, or wrong.  The balance loss is compared with the definition in 64 bits; its
+tolerance counts roundings (u = 2^-24): exp is off by at most 2 ulp (4 u) and its argument by u |l - m|, the sums
+of a row add at most 32 values a lane and 5 butterfly steps, so p is off by at most C u of itself and q by at
+most C u sum_e p |d| with C = max|l - m| + 64; d_e is off by 2 u of itself.
+"""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+moe = pytest.importorskip("quantized_routed_expert_router_gb300")
+
+U = 2.0 ** -24
+DEV = "cuda"
+
+
+def order_by_hand(ids, E):
+    """counts, offsets, rows, pos by walking over the pairs on the host"""
+    T, k = ids.shape
+    lists = [[] for _ in range(E)]
+    for i, e in enumerate(ids.reshape(-1).tolist()):
+        if 0 <= e < E:
+            lists[e].append(i)
+    flat = [i for one in lists for i in one]
+    pos = [-1] * (T * k)
+    for place, i in enumerate(flat):
+        pos[i] = place
+    offs = [0]
+    for one in lists:
+        offs.append(offs[-1] + len(one))
+    rows = [i // k for i in flat] + [-1] * (T * k - len(flat))
+    t = lambda v: torch.tensor(v, dtype=torch.int32)  # noqa: E731
+    return t([len(one) for one in lists]), t(offs), t(rows), t(pos).reshape(T, k)
+
+
+def order(ids, E, stream=None):
+    T, k = ids.shape
+    new = lambda *s: torch.full(s, -77, dtype=torch.int32, device=DEV)  # noqa: E731
+    counts, offsets, rows, pos = new(E), new(E + 1), new(T * k), new(T, k)
+    # any contents will do
+    ws = torch.full((max(16, moe.moe_expert_order_workspace_bytes(T, k, E)),), 0xA5, dtype=torch.uint8, device=DEV)
+    moe.moe_expert_order(ids, E, ws, counts=counts, offsets=offsets, rows=rows, pos=pos, stream=stream)
+    return counts, offsets, rows, pos
+
+
+def draw_ids(T, k, E, seed, outside=0.1, few=False):
+    g = torch.Generator().manual_seed(seed)
+    ids = torch.randint(0, max(1, E // 7) if few else E, (T, k), generator=g, dtype=torch.int32)
+    off = torch.rand(T, k, generator=g) < outside
+    ids[off] = torch.tensor([-1, E, -2 ** 31, 2 ** 31 - 1, E + 5])[torch.randint(0, 5, (int(off.sum()),), generator=g)].int()
+    return ids
+
+
+# one pair, one chunk and its edge (4096 pairs), several chunks, ragged ends; experts below, at and above
+# the number of threads of a block
+@pytest.mark.parametrize("T,k,E", [(1, 1, 1), (1, 8, 128), (3, 4, 32), (16, 8, 128), (512, 8, 256), (513, 8, 256),
+                                   (1000, 7, 97), (2000, 5, 511), (3000, 3, 512), (2100, 4, 1024), (5000, 1, 1),
+                                   (9000, 2, 513), (6, 32, 1000), (20000, 8, 300)])
+def test_order_equals_the_walk(T, k, E):
+    for seed, few in ((1, False), (2, True)):
+        ids = draw_ids(T, k, E, seed + T + E, few=few)
+        for name, got, want in zip(("counts", "offsets", "rows", "pos"), order(ids.to(DEV), E), order_by_hand(ids, E)):
+            assert torch.equal(got.cpu(), want), name
+
+
+def test_order_with_nothing_one_expert_and_no_tokens():
+    ids = torch.full((700, 8), -1, dtype=torch.int32, device=DEV)
+    counts, offsets, rows, pos = order(ids, 64)
+    assert int(counts.sum()) == 0 and int(offsets.abs().sum()) == 0
+    assert bool((rows == -1).all()) and bool((pos == -1).all())
+    counts, offsets, rows, pos = order(torch.full((700, 8), 63, dtype=torch.int32, device=DEV), 64)
+    assert counts.tolist() == [0] * 63 + [5600] and torch.equal(pos.reshape(-1).cpu(), torch.arange(5600).int())
+    counts, offsets, rows, pos = order(torch.empty(0, 8, dtype=torch.int32, device=DEV), 64)
+    assert counts.tolist() == [0] * 64 and offsets.tolist() == [0] * 65
+
+
+def test_order_outputs_may_be_left_out_and_captured():
+    ids = draw_ids(3000, 4, 100, 5).to(DEV)
+    want = order(ids, 100)
+    names = ("counts", "offsets", "rows", "pos")
+    ws = torch.empty(moe.moe_expert_order_workspace_bytes(3000, 4, 100), dtype=torch.uint8, device=DEV)
+    for name, w in zip(names, want):
+        out = torch.full_like(w, -9)
+        moe.moe_expert_order(ids, 100, ws, **{name: out})
+        assert torch.equal(out, w), name
+    out = {n: torch.full_like(w, -9) for n, w in zip(names, want)}
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        moe.moe_expert_order(ids, 100, ws, **out)
+    ids.copy_(draw_ids(3000, 4, 100, 6).to(DEV))
+    want = order(ids, 100)
+    g.replay()
+    for name, w in zip(names, want):
+        assert torch.equal(out[name], w), name
+    # one chunk needs no workspace
+    few, c = ids[:10].contiguous(), torch.empty(100, dtype=torch.int32, device=DEV)
+    moe.moe_expert_order(few, 100, counts=c)
+    assert torch.equal(c, order(few, 100)[0])
+
+
+# --------------------------------------------------------------- balance
+
+def definition(logits, counts, k, gating, alpha, valid=None):
+    """loss, gradient and the pieces of the tolerance, in 64 bits"""
+    l = logits.double()
+    live = torch.ones(l.shape[0], dtype=torch.bool, device=l.device) if valid is None else valid.bool()
+    live = live & (l > -float("inf")).any(1)
+    l = torch.where(live[:, None], l, torch.zeros_like(l))
+    if gating == moe.SOFTMAX:
+        p = torch.softmax(l, 1)
+        far = l.amax(1, keepdim=True) - l
+        slope = torch.ones_like(p)
+    else:
+        p = torch.softmax(torch.nn.functional.logsigmoid(l), 1)
+        far = (l.amax(1, keepdim=True).clamp(max=0) - l).clamp(min=0)
+        slope = torch.sigmoid(-l)
+    c, E = counts.double(), l.shape[1]
+    N = c.sum()
+    if float(N) == 0:
+        z = torch.zeros_like(l)
+        return 0.0, z, z, 0.0
+    d = (c * E - N) / N
+    coef = alpha * k / N
+    q = (p * d).sum(1, keepdim=True)
+    C = torch.where(p > 1e-45, far, torch.zeros_like(far)).amax(1, keepdim=True) + 64    # of those that count
+    spread = (p * d.abs()).sum(1, keepdim=True)
+    grad = coef * p * slope * (d - q) * live[:, None]
+    # p's, the slope's and the products' error, q's, d's
+    tol = coef * p * slope * ((d - q).abs() * (2 * C + 12) * U + spread * 2 * C * U + d.abs() * 2 * U) * live[:, None]
+    loss = float((coef * (1 + q) * live[:, None]).sum())
+    loss_tol = float((coef * spread * 2 * C * U * live[:, None]).sum()) + 6 * U * abs(loss)
+    return loss, grad, tol, loss_tol
+
+
+def case(T, E, k, seed, spread=1.0):
+    g = torch.Generator().manual_seed(seed)
+    logits = torch.randn(T, E, generator=g) * spread + 0.5 * torch.randn(E, generator=g)
+    ids = torch.topk(logits, k, 1).indices
+    counts = torch.bincount(ids.reshape(-1), minlength=E).int()
+    return logits.to(DEV), counts.to(DEV)
+
+
+def balance(logits, counts, k, gating, alpha=0.01, ws=None, **kw):
+    T, E = logits.shape
+    ws = torch.zeros(moe.moe_balance_loss_workspace_bytes(T, E), dtype=torch.uint8, device=DEV) if ws is None else ws
+    loss, d = torch.full((1,), 7.0, device=DEV), torch.full_like(logits, 7.0)
+    moe.moe_balance_loss(logits, counts, k, gating, alpha, ws, loss=loss, dlogits=d, **kw)
+    return loss, d
+
+
+def check(loss, d, want, scale=1.0):
+    l64, g64, tol, loss_tol = want
+    assert abs(float(loss) - l64) <= loss_tol, (float(loss), l64, loss_tol)
+    if d.dtype == torch.bfloat16:
+        tol = tol + g64.abs() * 2.0 ** -8 * 1.01
+    err = (d.double() - scale * g64).abs() - scale * tol * 1.01 - 1e-38
+    assert bool((err <= 0).all()), float(err.max())
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 128, 8), (5, 7, 3), (100, 32, 4), (333, 97, 5), (64, 256, 8), (2000, 257, 6),
+                                   (77, 512, 8), (50, 513, 2), (40, 1000, 32), (12, 1023, 8), (9000, 64, 6)])
+@pytest.mark.parametrize("gating", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_balance_against_the_definition(T, E, k, gating, dtype):
+    G = moe.SOFTMAX if gating == "softmax" else moe.SIGMOID
+    logits, counts = case(T, E, k, T + E)
+    logits = logits.to(dtype)
+    check(*balance(logits, counts, k, G), definition(logits, counts, k, G, 0.01))
+
+
+@pytest.mark.parametrize("gating", ["softmax", "sigmoid"])
+def test_balance_gradient_by_differences(gating):
+    """central differences of the definition's loss; h = 1e-4: h^2 |f'''| and 1e-16 / h both stay below 1e-7 of it"""
+    G = moe.SOFTMAX if gating == "softmax" else moe.SIGMOID
+    logits, counts = case(6, 12, 3, 4)
+    _, d = balance(logits, counts, 3, G, alpha=1.0)
+    for t, e in ((0, 0), (2, 5), (5, 11), (3, 7)):
+        h = torch.zeros(6, 12, dtype=torch.float64, device=DEV)
+        h[t, e] = 1e-4
+        up = definition(logits.double() + h, counts, 3, G, 1.0)[0]
+        down = definition(logits.double() - h, counts, 3, G, 1.0)[0]
+        slope = (up - down) / 2e-4
+        assert abs(float(d[t, e]) - slope) <= 1e-5 * float(d.abs().max())
+
+
+@pytest.mark.parametrize("gating", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [96, 97])
+def test_balance_masks(gating, E):
+    """padded tokens hold NaN, experts are shut with -inf and the type's lowest value, one row shuts all"""
+    G = moe.SOFTMAX if gating == "softmax" else moe.SIGMOID
+    T, k = 60, 4
+    logits, counts = case(T, E, k, 8)
+    logits[3, 10:40] = -float("inf")
+    logits[4, 1:] = -float("inf")
+    logits[5] = -float("inf")
+    logits[6] = torch.finfo(torch.float32).min
+    logits[7, :50] = torch.finfo(torch.float32).min
+    logits[8] = -300.0                     # sigma(-300) is 0 in fp32, its share is not
+    logits[9] = torch.linspace(-200, -150, E)
+    logits[10] = 80.0
+    valid = torch.ones(T, dtype=torch.uint8, device=DEV)
+    valid[50:] = 0
+    logits[50:55] = float("nan")
+    logits[55:] = float("inf")
+    clean = torch.where(torch.isfinite(logits) | (logits == -float("inf")), logits, torch.zeros_like(logits))
+    loss, d = balance(logits, counts, k, G, valid=valid)
+    want = definition(clean, counts, k, G, 0.01, valid)
+    assert bool((d[50:] == 0).all()) and bool((d[5] == 0).all())
+    assert bool((d[3, 10:40] == 0).all()) and bool(torch.isfinite(d).all())
+    check(loss, d, want)
+    # a bool mask is the same
+    loss2, d2 = balance(logits, counts, k, G, valid=valid.bool())
+    assert torch.equal(loss, loss2) and torch.equal(d, d2)
+
+
+def test_balance_scale_parts_in_place_and_repeat():
+    logits, counts = case(500, 64, 6, 3)
+    ws = torch.zeros(moe.moe_balance_loss_workspace_bytes(500, 64), dtype=torch.uint8, device=DEV)
+    loss, d = balance(logits, counts, 6, moe.SOFTMAX, ws=ws)
+    for _ in range(3):                                          # the workspace is ready again
+        l2, d2 = balance(logits, counts, 6, moe.SOFTMAX, ws=ws)
+        assert torch.equal(loss, l2) and torch.equal(d, d2)
+    check(*balance(logits, counts, 6, moe.SOFTMAX, ws=ws, grad_loss=torch.tensor([3.0], device=DEV)),
+          definition(logits, counts, 6, moe.SOFTMAX, 0.01), scale=3.0)
+    only = torch.empty(1, device=DEV)
+    moe.moe_balance_loss(logits, counts, 6, moe.SOFTMAX, 0.01, ws, loss=only)
+    assert torch.equal(only, loss)
+    x = logits.clone()
+    moe.moe_balance_loss(x, counts, 6, moe.SOFTMAX, 0.01, ws, dlogits=x)      # over the logits
+    assert torch.equal(x, d)
+    # even counts give alpha
+    l3, d3 = balance(torch.zeros(640, 64, device=DEV), torch.full((64,), 60, dtype=torch.int32, device=DEV), 6,
+                     moe.SOFTMAX)
+    assert abs(float(l3) - 0.01) <= 0.01 * 8 * U and bool((d3 == 0).all())
+
+
+def test_balance_without_counts_or_tokens():
+    logits, _ = case(20, 30, 2, 1)
+    zero = torch.zeros(30, dtype=torch.int32, device=DEV)
+    loss, d = balance(logits, zero, 2, moe.SOFTMAX)
+    assert float(loss) == 0.0 and bool((d == 0).all())
+    loss, _ = balance(logits[:0], zero, 2, moe.SOFTMAX)
+    assert float(loss) == 0.0
+
+
+def test_balance_captured():
+    logits, counts = case(300, 48, 4, 2)
+    ws = torch.zeros(moe.moe_balance_loss_workspace_bytes(300, 48), dtype=torch.uint8, device=DEV)
+    loss, d = torch.empty(1, device=DEV), torch.empty_like(logits)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        moe.moe_balance_loss(logits, counts, 4, moe.SIGMOID, 0.02, ws, loss=loss, dlogits=d)
+    logits.copy_(case(300, 48, 4, 9)[0])
+    for _ in range(2):
+        loss.zero_()
+        g.replay()
+        check(loss, d, definition(logits, counts, 4, moe.SIGMOID, 0.02))
+
+
+def test_refusals():
+    logits, counts = case(20, 30, 2, 1)
+    ws = torch.zeros(moe.moe_balance_loss_workspace_bytes(20, 30), dtype=torch.uint8, device=DEV)
+    loss = torch.full((1,), 7.0, device=DEV)
+    for kw in (dict(ws=ws[:-1]), dict(ws=None), dict(k=31), dict(k=0), dict(gating=2), dict(loss=None)):
+        a = dict(k=2, gating=moe.SOFTMAX, alpha=0.01, ws=ws, loss=loss)
+        a.update(kw)
+        with pytest.raises(moe.MoeError):
+            moe.moe_balance_loss(logits, counts, **a)
+    for kw in (dict(logits=logits.half()), dict(logits=logits.t()), dict(counts=counts.long()), dict(counts=counts[:5]),
+               dict(valid=torch.ones(3, dtype=torch.uint8, device=DEV)), dict(dlogits=logits.bfloat16())):
+        a = dict(logits=logits, counts=counts, k=2, gating=0, alpha=0.01, ws=ws, loss=loss)
+        a.update(kw)
+        with pytest.raises(ValueError):
+            moe.moe_balance_loss(**a)
+    ids = torch.zeros(3000, 4, dtype=torch.int32, device=DEV)
+    c = torch.full((8,), 7, dtype=torch.int32, device=DEV)
+    with pytest.raises(moe.MoeError):
+        moe.moe_expert_order(ids, 8, None, counts=c)              # several chunks need the workspace
+    with pytest.raises(moe.MoeError):
+        moe.moe_expert_order(ids, 8, torch.zeros(1 << 16, dtype=torch.uint8, device=DEV))
+    with pytest.raises(ValueError):
+        moe.moe_expert_order(ids.long(), 8, None, counts=c)
+    assert float(loss) == 7.0 and bool((c == 7).all())
