@@ -270,39 +270,44 @@ _DT = {torch.float32: DT_F32, torch.bfloat16: DT_BF16}
 _E4M3 = (torch.float8_e4m3fn, torch.uint8)
 
 
-def _expect(name: str, t, like, shape, dtypes):
-    """t is a contiguous CUDA tensor of this shape and one of these types, where `like` is; None passes."""
-    if t is None:
-        return
-    if t.shape != shape or t.dtype not in dtypes or not t.is_contiguous() or t.device != like.device:
-        raise ValueError(f"{name}: want a contiguous {' or '.join(map(str, dtypes))} tensor {tuple(shape)} on "
-                         f"{like.device}, got {t.dtype} {tuple(t.shape)} on {t.device}"
-                         f"{'' if t.is_contiguous() else ', not contiguous'}")
+def _expect(name, t, shape, dtypes, dev):
+    """t is a contiguous tensor of this shape and one of these types on device `dev`; None passes."""
+    if t is not None and (t.dtype not in dtypes or t.shape != shape or not t.is_contiguous() or t.get_device() != dev):
+        raise ValueError(f"{name}: want a contiguous {' or '.join(map(str, dtypes))} tensor {tuple(shape)} on device "
+                         f"{dev}, got {t.dtype} {tuple(t.shape)}{'' if t.is_contiguous() else ', not contiguous,'} on "
+                         f"device {t.get_device()}")
 
 
-def _ws(ws, like):
+def _ws(ws, dev):
     """(address, bytes) of a workspace; it lies where the inputs lie"""
     if ws is None:
         return None, 0
-    if ws.device != like.device or not ws.is_contiguous():
-        raise ValueError(f"ws: want a contiguous tensor on {like.device}")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"ws: want a contiguous tensor on device {dev}")
+    return ws.data_ptr(), ws.nbytes
 
 
-def _launch(call: str, fn, like, args, stream):
-    """fn(*args, stream) with the tensors' device current"""
-    if not like.is_cuda:
+def _launch(call: str, dev: int, args, stream):
+    """the library's `call` with the tensors' device current, on its current stream unless one is given"""
+    if dev < 0:
         raise ValueError(f"{call}: tensors must be on a CUDA device")
-    index = like.device.index
     if stream is None:
-        stream = torch.cuda.current_stream(index)
-    elif stream.device_index != index:
+        handle = torch._C._cuda_getCurrentRawStream(dev)   # current_stream(dev).cuda_stream without the object
+    elif stream.device_index != dev:
         raise ValueError(f"{call}: the stream belongs to another device than the tensors")
-    if index == torch.cuda.current_device():
-        _check(fn(*args, stream.cuda_stream), call)
     else:
-        with torch.cuda.device(index):
-            _check(fn(*args, stream.cuda_stream), call)
+        handle = stream.cuda_stream
+    fn = getattr(_lib_handle or lib(), call)
+    if dev == torch.cuda.current_device():
+        s = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            s = fn(*args, handle)
+    if s:
+        raise MoeError(s, call)
+
+
+_F32, _I32, _F32_BF16 = (torch.float32,), (torch.int32,), (torch.float32, torch.bfloat16)
 
 
 def moe_add_rmsnorm(x, residual, weight, eps: float, residual_out=None, y=None, xq=None, x8=None, x8_scale=None,
@@ -314,18 +319,19 @@ def moe_add_rmsnorm(x, residual, weight, eps: float, residual_out=None, y=None, 
     scales [T, ceil(n / 128)].  Give the outputs that are wanted."""
     if x.dim() != 2 or x.dtype not in _DT or not x.is_contiguous():
         raise ValueError("x: want a contiguous fp32 or bf16 tensor [T, n]")
-    T, n = x.shape
-    shape = x.shape
-    _expect("residual", residual, x, shape, (x.dtype,))
-    _expect("weight", weight, x, (n,), (torch.float32,))
-    _expect("residual_out", residual_out, x, shape, (x.dtype,))
-    _expect("y", y, x, shape, (torch.float32, torch.bfloat16))
-    _expect("x8", x8, x, shape, _E4M3)
-    _expect("x8_scale", x8_scale, x, (T, -(-n // FP8_GROUP)), (torch.float32,))
-    if xq is not None and (xq.device != x.device or not xq.is_contiguous() or
-                           xq.numel() * xq.element_size() < T * moe_q8_row_bytes(n)):
-        raise ValueError(f"xq: want at least {T} x {moe_q8_row_bytes(n)} contiguous bytes on {x.device}")
-    _launch("moe_add_rmsnorm", lib().moe_add_rmsnorm, x,
+    shape, dev = x.shape, x.get_device()
+    T, n = shape
+    same = (x.dtype,)
+    _expect("residual", residual, shape, same, dev)
+    _expect("weight", weight, (n,), _F32, dev)
+    _expect("residual_out", residual_out, shape, same, dev)
+    _expect("y", y, shape, _F32_BF16, dev)
+    _expect("x8", x8, shape, _E4M3, dev)
+    _expect("x8_scale", x8_scale, (T, -(-n // FP8_GROUP)), _F32, dev)
+    if xq is not None and (xq.get_device() != dev or not xq.is_contiguous() or
+                           xq.nbytes < T * moe_q8_row_bytes(n)):
+        raise ValueError(f"xq: want at least {T} x {moe_q8_row_bytes(n)} contiguous bytes on device {dev}")
+    _launch("moe_add_rmsnorm", dev,
             (x.data_ptr(), _ptr(residual), _ptr(weight), eps, T, n, _DT[x.dtype], _ptr(residual_out), _ptr(y),
              DT_F32 if y is None else _DT[y.dtype], _ptr(xq), _ptr(x8), _ptr(x8_scale)), stream)
 
@@ -340,14 +346,14 @@ def moe_expert_order(ids, E: int, ws=None, counts=None, offsets=None, rows=None,
     part, its id is not in [0, E)).  All int32; give the outputs that are wanted."""
     if ids.dim() != 2 or ids.dtype != torch.int32 or not ids.is_contiguous():
         raise ValueError("ids: want a contiguous int32 tensor [T, k]")
-    T, k = ids.shape
-    i32 = (torch.int32,)
-    _expect("counts", counts, ids, (E,), i32)
-    _expect("offsets", offsets, ids, (E + 1,), i32)
-    _expect("rows", rows, ids, (T * k,), i32)
-    _expect("pos", pos, ids, ids.shape, i32)
-    _launch("moe_expert_order", lib().moe_expert_order, ids,
-            (ids.data_ptr(), T, k, E, _ptr(counts), _ptr(offsets), _ptr(rows), _ptr(pos), *_ws(ws, ids)), stream)
+    shape, dev = ids.shape, ids.get_device()
+    T, k = shape
+    _expect("counts", counts, (E,), _I32, dev)
+    _expect("offsets", offsets, (E + 1,), _I32, dev)
+    _expect("rows", rows, (T * k,), _I32, dev)
+    _expect("pos", pos, shape, _I32, dev)
+    _launch("moe_expert_order", dev,
+            (ids.data_ptr(), T, k, E, _ptr(counts), _ptr(offsets), _ptr(rows), _ptr(pos), *_ws(ws, dev)), stream)
 
 
 def moe_balance_loss_workspace_bytes(T: int, E: int) -> int:
@@ -361,16 +367,16 @@ def moe_balance_loss(logits, counts, k: int, gating: int, alpha: float, ws, loss
     None.  valid: uint8 or bool [T], 0 for padded tokens."""
     if logits.dim() != 2 or logits.dtype not in _DT or not logits.is_contiguous():
         raise ValueError("logits: want a contiguous fp32 or bf16 tensor [T, E]")
-    T, E = logits.shape
-    f32 = (torch.float32,)
-    _expect("counts", counts, logits, (E,), (torch.int32,))
-    _expect("valid", valid, logits, (T,), (torch.uint8, torch.bool))
-    _expect("grad_loss", grad_loss, logits, (1,), f32)
-    _expect("loss", loss, logits, (1,), f32)
-    _expect("dlogits", dlogits, logits, logits.shape, (logits.dtype,))
-    _launch("moe_balance_loss", lib().moe_balance_loss, logits,
+    shape, dev = logits.shape, logits.get_device()
+    T, E = shape
+    _expect("counts", counts, (E,), _I32, dev)
+    _expect("valid", valid, (T,), (torch.uint8, torch.bool), dev)
+    _expect("grad_loss", grad_loss, (1,), _F32, dev)
+    _expect("loss", loss, (1,), _F32, dev)
+    _expect("dlogits", dlogits, shape, (logits.dtype,), dev)
+    _launch("moe_balance_loss", dev,
             (logits.data_ptr(), _DT[logits.dtype], _ptr(counts), _ptr(valid), T, E, k, gating, alpha, _ptr(grad_loss),
-             _ptr(loss), _ptr(dlogits), *_ws(ws, logits)), stream)
+             _ptr(loss), _ptr(dlogits), *_ws(ws, dev)), stream)
 
 
 def moe_fp8_matmul_workspace_bytes() -> int:
@@ -387,21 +393,19 @@ def moe_fp8_matmul(x8, x_scale, w, w_scale, y, ws, offsets=None, rows=None, stre
         raise ValueError("x8: want a contiguous e4m3 tensor [X, K]")
     if w.dim() not in (2, 3) or y.dim() != 2:
         raise ValueError("w: want [N, K] or [G, N, K]; y: [M, N]")
-    X, K = x8.shape
-    N, M = w.shape[-2], y.shape[0]
-    kb, nb = -(-K // FP8_GROUP), -(-N // FP8_GROUP)
-    G = w.shape[0] if w.dim() == 3 else 1
+    (X, K), dev = x8.shape, x8.get_device()
     lead = w.shape[:-2]
-    f32 = (torch.float32,)
-    _expect("x_scale", x_scale, x8, (X, kb), f32)
-    _expect("w", w, x8, (*lead, N, K), _E4M3)
-    _expect("w_scale", w_scale, x8, (*lead, nb, kb), f32)
-    _expect("y", y, x8, (M, N), (torch.float32, torch.bfloat16))
-    _expect("offsets", offsets, x8, (G + 1,), (torch.int32,))
-    _expect("rows", rows, x8, (M,), (torch.int32,))
-    _launch("moe_fp8_matmul", lib().moe_fp8_matmul, x8,
-            (x8.data_ptr(), x_scale.data_ptr(), X, _ptr(rows), M, _ptr(offsets), G, w.data_ptr(), w_scale.data_ptr(),
-             N, K, y.data_ptr(), _DT[y.dtype], *_ws(ws, x8)), stream)
+    N, M, G = w.shape[-2], y.shape[0], lead[0] if lead else 1
+    kb, nb = -(-K // FP8_GROUP), -(-N // FP8_GROUP)
+    _expect("x_scale", x_scale, (X, kb), _F32, dev)
+    _expect("w", w, (*lead, N, K), _E4M3, dev)
+    _expect("w_scale", w_scale, (*lead, nb, kb), _F32, dev)
+    _expect("y", y, (M, N), _F32_BF16, dev)
+    _expect("offsets", offsets, (G + 1,), _I32, dev)
+    _expect("rows", rows, (M,), _I32, dev)
+    _launch("moe_fp8_matmul", dev,
+            (x8.data_ptr(), _ptr(x_scale), X, _ptr(rows), M, _ptr(offsets), G, w.data_ptr(), _ptr(w_scale),
+             N, K, y.data_ptr(), _DT[y.dtype], *_ws(ws, dev)), stream)
 
 
 def moe_debug_set_exchange_wait(cycles: int):

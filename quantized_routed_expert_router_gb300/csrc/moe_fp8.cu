@@ -7,17 +7,17 @@
 // D_b is one 128-deep product on the tensor cores (four tcgen05.mma of depth
 // 32, accumulated in TMEM in fp32); the scales change from block to block, so
 // every D_b is read back and added to fp32 registers with its scale.  The
-// roles of a block of 320 threads work on different blocks b at once:
-//   warp 0     : TMA copies of x and w tiles (128 bytes deep, 128-byte swizzle)
-//                into a ring of stages; gathered rows by tile::gather4, four
-//                rows an instruction, one lane each
-//   warp 1     : one thread issues the products into one of two TMEM buffers
-//   warps 2..9 : acc += (sx * sw) * D_b.  TMEM gives lane i of the tile to
-//                thread i, so sx is one number a thread and sw one number a
-//                warp: the scaling is one (packed) multiply-add a value
+// warps of a block have roles that work on different blocks b at once:
+//   warp 0    : TMA copies of w tiles, and of x tiles where the rows are in
+//               order (128 bytes deep, 128-byte swizzle), into a ring of stages
+//   warp 1    : one thread issues the products into one of two TMEM buffers
+//   warps 2-3 : rows that are gathered, by 16-byte asynchronous copies
+//   warps 4.. : acc += (sx * sw) * D_b, 64 columns a warp.  TMEM gives lane i of
+//               the tile to thread i, so sx is one number a thread and sw one a
+//               warp: the scaling is one (packed) multiply-add a value
 // A tile is 128 places of one group by BN columns.  Blocks beyond the ends of
-// x, w or K are zero-filled by TMA; rows of other groups that a tile happens to
-// load only reach accumulators that are not stored.
+// x, w or K are zero-filled; rows of other groups that a tile happens to load
+// only reach accumulators that are not stored.
 //
 // Large products are persistent blocks, one an SM, over the tiles (BN 256).
 // When there are fewer tiles than SMs, a cluster of S blocks splits the depth of
@@ -33,8 +33,9 @@ namespace {
 
 constexpr int BM = 128;             // places of a tile (TMEM lanes)
 constexpr int BK = 128;             // bytes of depth of a stage (one scale block)
-constexpr int THREADS = 320;
-constexpr int EPI_WARPS = 8;
+constexpr int EPI_FIRST = 4;        // first accumulating warp
+constexpr int HC = 64;              // columns of an accumulating warp
+constexpr int GATHER_LAG = 2;       // stages of gathered rows in flight before one is handed over
 constexpr int NBUF = 2;             // TMEM buffers
 constexpr int RED_PITCH = BM + 1;   // fp32 partial tiles, column by column
 // bound on every device-side wait, in SM clock cycles (under a second)
@@ -45,14 +46,16 @@ struct Shape {
     static constexpr int STAGES = BN == 256 ? 4 : 6;
     static constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE = A_BYTES + B_BYTES;
     static constexpr int SMEM = STAGES * STAGE + 1024;   // + alignment of the swizzle pattern
+    static constexpr int EPI_WARPS = 4 * (BN / HC), THREADS = 32 * (EPI_FIRST + EPI_WARPS);
 };
 
 struct Fp8Args {
+    const uint8_t *x;
     const float *xs, *ws;
     const int32_t *rows, *offsets;
     void *y;
     unsigned *status;
-    int X, M, G, N, KB, NB, ntn;
+    int X, M, G, N, K, KB, NB, ntn;
     int xbox;      // rows of an x copy (ungathered)
 };
 
@@ -82,6 +85,14 @@ __device__ __forceinline__ bool bar_test(uint64_t *b, uint32_t parity) {
         "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
         : "=r"(ok) : "r"(sa(b)), "r"(parity) : "memory");
     return ok != 0;
+}
+// one lane of a converged warp.  The single-thread instructions (copies, products,
+// commits) sit behind this inside loops that the whole warp runs: behind a
+// test of the lane number one stage's four products took 540-800 cycles to issue.
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p != 0;
 }
 // wait for a phase; false once this block has given up (the first wait to run
 // out says so to the others and in the status word)
@@ -113,12 +124,9 @@ __device__ __forceinline__ void tma_tile(void *dst, const CUtensorMap *m, int x,
             sa(dst)), "l"(m), "r"(x), "r"(y), "r"(sa(bar))
         : "memory");
 }
-__device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *m, int x, const int r[4], uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], "
-        "[%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(sa(dst)), "l"(m), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]),
-        "r"(r[3]), "r"(sa(bar))
-        : "memory");
+// 16 bytes, or 16 zeros where `bytes` is 0
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 // shared-memory descriptor of a K-major tile with 128-byte rows and the
 // 128-byte swizzle: 8-row groups 1024 bytes apart
@@ -143,7 +151,13 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t v[16]) {
           "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
         : "r"(addr));
 }
-__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// waits for this thread's loads; the values pass through it, so that none is used before it
+__device__ __forceinline__ void tmem_ld_wait(uint32_t v[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+                 ::"memory");
+}
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 // acc (two fp32) += {lo, hi} * {s, s}
@@ -243,10 +257,10 @@ __device__ __forceinline__ void store_cols<__nv_bfloat16>(__nv_bfloat16 *y, cons
 }
 
 template <int BN, typename TY, bool SPLIT>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
     fp8_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw, const Fp8Args a) {
     using S = Shape<BN>;
-    constexpr int HC = BN / 2;   // columns of an accumulating warp
+    constexpr int THREADS = S::THREADS;
     extern __shared__ uint8_t raw[];
     __shared__ Ctl c;
     uint8_t *stages = raw + ((1024 - (sa(raw) & 1023)) & 1023);
@@ -254,12 +268,12 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::STAGES; ++i) {
-            bar_init(&c.full[i], 1);
+            bar_init(&c.full[i], a.rows ? 3 : 1);   // the w copy, and the two gathering warps
             bar_init(&c.empty[i], 1);
         }
         for (int i = 0; i < NBUF; ++i) {
             bar_init(&c.dfull[i], 1);
-            bar_init(&c.dempty[i], EPI_WARPS);
+            bar_init(&c.dempty[i], S::EPI_WARPS);
         }
         bar_init(&c.drain, 1);
         c.abort = 0;
@@ -283,7 +297,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             c.goff[g] = min(max(o, 0), a.M);
         }
         __syncthreads();
-        if (warp == 2) {
+        if (warp == EPI_FIRST) {
             // a group ends where the next one begins, never before its own start
             int sum = 0;
             for (int g0 = 0; g0 < a.G; g0 += 32) {
@@ -311,75 +325,111 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int kb0 = SPLIT ? rank * a.KB / parts : 0, kb1 = SPLIT ? (rank + 1) * a.KB / parts : a.KB;
 
     if (warp == 0) {
+        const uint32_t bytes = (a.rows ? 0 : a.xbox) * BK + S::B_BYTES;
         int it = 0;
         bool ok = true;
         for (int t = t0; t < total && ok; t += dt) {
             const Tile tl = tile_at(&c, a, t, BN);
-            int r[4] = {0, 0, 0, 0};
-            const int quads = a.rows ? (tl.rows + 3) >> 2 : 0;
-            if (lane < quads) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = a.rows[tl.first + min(4 * lane + i, tl.rows - 1)];
-                    r[i] = (unsigned)row < (unsigned)a.X ? row : 0;
-                }
-            }
-            const uint32_t bytes = (a.rows ? quads * 4 : a.xbox) * BK + S::B_BYTES;
+            const int wrow = __shfl_sync(0xFFFFFFFFu, tl.g * a.N + tl.n0, 0);
+            const int xrow = __shfl_sync(0xFFFFFFFFu, tl.first, 0);
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int st = it % S::STAGES;
                 ok = bar_wait(&c.empty[st], ((it / S::STAGES) & 1) ^ 1, &c, a.status);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 uint8_t *sx = stages + st * S::STAGE;
-                if (lane == 0) {
+                if (elect()) {
                     bar_expect(&c.full[st], bytes);
-                    tma_tile(sx + S::A_BYTES, &mw, kb * BK, tl.g * a.N + tl.n0, &c.full[st]);
-                    if (!a.rows) tma_tile(sx, &mx, kb * BK, tl.first, &c.full[st]);
+                    tma_tile(sx + S::A_BYTES, &mw, kb * BK, wrow, &c.full[st]);
+                    if (!a.rows) tma_tile(sx, &mx, kb * BK, xrow, &c.full[st]);
                 }
                 __syncwarp();
-                if (lane < quads) tma_gather4(sx + lane * 4 * BK, &mx, kb * BK, r, &c.full[st]);
             }
         }
         // copies in flight land, and their stages are handed back, before the block ends
-        if (lane == 0)
-            for (int i = it > S::STAGES ? it - S::STAGES : 0; i < it; ++i)
-                bar_settle(ok ? &c.empty[i % S::STAGES] : &c.full[i % S::STAGES], (i / S::STAGES) & 1);
+        for (int i = it > S::STAGES ? it - S::STAGES : 0; i < it; ++i)
+            bar_settle(ok ? &c.empty[i % S::STAGES] : &c.full[i % S::STAGES], (i / S::STAGES) & 1);
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
-            int it = 0;
-            bool ok = true;
-            for (int t = t0; t < total && ok; t += dt) {
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const int st = it % S::STAGES, buf = it % NBUF;
-                    ok = bar_wait(&c.dempty[buf], ((it / NBUF) & 1) ^ 1, &c, a.status) &&
-                         bar_wait(&c.full[st], (it / S::STAGES) & 1, &c, a.status);
-                    if (!ok) break;
-                    fence_after();
-                    const uint32_t sx = sa(stages + st * S::STAGE);
-                    const uint64_t ad = tile_desc(sx), bd = tile_desc(sx + S::A_BYTES);
+        constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+        int it = 0;
+        bool ok = true;
+        for (int t = t0; t < total && ok; t += dt) {
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const int st = it % S::STAGES, buf = it % NBUF;
+                ok = bar_wait(&c.dempty[buf], ((it / NBUF) & 1) ^ 1, &c, a.status) &&
+                     bar_wait(&c.full[st], (it / S::STAGES) & 1, &c, a.status);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                fence_after();
+                const uint32_t sx = sa(stages) + st * S::STAGE;
+                const uint64_t ad = tile_desc(sx), bd = tile_desc(sx + S::A_BYTES);
+                if (elect()) {
 #pragma unroll
                     for (int k = 0; k < BK / 32; ++k)   // 32 bytes of depth: 2 units of 16 bytes
                         mma_e4m3(tmem + buf * BN, ad + 2 * k, bd + 2 * k, idesc, k);
                     mma_commit(&c.empty[st]);
                     mma_commit(&c.dfull[buf]);
                 }
-            }
-            if (!ok) {   // products in flight end before TMEM is freed
-                mma_commit(&c.drain);
-                bar_settle(&c.drain, 0);
+                __syncwarp();
             }
         }
+        if (!ok) {   // products in flight end before TMEM is freed
+            if (elect()) mma_commit(&c.drain);
+            __syncwarp();
+            bar_settle(&c.drain, 0);
+        }
         __syncwarp();
+    } else if (warp < EPI_FIRST) {
+        if (a.rows) {
+            // thread: 16 bytes (piece pc) of rows r0, r0 + 8, ...; the swizzle moves piece p of row r to p ^ (r & 7)
+            const int id = threadIdx.x - 64, pc = id & 7, r0 = id >> 3;
+            const uint32_t to = sa(stages) + r0 * BK + ((pc ^ r0) << 4);
+            int it = 0;
+            bool ok = true;
+            for (int t = t0; t < total && ok; t += dt) {
+                const Tile tl = tile_at(&c, a, t, BN);
+                int row[BM / 8];
+#pragma unroll
+                for (int i = 0; i < BM / 8; ++i) {
+                    const int r = r0 + 8 * i < tl.rows ? a.rows[tl.first + r0 + 8 * i] : 0;
+                    row[i] = (unsigned)r < (unsigned)a.X ? r : 0;
+                }
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    const int st = it % S::STAGES;
+                    ok = bar_wait(&c.empty[st], ((it / S::STAGES) & 1) ^ 1, &c, a.status);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    const int at = kb * BK + 16 * pc;
+                    const uint32_t bytes = at < a.K ? 16 : 0;
+                    const uint8_t *src = a.x + (bytes ? at : 0);
+#pragma unroll
+                    for (int i = 0; i < BM / 8; ++i)
+                        if (r0 + 8 * i < tl.rows)
+                            copy16(to + st * S::STAGE + i * 8 * BK, src + (size_t)row[i] * a.K, bytes);
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                    if (it >= GATHER_LAG) {
+                        asm volatile("cp.async.wait_group %0;" ::"n"(GATHER_LAG) : "memory");
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(&c.full[(it - GATHER_LAG) % S::STAGES]);
+                    }
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0)
+                for (int i = it > GATHER_LAG ? it - GATHER_LAG : 0; i < it; ++i) bar_arrive(&c.full[i % S::STAGES]);
+        }
     } else {
-        const int quad = warp & 3, half = (warp - 2) >> 2;   // TMEM lanes and columns of this warp
+        const int quad = warp & 3, part = (warp - EPI_FIRST) >> 2;   // TMEM lanes and columns of this warp
         const int lrow = 32 * quad + lane;
         int it = 0;
         bool ok = true;
         for (int t = t0; t < total && ok; t += dt) {
             const Tile tl = tile_at(&c, a, t, BN);
-            const int n0 = tl.n0 + half * HC;
+            const int n0 = tl.n0 + part * HC;
             const bool mine = lrow < tl.rows;
             const bool work = 32 * quad < tl.rows && n0 < a.N;   // uniform over the warp
             int row = mine ? tl.first + lrow : 0;
@@ -416,17 +466,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (work) {
                     uint64_t ss;
                     asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "r"(__float_as_uint(s)));
-                    const uint32_t at = tmem + buf * BN + half * HC + ((uint32_t)(32 * quad) << 16);
+                    const uint32_t at = tmem + buf * BN + part * HC + ((uint32_t)(32 * quad) << 16);
+                    // one load is on its way while the one before it is added
+                    uint32_t u[2][16];
+                    tmem_ld16(at, u[0]);
 #pragma unroll
-                    for (int j = 0; j < HC; j += 32) {
-                        uint32_t u[16], v[16];
-                        tmem_ld16(at + j, u);
-                        tmem_ld16(at + j + 16, v);
-                        tmem_ld_wait();
+                    for (int j = 0; j < HC / 16; ++j) {
+                        tmem_ld_wait(u[j & 1]);
+                        if (j + 1 < HC / 16) tmem_ld16(at + 16 * (j + 1), u[(j + 1) & 1]);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) fma2(acc[j / 2 + i], u[2 * i], u[2 * i + 1], ss);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) fma2(acc[j / 2 + 8 + i], v[2 * i], v[2 * i + 1], ss);
+                        for (int i = 0; i < 8; ++i) fma2(acc[8 * j + i], u[j & 1][2 * i], u[j & 1][2 * i + 1], ss);
                     }
                 }
                 fence_before();
@@ -443,8 +492,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (mine && work) {
 #pragma unroll
                     for (int i = 0; i < HC / 2; ++i) {
-                        red[(half * HC + 2 * i) * RED_PITCH + lrow] = __uint_as_float((uint32_t)acc[i]);
-                        red[(half * HC + 2 * i + 1) * RED_PITCH + lrow] = __uint_as_float((uint32_t)(acc[i] >> 32));
+                        red[(part * HC + 2 * i) * RED_PITCH + lrow] = __uint_as_float((uint32_t)acc[i]);
+                        red[(part * HC + 2 * i + 1) * RED_PITCH + lrow] = __uint_as_float((uint32_t)(acc[i] >> 32));
                     }
                 }
             } else if (mine && work) {
@@ -459,12 +508,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (SPLIT) {
         __syncwarp();
         cluster_sync();
-        if (warp >= 2 && t0 < total && !*(volatile int *)&c.abort) {
+        if (warp >= EPI_FIRST && t0 < total && !*(volatile int *)&c.abort) {
             // each block adds its share of the columns over the cluster, in rank order
             const Tile tl = tile_at(&c, a, t0, BN);
             const int C = BN / parts, c0 = rank * C;
             const uint32_t red = sa(stages);
-            for (int i = threadIdx.x - 64; i < tl.rows * C; i += EPI_WARPS * 32) {
+            for (int i = threadIdx.x - 32 * EPI_FIRST; i < tl.rows * C; i += S::EPI_WARPS * 32) {
                 const int col = c0 + i % C, r = i / C;
                 if (tl.n0 + col >= a.N) continue;
                 float v = 0.f;
@@ -517,7 +566,7 @@ cudaError_t launch_t(const CUtensorMap &mx, const CUtensorMap &mw, const Fp8Args
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(THREADS);
+    cfg.blockDim = dim3(Shape<BN>::THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
@@ -542,7 +591,7 @@ cudaError_t launch_fp8_t(Fp8Args a, const void *x8, const void *w, int K, cudaSt
     while (split < 8 && t128 * split * 2 <= sms && a.KB >= split * 4) split *= 2;
     const bool wide = split == 1 && t256 >= sms && a.M >= 64 * mt;
     CUtensorMap mx, mw;
-    a.xbox = a.rows ? 1 : a.M >= BM || a.offsets ? BM : (a.M + 7) / 8 * 8;
+    a.xbox = a.M >= BM || a.offsets ? BM : (a.M + 7) / 8 * 8;
     if (!encode_fn()) return cudaErrorSymbolNotFound;
     if (!encode(&mx, x8, (size_t)a.X, (size_t)K, a.xbox) ||
         !encode(&mw, w, (size_t)a.G * a.N, (size_t)K, wide ? 256 : 128))
@@ -559,6 +608,7 @@ cudaError_t launch_fp8(const void *x8, const float *x_scale, int X, const int32_
                        int G, const void *w, const float *w_scale, int N, int K, void *y, int ydtype,
                        unsigned *status, cudaStream_t s) {
     Fp8Args a = {};
+    a.x = static_cast<const uint8_t *>(x8);
     a.xs = x_scale;
     a.ws = w_scale;
     a.rows = rows;
@@ -569,6 +619,7 @@ cudaError_t launch_fp8(const void *x8, const float *x_scale, int X, const int32_
     a.M = M;
     a.G = G;
     a.N = N;
+    a.K = K;
     a.KB = (K + BK - 1) / BK;
     a.NB = (N + BK - 1) / BK;
     return ydtype == MOE_DT_BF16 ? launch_fp8_t<__nv_bfloat16>(a, x8, w, K, s) : launch_fp8_t<float>(a, x8, w, K, s);

@@ -19,22 +19,26 @@ namespace {
 //   order_count : chunk b's pairs per expert -> hist[b][E]
 //   order_place : place = offsets[e] + sum of hist[b' < b][e] + the chunk's
 //                 earlier runs + rank
-// One chunk needs no hist: order_place counts it itself, in one launch.
+// order_place starts while order_count still runs (its votes need only the
+// ids) and waits for it before it reads hist.  One chunk needs no hist:
+// order_place counts it itself, in one launch.
 // Few pairs: the launches and the chain of votes bound it; many: the votes
 // and the 4-byte scatter of rows.
-constexpr int kOrderWarps = 16;
+constexpr int kOrderWarps = 32;
+constexpr int kOrderThreads = 32 * kOrderWarps;
 constexpr int kOrderIters = 8;
-constexpr int kOrderChunk = kOrderWarps * 32 * kOrderIters;   // 4096; run counts fit 16 bits
+constexpr int kOrderChunk = kOrderThreads * kOrderIters;   // 8192; counts in a chunk fit 16 bits
 
-__global__ void __launch_bounds__(512) order_count(const int32_t *__restrict__ ids, int n, int E,
+__global__ void __launch_bounds__(kOrderThreads) order_count(const int32_t *__restrict__ ids, int n, int E,
                                                    int32_t *__restrict__ hist) {
     extern __shared__ int32_t cnt[];
+    asm volatile("griddepcontrol.launch_dependents;");
     for (int e = threadIdx.x; e < E; e += blockDim.x) cnt[e] = 0;
     __syncthreads();
     const int first = blockIdx.x * kOrderChunk;
 #pragma unroll
-    for (int j = 0; j < kOrderChunk / 512; ++j) {
-        const int i = first + j * 512 + threadIdx.x;
+    for (int j = 0; j < kOrderIters; ++j) {
+        const int i = first + j * kOrderThreads + threadIdx.x;
         const int id = i < n ? ids[i] : -1;
         if ((unsigned)id < (unsigned)E) atomicAdd(cnt + id, 1);
     }
@@ -42,34 +46,38 @@ __global__ void __launch_bounds__(512) order_count(const int32_t *__restrict__ i
     for (int e = threadIdx.x; e < E; e += blockDim.x) hist[(size_t)blockIdx.x * E + e] = cnt[e];
 }
 
-__global__ void __launch_bounds__(512) order_place(const int32_t *__restrict__ ids, int n, int k, int E,
-                                                   const int32_t *__restrict__ hist, int32_t *__restrict__ counts,
+__global__ void __launch_bounds__(kOrderThreads) order_place(const int32_t *__restrict__ ids, int n, int k, int E,
+                                                   const int32_t *hist, int32_t *__restrict__ counts,
                                                    int32_t *__restrict__ offsets, int32_t *__restrict__ rows,
                                                    int32_t *__restrict__ pos) {
     extern __shared__ int32_t sm[];
     int32_t *base = sm;                                          // [E] first place of this chunk's pairs
     int32_t *total = sm + E;                                     // [E] pairs of an expert in all chunks
     uint16_t *run = reinterpret_cast<uint16_t *>(sm + 2 * E);    // [kOrderWarps][E]
-    __shared__ int32_t wsum[kOrderWarps], live;
+    __shared__ int32_t wsum[kOrderWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int i = threadIdx.x; i < kOrderWarps * E; i += blockDim.x) run[i] = 0;
+    // this chunk's pairs in runs of 32 * iters, one a warp: few pairs take few votes in a row
+    const int chunk0 = blockIdx.x * kOrderChunk, have = min(n - chunk0, kOrderChunk);
+    const int iters = (have + kOrderThreads - 1) / kOrderThreads;
+    const int used = iters ? (have + 32 * iters - 1) / (32 * iters) : 0;   // warps with pairs
+    for (int i = threadIdx.x; i < used * E; i += blockDim.x) run[i] = 0;
     for (int e = threadIdx.x; e < E; e += blockDim.x) base[e] = total[e] = 0;
     __syncthreads();
 
     // votes: this lane's pairs, their experts and ranks within the warp's run
-    const int first = blockIdx.x * kOrderChunk + warp * 32 * kOrderIters;
+    const int first = chunk0 + warp * 32 * iters;
     uint16_t *mine = run + warp * E;
     int key[kOrderIters], rank[kOrderIters];
 #pragma unroll
     for (int j = 0; j < kOrderIters; ++j) {
         const int i = first + 32 * j + lane;
-        const int id = i < n ? ids[i] : -1;
+        const int id = j < iters && i < n ? ids[i] : -1;
         key[j] = (unsigned)id < (unsigned)E ? id : -1;
     }
 #pragma unroll
     for (int j = 0; j < kOrderIters; ++j) {
         rank[j] = 0;
-        if (first + 32 * j >= n) continue;   // uniform over the warp
+        if (j >= iters || first + 32 * j >= n) continue;   // uniform over the warp
         const unsigned same = __match_any_sync(0xFFFFFFFFu, key[j]);
         const int before = __popc(same & ((1u << lane) - 1u));
         const int old = key[j] >= 0 ? mine[key[j]] : 0;
@@ -80,25 +88,23 @@ __global__ void __launch_bounds__(512) order_place(const int32_t *__restrict__ i
     }
     // pairs of the chunks before this one, and of all
     if (hist) {
-        // threads of a group of P share an expert's column of hist
-        const int P = E >= 512 ? 1 : 512 / E < (int)gridDim.x ? 512 / E : (int)gridDim.x;
-        for (int e0 = 0; e0 < E; e0 += 512) {
-            const int e = e0 + threadIdx.x % (E < 512 ? E : 512), p = E < 512 ? threadIdx.x / E : 0;
-            if (e < E && p < P) {
-                int b = 0, t = 0;
-#pragma unroll 8
-                for (int c = p; c < (int)gridDim.x; c += P) {
-                    const int h = hist[(size_t)c * E + e];
-                    t += h;
-                    if (c < (int)blockIdx.x) b += h;
-                }
-                if (P == 1) {
-                    base[e] = b;
-                    total[e] = t;
-                } else {
-                    atomicAdd(base + e, b);
-                    atomicAdd(total + e, t);
-                }
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        // P threads share an expert's column of hist (kOrderThreads >= MOE_MAX_EXPERTS: every expert has one)
+        const int P = min(kOrderThreads / E, (int)gridDim.x), e = threadIdx.x % E, p = threadIdx.x / E;
+        if (p < P) {
+            int b = 0, t = 0;
+#pragma unroll 16
+            for (int ch = p; ch < (int)gridDim.x; ch += P) {
+                const int h = hist[(size_t)ch * E + e];
+                t += h;
+                if (ch < (int)blockIdx.x) b += h;
+            }
+            if (P == 1) {
+                base[e] = b;
+                total[e] = t;
+            } else {
+                atomicAdd(base + e, b);
+                atomicAdd(total + e, t);
             }
         }
     }
@@ -106,8 +112,8 @@ __global__ void __launch_bounds__(512) order_place(const int32_t *__restrict__ i
     // the runs before each run of this chunk
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         int sum = 0;
-#pragma unroll
-        for (int w = 0; w < kOrderWarps; ++w) {
+#pragma unroll 8
+        for (int w = 0; w < used; ++w) {
             const int c = run[w * E + e];
             run[w * E + e] = (uint16_t)sum;
             sum += c;
@@ -115,44 +121,38 @@ __global__ void __launch_bounds__(512) order_place(const int32_t *__restrict__ i
         if (!hist) total[e] = sum;
     }
     __syncthreads();
-    // offsets: exclusive prefix sums over the experts, 512 at a time
-    int carry = 0;
-    for (int e0 = 0; e0 < E; e0 += 512) {
-        const int e = e0 + threadIdx.x;
-        const int c = e < E ? total[e] : 0;
-        int s = c;
+    // offsets: exclusive prefix sums over the experts, one a thread
+    const int e = threadIdx.x, c = e < E ? total[e] : 0;
+    int s = c;
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int o = __shfl_up_sync(0xFFFFFFFFu, s, off);
-            if (lane >= off) s += o;
-        }
-        if (lane == 31) wsum[warp] = s;
-        __syncthreads();
-        int up = carry, all = 0;
-        for (int w = 0; w < kOrderWarps; ++w) {
-            if (w < warp) up += wsum[w];
-            all += wsum[w];
-        }
-        if (e < E) {
-            const int o = up + s - c;
-            base[e] += o;
-            if (blockIdx.x == 0) {
-                if (counts) counts[e] = c;
-                if (offsets) offsets[e] = o;
-            }
-        }
-        carry += all;
-        __syncthreads();
+    for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, s, off);
+        if (lane >= off) s += o;
     }
-    if (threadIdx.x == 0) {
-        live = carry;
-        if (blockIdx.x == 0 && offsets) offsets[E] = carry;
+    if (lane == 31) wsum[warp] = s;
+    __syncthreads();
+    int up = wsum[lane];
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, up, off);
+        if (lane >= off) up += o;
     }
+    const int live = __shfl_sync(0xFFFFFFFFu, up, 31);
+    up = warp ? __shfl_sync(0xFFFFFFFFu, up, (warp + 31) & 31) : 0;
+    if (e < E) {
+        const int o = up + s - c;
+        base[e] += o;
+        if (blockIdx.x == 0) {
+            if (counts) counts[e] = c;
+            if (offsets) offsets[e] = o;
+        }
+    }
+    if (blockIdx.x == 0 && e == 0 && offsets) offsets[E] = live;
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kOrderIters; ++j) {
         const int i = first + 32 * j + lane;
-        if (i >= n) continue;
+        if (j >= iters || i >= n) continue;
         const int place = key[j] >= 0 ? base[key[j]] + mine[key[j]] + rank[j] : -1;
         if (pos) pos[i] = place;
         if (rows && place >= 0) rows[place] = (unsigned)i / (unsigned)k;
@@ -172,8 +172,12 @@ __global__ void __launch_bounds__(512) order_place(const int32_t *__restrict__ i
 // loss and gradient come from one reading of the logits: a warp holds a row,
 // its d_e stay in registers, and it walks over the rows.  Bandwidth bounds it.
 //
-// Sums: a row in fp32 by an xor butterfly; a warp's rows, a block's warps and
-// the blocks in double, in order (the last block to finish adds the blocks).
+// Sums: a row and a warp's few rows in fp32 (a count holds the ones of 1 + q),
+// a block's warps and the blocks in double, in order (the last block to finish
+// adds the blocks).  Double arithmetic stays out of the loop: this part has few
+// units for it, and one addition a row cost a third of the kernel's time.
+// exp and the reciprocal of sigma are the fast ones (2 ulp and |l - m| u, 1 ulp):
+// the accurate ones made the kernel issue-bound (70% of issue slots).
 constexpr int kBalanceWarps = 8;
 
 struct BalanceArgs {
@@ -186,7 +190,7 @@ struct BalanceArgs {
     unsigned *ticket;     // ws
     double *partial;      // ws [blocks]
     float alpha;
-    int T, E, k, sigmoid;
+    int T, E, k;
 };
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -195,13 +199,10 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, off));
-    return v;
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
 }
-
-template <typename T>
-__device__ __forceinline__ float to_f32(T v) { return (float)v; }
 
 // VEC consecutive values of a row (VEC 1: any alignment)
 template <typename T, int VEC>
@@ -231,7 +232,7 @@ __device__ __forceinline__ void store_vec(T *p, const float v[VEC]) {
 }
 
 // J vectors of VEC values a lane: value i of vector j is expert 32*VEC*j + VEC*lane + i
-template <typename T, int VEC, int J>
+template <typename T, bool SIGMOID, int VEC, int J>
 __global__ void __launch_bounds__(32 * kBalanceWarps) balance_kernel(const BalanceArgs a) {
     __shared__ double part[kBalanceWarps];
     __shared__ int last;
@@ -257,7 +258,8 @@ __global__ void __launch_bounds__(32 * kBalanceWarps) balance_kernel(const Balan
 #pragma unroll
         for (int i = 0; i < VEC; ++i) d[j][i] = (float)((long long)__float_as_int(d[j][i]) * E - N) * invN;
 
-    double sum = 0.0;
+    float sum = 0.f;   // of q
+    int rows = 0;      // rows that count
     const int step = gridDim.x * kBalanceWarps;
     for (int t = blockIdx.x * kBalanceWarps + warp; t < a.T; t += step) {
         const T *row = static_cast<const T *>(a.logits) + (size_t)t * E;
@@ -289,51 +291,54 @@ __global__ void __launch_bounds__(32 * kBalanceWarps) balance_kernel(const Balan
             continue;
         }
         float s = 0.f, q = 0.f;
-        float slope[J][VEC];   // 1 - sigma(l); softmax: 1
-        if (a.sigmoid) {
+        float slope[SIGMOID ? J : 1][VEC];   // 1 - sigma(l)
+        if constexpr (SIGMOID) {
             // sigma(l) e^-m with m = min(0, the row's largest logit): the
             // factor falls out of the ratio, and rows far below 0 keep their
             // probabilities where sigma itself would vanish
-            m = fminf(m, 0.f);
 #pragma unroll
             for (int j = 0; j < J; ++j)
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
-                    const float l = p[j][i], u = expf(-fabsf(l)), r = 1.f / (1.f + u);
-                    slope[j][i] = l > 0.f ? u * r : r;
-                    p[j][i] = l > 0.f ? r : (m < 0.f ? expf(l - m) : u) * r;
-                    s += p[j][i];
-                    q = fmaf(p[j][i], d[j][i], q);
+                    const float l = p[j][i], u = __expf(-fabsf(l)), r = __fdividef(1.f, 1.f + u), ur = u * r;
+                    slope[j][i] = l > 0.f ? ur : r;
+                    p[j][i] = l > 0.f ? r : m < 0.f ? __expf(l - m) * r : ur;
                 }
         } else {
 #pragma unroll
             for (int j = 0; j < J; ++j)
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    p[j][i] = expf(p[j][i] - m);
-                    slope[j][i] = 1.f;
-                    s += p[j][i];
-                    q = fmaf(p[j][i], d[j][i], q);
-                }
+                for (int i = 0; i < VEC; ++i) p[j][i] = __expf(p[j][i] - m);
         }
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                s += p[j][i];
+                q = fmaf(p[j][i], d[j][i], q);
+            }
         s = warp_sum(s);
         q = warp_sum(q);
-        const float inv = 1.f / s;
+        const float inv = __fdiv_rn(1.f, s);
         q *= inv;
-        sum += 1.0 + (double)q;
+        sum += q;
+        ++rows;
         if (out) {
             const float g = gcoef * inv;
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 const int e = 32 * VEC * j + VEC * lane;
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) p[j][i] = g * p[j][i] * slope[j][i] * (d[j][i] - q);
+                for (int i = 0; i < VEC; ++i) {
+                    p[j][i] *= g * (d[j][i] - q);
+                    if constexpr (SIGMOID) p[j][i] *= slope[j][i];
+                }
                 if (e < E) store_vec<T, VEC>(out + e, p[j]);
             }
         }
     }
     if (!a.loss) return;
-    if (lane == 0) part[warp] = sum;
+    if (lane == 0) part[warp] = (double)sum + rows;
     __syncthreads();
     if (threadIdx.x == 0) {
         double b = 0.0;
@@ -364,20 +369,20 @@ int balance_blocks(int T) {
     return b < 1 ? 1 : b > kBalanceBlocks ? kBalanceBlocks : b;
 }
 
-template <typename T>
+template <typename T, bool SIGMOID>
 cudaError_t launch_balance_t(const BalanceArgs &a, cudaStream_t s) {
     const int g = balance_blocks(a.T), th = 32 * kBalanceWarps;
     // rows whose length is a multiple of 4 are read 4 values at a time
     if (a.E % 4 == 0) {
-        if (a.E <= 128) balance_kernel<T, 4, 1><<<g, th, 0, s>>>(a);
-        else if (a.E <= 256) balance_kernel<T, 4, 2><<<g, th, 0, s>>>(a);
-        else if (a.E <= 512) balance_kernel<T, 4, 4><<<g, th, 0, s>>>(a);
-        else balance_kernel<T, 4, 8><<<g, th, 0, s>>>(a);
+        if (a.E <= 128) balance_kernel<T, SIGMOID, 4, 1><<<g, th, 0, s>>>(a);
+        else if (a.E <= 256) balance_kernel<T, SIGMOID, 4, 2><<<g, th, 0, s>>>(a);
+        else if (a.E <= 512) balance_kernel<T, SIGMOID, 4, 4><<<g, th, 0, s>>>(a);
+        else balance_kernel<T, SIGMOID, 4, 8><<<g, th, 0, s>>>(a);
     } else {
-        if (a.E <= 128) balance_kernel<T, 1, 4><<<g, th, 0, s>>>(a);
-        else if (a.E <= 256) balance_kernel<T, 1, 8><<<g, th, 0, s>>>(a);
-        else if (a.E <= 512) balance_kernel<T, 1, 16><<<g, th, 0, s>>>(a);
-        else balance_kernel<T, 1, 32><<<g, th, 0, s>>>(a);
+        if (a.E <= 128) balance_kernel<T, SIGMOID, 1, 4><<<g, th, 0, s>>>(a);
+        else if (a.E <= 256) balance_kernel<T, SIGMOID, 1, 8><<<g, th, 0, s>>>(a);
+        else if (a.E <= 512) balance_kernel<T, SIGMOID, 1, 16><<<g, th, 0, s>>>(a);
+        else balance_kernel<T, SIGMOID, 1, 32><<<g, th, 0, s>>>(a);
     }
     return cudaGetLastError();
 }
@@ -394,15 +399,28 @@ cudaError_t launch_order(const int32_t *ids, int T, int k, int E, int32_t *count
     const int n = T * k;
     const int chunks = n > 0 ? (n + kOrderChunk - 1) / kOrderChunk : 1;
     int32_t *hist = chunks > 1 ? static_cast<int32_t *>(ws) : nullptr;
-    if (hist) {
-        order_count<<<chunks, 512, E * sizeof(int32_t), s>>>(ids, n, E, hist);
-        const cudaError_t err = cudaGetLastError();
-        if (err != cudaSuccess) return err;
-    }
-    // at most 40 KB (E = 1024): below the limit that needs an opt-in
+    // 72 KB at E = 1024
     const size_t smem = (size_t)E * (2 * sizeof(int32_t) + kOrderWarps * sizeof(uint16_t));
-    order_place<<<chunks, 512, smem, s>>>(ids, n, k, E, hist, counts, offsets, rows, pos);
-    return cudaGetLastError();
+    cudaError_t err = cudaSuccess;
+    if (smem > 48 * 1024)
+        err = cudaFuncSetAttribute(order_place, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)chunks);
+    cfg.blockDim = dim3(kOrderThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    if (hist) {
+        order_count<<<chunks, kOrderThreads, E * sizeof(int32_t), s>>>(ids, n, E, hist);
+        err = cudaGetLastError();
+        if (err != cudaSuccess) return err;
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+    }
+    return cudaLaunchKernelEx(&cfg, order_place, ids, n, k, E, (const int32_t *)hist, counts, offsets, rows, pos);
 }
 
 size_t balance_ws_bytes() { return 256 + kBalanceBlocks * sizeof(double); }
@@ -423,8 +441,9 @@ cudaError_t launch_balance(const void *logits, int dtype, const int32_t *counts,
     a.T = T;
     a.E = E;
     a.k = k;
-    a.sigmoid = gating == MOE_GATE_SIGMOID;
-    return dtype == MOE_DT_BF16 ? launch_balance_t<__nv_bfloat16>(a, s) : launch_balance_t<float>(a, s);
+    if (gating == MOE_GATE_SIGMOID)
+        return dtype == MOE_DT_BF16 ? launch_balance_t<__nv_bfloat16, true>(a, s) : launch_balance_t<float, true>(a, s);
+    return dtype == MOE_DT_BF16 ? launch_balance_t<__nv_bfloat16, false>(a, s) : launch_balance_t<float, false>(a, s);
 }
 
 }  // namespace moe
