@@ -10,7 +10,7 @@
 // warps of a block have roles that work on different blocks b at once:
 //   warp 0    : TMA copies of w tiles, and of x tiles where the rows are in
 //               order (128 bytes deep, 128-byte swizzle), into a ring of stages
-//   warp 1    : one thread issues the products into one of two TMEM buffers
+//   warp 1    : one thread issues the products into one of the TMEM buffers
 //   warps 2-3 : rows that are gathered, by 16-byte asynchronous copies
 //   warps 4.. : acc += (sx * sw) * D_b, 64 columns a warp.  TMEM gives lane i of
 //               the tile to thread i, so sx is one number a thread and sw one a
@@ -36,7 +36,6 @@ constexpr int BK = 128;             // bytes of depth of a stage (one scale bloc
 constexpr int EPI_FIRST = 4;        // first accumulating warp
 constexpr int HC = 64;              // columns of an accumulating warp
 constexpr int GATHER_LAG = 2;       // stages of gathered rows in flight before one is handed over
-constexpr int NBUF = 2;             // TMEM buffers
 constexpr int RED_PITCH = BM + 1;   // fp32 partial tiles, column by column
 // bound on every device-side wait, in SM clock cycles (under a second)
 constexpr long long FP8_WAIT_CYCLES = 800ll * 1000ll * 1000ll;
@@ -46,6 +45,8 @@ struct Shape {
     static constexpr int STAGES = BN == 256 ? 4 : 6;
     static constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE = A_BYTES + B_BYTES;
     static constexpr int SMEM = STAGES * STAGE + 1024;   // + alignment of the swizzle pattern
+    static constexpr int NBUF = 512 / BN;                // TMEM buffers
+    static constexpr int AHEAD = BN == 256 ? 2 : 4;      // 16-column loads on their way in an accumulating warp
     static constexpr int EPI_WARPS = 4 * (BN / HC), THREADS = 32 * (EPI_FIRST + EPI_WARPS);
 };
 
@@ -60,7 +61,7 @@ struct Fp8Args {
 };
 
 struct Ctl {
-    uint64_t full[6], empty[6], dfull[NBUF], dempty[NBUF], drain;
+    uint64_t full[6], empty[6], dfull[4], dempty[4], drain;
     uint32_t tmem;
     int abort;
     int goff[MOE_MAX_EXPERTS + 1];     // first place of each group, clamped
@@ -260,7 +261,7 @@ template <int BN, typename TY, bool SPLIT>
 __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
     fp8_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw, const Fp8Args a) {
     using S = Shape<BN>;
-    constexpr int THREADS = S::THREADS;
+    constexpr int THREADS = S::THREADS, NBUF = S::NBUF;
     extern __shared__ uint8_t raw[];
     __shared__ Ctl c;
     uint8_t *stages = raw + ((1024 - (sa(raw) & 1023)) & 1023);
@@ -467,19 +468,35 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
                     uint64_t ss;
                     asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "r"(__float_as_uint(s)));
                     const uint32_t at = tmem + buf * BN + part * HC + ((uint32_t)(32 * quad) << 16);
-                    // one load is on its way while the one before it is added
-                    uint32_t u[2][16];
-                    tmem_ld16(at, u[0]);
+                    // Beside running products a load takes about 250 cycles, however much is on its way, so as
+                    // much is as the registers beside the sums hold: all 64 columns (BN 128), or the next 16
+                    // while 16 are added (BN 256).  The buffer goes back before the last columns are added.
+                    uint32_t u[S::AHEAD][16];
+                    if constexpr (S::AHEAD == 4) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) tmem_ld16(at + 16 * j, u[j]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) tmem_ld_wait(u[j]);
+                    } else {
+                        tmem_ld16(at, u[0]);
+                    }
 #pragma unroll
                     for (int j = 0; j < HC / 16; ++j) {
-                        tmem_ld_wait(u[j & 1]);
-                        if (j + 1 < HC / 16) tmem_ld16(at + 16 * (j + 1), u[(j + 1) & 1]);
+                        uint32_t *v = u[j % S::AHEAD];
+                        if constexpr (S::AHEAD == 2) {
+                            tmem_ld_wait(v);
+                            if (j + 1 < HC / 16) tmem_ld16(at + 16 * (j + 1), u[(j + 1) % 2]);
+                        }
+                        if (j == (S::AHEAD == 4 ? 0 : HC / 16 - 1)) {
+                            fence_before();
+                            if (lane == 0) bar_arrive(&c.dempty[buf]);
+                        }
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) fma2(acc[8 * j + i], u[j & 1][2 * i], u[j & 1][2 * i + 1], ss);
+                        for (int i = 0; i < 8; ++i) fma2(acc[8 * j + i], v[2 * i], v[2 * i + 1], ss);
                     }
+                } else if (lane == 0) {
+                    bar_arrive(&c.dempty[buf]);
                 }
-                fence_before();
-                if (lane == 0) bar_arrive(&c.dempty[buf]);
             }
             if (!ok) break;
             if (bad) {
