@@ -13,9 +13,10 @@ namespace {
 // A stable counting sort by expert.  The pairs are cut into chunks of
 // kOrderChunk, one block each; in a chunk, warp w takes the w-th run of
 // 32 * kOrderIters pairs, 32 at a time in order.  Lanes with the same expert
-// find one another with a match vote, so a pair's rank among the run's pairs
-// of its expert is the run's count so far plus the earlier lanes of its vote:
-// no atomics, and the order is that of the pairs.
+// find one another with one ballot for each bit of its number (a match vote of
+// 32 warps took 2,200 cycles, the ballots take 400), so a pair's rank among the
+// run's pairs of its expert is the run's count so far plus the earlier lanes
+// of its vote: no atomics, and the order is that of the pairs.
 //   order_count : chunk b's pairs per expert -> hist[b][E]
 //   order_place : place = offsets[e] + sum of hist[b' < b][e] + the chunk's
 //                 earlier runs + rank
@@ -26,11 +27,14 @@ namespace {
 // and the 4-byte scatter of rows.
 constexpr int kOrderWarps = 32;
 constexpr int kOrderThreads = 32 * kOrderWarps;
-constexpr int kOrderIters = 8;
-constexpr int kOrderChunk = kOrderThreads * kOrderIters;   // 8192; counts in a chunk fit 16 bits
+constexpr int kOrderIters = 4;
+constexpr int kOrderChunk = kOrderThreads * kOrderIters;   // 4096; counts in a chunk fit 16 bits
+
+// counts of a chunk in hist: 16 bits each, rows of whole 16-byte pieces
+__host__ __device__ constexpr int hist_pitch(int E) { return (E + 7) & ~7; }
 
 __global__ void __launch_bounds__(kOrderThreads) order_count(const int32_t *__restrict__ ids, int n, int E,
-                                                   int32_t *__restrict__ hist) {
+                                                   uint16_t *__restrict__ hist) {
     extern __shared__ int32_t cnt[];
     asm volatile("griddepcontrol.launch_dependents;");
     for (int e = threadIdx.x; e < E; e += blockDim.x) cnt[e] = 0;
@@ -43,68 +47,95 @@ __global__ void __launch_bounds__(kOrderThreads) order_count(const int32_t *__re
         if ((unsigned)id < (unsigned)E) atomicAdd(cnt + id, 1);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += blockDim.x) hist[(size_t)blockIdx.x * E + e] = cnt[e];
+    const int pitch = hist_pitch(E);
+    for (int e = threadIdx.x; e < pitch; e += blockDim.x)
+        hist[(size_t)blockIdx.x * pitch + e] = e < E ? (uint16_t)cnt[e] : 0;
 }
 
 __global__ void __launch_bounds__(kOrderThreads) order_place(const int32_t *__restrict__ ids, int n, int k, int E,
-                                                   const int32_t *hist, int32_t *__restrict__ counts,
+                                                   const uint16_t *hist, int32_t *__restrict__ counts,
                                                    int32_t *__restrict__ offsets, int32_t *__restrict__ rows,
                                                    int32_t *__restrict__ pos) {
     extern __shared__ int32_t sm[];
-    int32_t *base = sm;                                          // [E] first place of this chunk's pairs
-    int32_t *total = sm + E;                                     // [E] pairs of an expert in all chunks
-    uint16_t *run = reinterpret_cast<uint16_t *>(sm + 2 * E);    // [kOrderWarps][E]
+    const int pitch = hist_pitch(E), pieces = pitch / 8;
+    int32_t *base = sm;                                            // [E] first place of this chunk's pairs
+    int32_t *total = sm + pitch;                                   // [E] pairs of an expert in all chunks
+    uint16_t *run = reinterpret_cast<uint16_t *>(sm + 2 * pitch);  // [kOrderWarps][pitch]
     __shared__ int32_t wsum[kOrderWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // this chunk's pairs in runs of 32 * iters, one a warp: few pairs take few votes in a row
     const int chunk0 = blockIdx.x * kOrderChunk, have = min(n - chunk0, kOrderChunk);
     const int iters = (have + kOrderThreads - 1) / kOrderThreads;
     const int used = iters ? (have + 32 * iters - 1) / (32 * iters) : 0;   // warps with pairs
-    for (int i = threadIdx.x; i < used * E; i += blockDim.x) run[i] = 0;
-    for (int e = threadIdx.x; e < E; e += blockDim.x) base[e] = total[e] = 0;
+    for (int i = threadIdx.x; i < used * pieces; i += blockDim.x)
+        reinterpret_cast<uint4 *>(run)[i] = make_uint4(0, 0, 0, 0);
+    for (int e = threadIdx.x; e < 2 * pitch; e += blockDim.x) base[e] = 0;   // total too
     __syncthreads();
 
     // votes: this lane's pairs, their experts and ranks within the warp's run
     const int first = chunk0 + warp * 32 * iters;
-    uint16_t *mine = run + warp * E;
+    uint16_t *mine = run + warp * pitch;
+    const int bits = 32 - __clz(E);   // of 0 .. E: E stands for a pair that takes no part
     int key[kOrderIters], rank[kOrderIters];
 #pragma unroll
     for (int j = 0; j < kOrderIters; ++j) {
         const int i = first + 32 * j + lane;
         const int id = j < iters && i < n ? ids[i] : -1;
-        key[j] = (unsigned)id < (unsigned)E ? id : -1;
+        key[j] = (unsigned)id < (unsigned)E ? id : E;
+    }
+    unsigned same[kOrderIters];
+#pragma unroll
+    for (int j = 0; j < kOrderIters; ++j) same[j] = 0xFFFFFFFFu;
+    const auto vote = [&](int j, int b) {
+        const bool one = (key[j] >> b) & 1;
+        const unsigned with = __ballot_sync(0xFFFFFFFFu, one);
+        same[j] &= one ? with : ~with;
+    };
+    // (not unrolled: a small call is bound by its launch and the fetch of its instructions)
+    if (iters == 1) {
+#pragma unroll 1
+        for (int b = 0; b < bits; ++b) vote(0, b);
+    } else {
+#pragma unroll 1
+        for (int b = 0; b < bits; ++b)
+#pragma unroll
+            for (int j = 0; j < kOrderIters; ++j) vote(j, b);
     }
 #pragma unroll
     for (int j = 0; j < kOrderIters; ++j) {
         rank[j] = 0;
         if (j >= iters || first + 32 * j >= n) continue;   // uniform over the warp
-        const unsigned same = __match_any_sync(0xFFFFFFFFu, key[j]);
-        const int before = __popc(same & ((1u << lane) - 1u));
-        const int old = key[j] >= 0 ? mine[key[j]] : 0;
+        const int before = __popc(same[j] & ((1u << lane) - 1u));
+        const int old = key[j] < E ? mine[key[j]] : 0;
         __syncwarp();
-        if (key[j] >= 0 && before == 0) mine[key[j]] = (uint16_t)(old + __popc(same));
+        if (key[j] < E && before == 0) mine[key[j]] = (uint16_t)(old + __popc(same[j]));
         __syncwarp();
         rank[j] = old + before;
     }
     // pairs of the chunks before this one, and of all
     if (hist) {
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        // P threads share an expert's column of hist (kOrderThreads >= MOE_MAX_EXPERTS: every expert has one)
-        const int P = min(kOrderThreads / E, (int)gridDim.x), e = threadIdx.x % E, p = threadIdx.x / E;
+        // a thread takes 8 experts (one 16-byte piece) of every P-th chunk; experts e, e + 1, ... of a piece are
+        // `pieces` words apart in base and total until they are read, which keeps the additions free of conflicts
+        const int P = kOrderThreads / pieces, q = threadIdx.x % pieces, p = threadIdx.x / pieces;
         if (p < P) {
-            int b = 0, t = 0;
-#pragma unroll 16
+            int b[8] = {}, s8[8] = {};
+#pragma unroll 8
             for (int ch = p; ch < (int)gridDim.x; ch += P) {
-                const int h = hist[(size_t)ch * E + e];
-                t += h;
-                if (ch < (int)blockIdx.x) b += h;
+                const uint4 v = reinterpret_cast<const uint4 *>(hist + (size_t)ch * pitch)[q];
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                const bool before = ch < (int)blockIdx.x;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int h = (w[i / 2] >> (16 * (i & 1))) & 0xFFFF;
+                    s8[i] += h;
+                    b[i] += before ? h : 0;
+                }
             }
-            if (P == 1) {
-                base[e] = b;
-                total[e] = t;
-            } else {
-                atomicAdd(base + e, b);
-                atomicAdd(total + e, t);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (b[i]) atomicAdd(base + i * pieces + q, b[i]);
+                if (s8[i]) atomicAdd(total + i * pieces + q, s8[i]);
             }
         }
     }
@@ -112,17 +143,18 @@ __global__ void __launch_bounds__(kOrderThreads) order_place(const int32_t *__re
     // the runs before each run of this chunk
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         int sum = 0;
-#pragma unroll 8
+#pragma unroll 4
         for (int w = 0; w < used; ++w) {
-            const int c = run[w * E + e];
-            run[w * E + e] = (uint16_t)sum;
+            const int c = run[w * pitch + e];
+            run[w * pitch + e] = (uint16_t)sum;
             sum += c;
         }
         if (!hist) total[e] = sum;
     }
     __syncthreads();
     // offsets: exclusive prefix sums over the experts, one a thread
-    const int e = threadIdx.x, c = e < E ? total[e] : 0;
+    const int e = threadIdx.x, at = hist ? (e & 7) * pieces + (e >> 3) : e;
+    const int c = e < E ? total[at] : 0, before = e < E ? base[at] : 0;
     int s = c;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -141,7 +173,7 @@ __global__ void __launch_bounds__(kOrderThreads) order_place(const int32_t *__re
     up = warp ? __shfl_sync(0xFFFFFFFFu, up, (warp + 31) & 31) : 0;
     if (e < E) {
         const int o = up + s - c;
-        base[e] += o;
+        base[e] = before + o;
         if (blockIdx.x == 0) {
             if (counts) counts[e] = c;
             if (offsets) offsets[e] = o;
@@ -153,7 +185,7 @@ __global__ void __launch_bounds__(kOrderThreads) order_place(const int32_t *__re
     for (int j = 0; j < kOrderIters; ++j) {
         const int i = first + 32 * j + lane;
         if (j >= iters || i >= n) continue;
-        const int place = key[j] >= 0 ? base[key[j]] + mine[key[j]] + rank[j] : -1;
+        const int place = key[j] < E ? base[key[j]] + mine[key[j]] + rank[j] : -1;
         if (pos) pos[i] = place;
         if (rows && place >= 0) rows[place] = (unsigned)i / (unsigned)k;
         if (rows && i >= live) rows[i] = -1;
@@ -170,14 +202,16 @@ __global__ void __launch_bounds__(kOrderThreads) order_place(const int32_t *__re
 // and d_e - q_t keeps its digits where f_e - sum f p would lose them (even
 // counts: both are close to 1).  The counts are known before the pass, so
 // loss and gradient come from one reading of the logits: a warp holds a row,
-// its d_e stay in registers, and it walks over the rows.  Bandwidth bounds it.
+// its d_e stay in registers, and it walks over the rows, the next row's loads
+// under way while it adds up one.  Bandwidth bounds it.
 //
 // Sums: a row and a warp's few rows in fp32 (a count holds the ones of 1 + q),
 // a block's warps and the blocks in double, in order (the last block to finish
 // adds the blocks).  Double arithmetic stays out of the loop: this part has few
 // units for it, and one addition a row cost a third of the kernel's time.
-// exp and the reciprocal of sigma are the fast ones (2 ulp and |l - m| u, 1 ulp):
-// the accurate ones made the kernel issue-bound (70% of issue slots).
+// exp and the reciprocal of sigma are the machine's own, flushing below 2^-126
+// (exp is off by 2 ulp and |l - m| u, the reciprocal by 1 ulp): with the library
+// functions the kernel was bound by issue slots (350 instructions a row of 256).
 constexpr int kBalanceWarps = 8;
 
 struct BalanceArgs {
@@ -204,20 +238,33 @@ __device__ __forceinline__ float warp_max(float v) {
     return m;
 }
 
-// VEC consecutive values of a row (VEC 1: any alignment)
-template <typename T, int VEC>
-__device__ __forceinline__ void load_vec(const T *p, float v[VEC]) {
-    if constexpr (VEC == 1) {
-        v[0] = (float)p[0];
-    } else if constexpr (sizeof(T) == 4) {
-        const float4 a = *reinterpret_cast<const float4 *>(p);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    } else {
-        const uint2 a = *reinterpret_cast<const uint2 *>(p);
-        v[0] = __uint_as_float(a.x << 16); v[1] = __uint_as_float(a.x & 0xFFFF0000u);
-        v[2] = __uint_as_float(a.y << 16); v[3] = __uint_as_float(a.y & 0xFFFF0000u);
-    }
+// e^x for x <= 0 and 1/x for x in [1, 2]
+__device__ __forceinline__ float exp_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+    return r;
 }
+__device__ __forceinline__ float rcp_fast(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// VEC consecutive values of a row as they lie in memory (VEC 1: any alignment), and their values
+template <typename T, int VEC>
+struct Raw {
+    uint32_t w[VEC == 1 ? 1 : VEC * sizeof(T) / 4];
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (VEC == 1 && sizeof(T) == 2) w[0] = *reinterpret_cast<const uint16_t *>(p);
+        else if constexpr (VEC == 1) w[0] = *reinterpret_cast<const uint32_t *>(p);
+        else if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4 *>(w) = *reinterpret_cast<const uint4 *>(p);
+        else *reinterpret_cast<uint2 *>(w) = *reinterpret_cast<const uint2 *>(p);
+    }
+    __device__ __forceinline__ float value(int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+    }
+};
 template <typename T, int VEC>
 __device__ __forceinline__ void store_vec(T *p, const float v[VEC]) {
     if constexpr (VEC == 1) {
@@ -232,11 +279,29 @@ __device__ __forceinline__ void store_vec(T *p, const float v[VEC]) {
 }
 
 // J vectors of VEC values a lane: value i of vector j is expert 32*VEC*j + VEC*lane + i
+// blocks of a launch that share an SM (one row, its d and the next row take 3 to 4 registers a value)
+constexpr int balance_per_sm(int values) { return values <= 8 ? 4 : 2; }
+
 template <typename T, bool SIGMOID, int VEC, int J>
-__global__ void __launch_bounds__(32 * kBalanceWarps) balance_kernel(const BalanceArgs a) {
+__global__ void __launch_bounds__(32 * kBalanceWarps, balance_per_sm(VEC * J)) balance_kernel(const BalanceArgs a) {
     __shared__ double part[kBalanceWarps];
     __shared__ int last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.E;
+    const int step = gridDim.x * kBalanceWarps;
+    Raw<T, VEC> next[J];
+    bool next_live = false;
+    const auto fetch = [&](int t) {
+        next_live = !a.valid || a.valid[t];
+        if (!next_live) return;
+        const T *row = static_cast<const T *>(a.logits) + (size_t)t * E;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int e = 32 * VEC * j + VEC * lane;
+            if (e < E) next[j].load(row + e);
+        }
+    };
+    int t = blockIdx.x * kBalanceWarps + warp;
+    if (t < a.T) fetch(t);   // on its way while the counts are added up
     float d[J][VEC];
     long long N = 0;
 #pragma unroll
@@ -260,25 +325,24 @@ __global__ void __launch_bounds__(32 * kBalanceWarps) balance_kernel(const Balan
 
     float sum = 0.f;   // of q
     int rows = 0;      // rows that count
-    const int step = gridDim.x * kBalanceWarps;
-    for (int t = blockIdx.x * kBalanceWarps + warp; t < a.T; t += step) {
-        const T *row = static_cast<const T *>(a.logits) + (size_t)t * E;
+    for (; t < a.T; t += step) {
         T *out = a.dlogits ? static_cast<T *>(a.dlogits) + (size_t)t * E : nullptr;
         float p[J][VEC];
         float m = -INFINITY;
-        const bool live = N > 0 && (!a.valid || a.valid[t]);
+        const bool live = next_live && N > 0;
         if (live) {
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 const int e = 32 * VEC * j + VEC * lane;
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) p[j][i] = -INFINITY;
-                if (e < E) load_vec<T, VEC>(row + e, p[j]);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) m = fmaxf(m, p[j][i]);
+                for (int i = 0; i < VEC; ++i) {
+                    p[j][i] = e < E ? next[j].value(i) : -INFINITY;
+                    m = fmaxf(m, p[j][i]);
+                }
             }
-            m = warp_max(m);
         }
+        if (t + step < a.T) fetch(t + step);
+        if (live) m = warp_max(m);
         if (!live || m == -INFINITY) {   // uniform over the warp
             if (out) {
                 const float zero[VEC] = {};
@@ -291,24 +355,35 @@ __global__ void __launch_bounds__(32 * kBalanceWarps) balance_kernel(const Balan
             continue;
         }
         float s = 0.f, q = 0.f;
-        float slope[SIGMOID ? J : 1][VEC];   // 1 - sigma(l)
+        float ps[SIGMOID ? J : 1][VEC];   // sigma (1 - sigma), up to the factor of p
         if constexpr (SIGMOID) {
-            // sigma(l) e^-m with m = min(0, the row's largest logit): the
-            // factor falls out of the ratio, and rows far below 0 keep their
-            // probabilities where sigma itself would vanish
+            // with u = e^-|l| and r = 1 / (1 + u): sigma is r or u r, 1 - sigma the other one
+            if (m >= 0.f) {
 #pragma unroll
-            for (int j = 0; j < J; ++j)
+                for (int j = 0; j < J; ++j)
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const float l = p[j][i], u = __expf(-fabsf(l)), r = __fdividef(1.f, 1.f + u), ur = u * r;
-                    slope[j][i] = l > 0.f ? ur : r;
-                    p[j][i] = l > 0.f ? r : m < 0.f ? __expf(l - m) * r : ur;
-                }
+                    for (int i = 0; i < VEC; ++i) {
+                        const float l = p[j][i], u = exp_fast(-fabsf(l)), r = rcp_fast(1.f + u), ur = u * r;
+                        ps[j][i] = ur * r;
+                        p[j][i] = l > 0.f ? r : ur;
+                    }
+            } else {
+                // all logits below 0: sigma e^-m with the largest logit m.  The factor falls out of the ratio,
+                // and rows far below 0 keep their probabilities where sigma itself would vanish.
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        const float l = p[j][i], r = rcp_fast(1.f + exp_fast(l));
+                        p[j][i] = exp_fast(l - m) * r;
+                        ps[j][i] = p[j][i] * r;
+                    }
+            }
         } else {
 #pragma unroll
             for (int j = 0; j < J; ++j)
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) p[j][i] = __expf(p[j][i] - m);
+                for (int i = 0; i < VEC; ++i) p[j][i] = exp_fast(p[j][i] - m);
         }
 #pragma unroll
         for (int j = 0; j < J; ++j)
@@ -329,10 +404,7 @@ __global__ void __launch_bounds__(32 * kBalanceWarps) balance_kernel(const Balan
             for (int j = 0; j < J; ++j) {
                 const int e = 32 * VEC * j + VEC * lane;
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    p[j][i] *= g * (d[j][i] - q);
-                    if constexpr (SIGMOID) p[j][i] *= slope[j][i];
-                }
+                for (int i = 0; i < VEC; ++i) p[j][i] = (SIGMOID ? ps[SIGMOID ? j : 0][i] : p[j][i]) * (g * (d[j][i] - q));
                 if (e < E) store_vec<T, VEC>(out + e, p[j]);
             }
         }
@@ -348,13 +420,17 @@ __global__ void __launch_bounds__(32 * kBalanceWarps) balance_kernel(const Balan
         last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
     }
     __syncthreads();
-    if (!last || warp != 0) return;
+    if (!last) return;
     __threadfence();
     double b = 0.0;
-    for (int i = lane; i < (int)gridDim.x; i += 32) b += __ldcg(a.partial + i);
+    for (int i = threadIdx.x; i < (int)gridDim.x; i += 32 * kBalanceWarps) b += __ldcg(a.partial + i);
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) b += __shfl_xor_sync(0xFFFFFFFFu, b, off);
-    if (lane == 0) {
+    if (lane == 0) part[warp] = b;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        b = 0.0;
+        for (int w = 0; w < kBalanceWarps; ++w) b += part[w];
         a.loss[0] = (float)((double)a.alpha * b * (N > 0 ? (double)a.k / (double)N : 0.0));
         *a.ticket = 0;   // ready for the next call
     }
@@ -362,27 +438,27 @@ __global__ void __launch_bounds__(32 * kBalanceWarps) balance_kernel(const Balan
 
 constexpr int kBalanceBlocks = 1024;   // most blocks of a launch (the workspace's partial sums)
 
-int balance_blocks(int T) {
-    // five blocks an SM are resident at most; fewer rows than warps: one row a warp
-    const int want = (T + kBalanceWarps - 1) / kBalanceWarps, most = 5 * num_sms();
-    const int b = want < most ? want : most;
-    return b < 1 ? 1 : b > kBalanceBlocks ? kBalanceBlocks : b;
+template <typename T, bool SIGMOID, int VEC, int J>
+void launch_balance_k(const BalanceArgs &a, cudaStream_t s) {
+    // all blocks resident at once, each walking over its share of the rows; one row a warp where there are few
+    const int want = (a.T + kBalanceWarps - 1) / kBalanceWarps, most = balance_per_sm(VEC * J) * num_sms();
+    const int b = min(max(min(want, most), 1), kBalanceBlocks);
+    balance_kernel<T, SIGMOID, VEC, J><<<b, 32 * kBalanceWarps, 0, s>>>(a);
 }
 
 template <typename T, bool SIGMOID>
 cudaError_t launch_balance_t(const BalanceArgs &a, cudaStream_t s) {
-    const int g = balance_blocks(a.T), th = 32 * kBalanceWarps;
     // rows whose length is a multiple of 4 are read 4 values at a time
     if (a.E % 4 == 0) {
-        if (a.E <= 128) balance_kernel<T, SIGMOID, 4, 1><<<g, th, 0, s>>>(a);
-        else if (a.E <= 256) balance_kernel<T, SIGMOID, 4, 2><<<g, th, 0, s>>>(a);
-        else if (a.E <= 512) balance_kernel<T, SIGMOID, 4, 4><<<g, th, 0, s>>>(a);
-        else balance_kernel<T, SIGMOID, 4, 8><<<g, th, 0, s>>>(a);
+        if (a.E <= 128) launch_balance_k<T, SIGMOID, 4, 1>(a, s);
+        else if (a.E <= 256) launch_balance_k<T, SIGMOID, 4, 2>(a, s);
+        else if (a.E <= 512) launch_balance_k<T, SIGMOID, 4, 4>(a, s);
+        else launch_balance_k<T, SIGMOID, 4, 8>(a, s);
     } else {
-        if (a.E <= 128) balance_kernel<T, SIGMOID, 1, 4><<<g, th, 0, s>>>(a);
-        else if (a.E <= 256) balance_kernel<T, SIGMOID, 1, 8><<<g, th, 0, s>>>(a);
-        else if (a.E <= 512) balance_kernel<T, SIGMOID, 1, 16><<<g, th, 0, s>>>(a);
-        else balance_kernel<T, SIGMOID, 1, 32><<<g, th, 0, s>>>(a);
+        if (a.E <= 128) launch_balance_k<T, SIGMOID, 1, 4>(a, s);
+        else if (a.E <= 256) launch_balance_k<T, SIGMOID, 1, 8>(a, s);
+        else if (a.E <= 512) launch_balance_k<T, SIGMOID, 1, 16>(a, s);
+        else launch_balance_k<T, SIGMOID, 1, 32>(a, s);
     }
     return cudaGetLastError();
 }
@@ -391,16 +467,16 @@ cudaError_t launch_balance_t(const BalanceArgs &a, cudaStream_t s) {
 
 size_t order_ws_bytes(int T, int k, int E) {
     const long long n = (long long)T * k, chunks = (n + kOrderChunk - 1) / kOrderChunk;
-    return chunks > 1 ? (size_t)chunks * E * sizeof(int32_t) : 0;
+    return chunks > 1 ? (size_t)chunks * hist_pitch(E) * sizeof(uint16_t) : 0;
 }
 
 cudaError_t launch_order(const int32_t *ids, int T, int k, int E, int32_t *counts, int32_t *offsets, int32_t *rows,
                          int32_t *pos, void *ws, cudaStream_t s) {
     const int n = T * k;
     const int chunks = n > 0 ? (n + kOrderChunk - 1) / kOrderChunk : 1;
-    int32_t *hist = chunks > 1 ? static_cast<int32_t *>(ws) : nullptr;
+    uint16_t *hist = chunks > 1 ? static_cast<uint16_t *>(ws) : nullptr;
     // 72 KB at E = 1024
-    const size_t smem = (size_t)E * (2 * sizeof(int32_t) + kOrderWarps * sizeof(uint16_t));
+    const size_t smem = (size_t)hist_pitch(E) * (2 * sizeof(int32_t) + kOrderWarps * sizeof(uint16_t));
     cudaError_t err = cudaSuccess;
     if (smem > 48 * 1024)
         err = cudaFuncSetAttribute(order_place, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -420,7 +496,7 @@ cudaError_t launch_order(const int32_t *ids, int T, int k, int E, int32_t *count
         cfg.attrs = at;
         cfg.numAttrs = 1;
     }
-    return cudaLaunchKernelEx(&cfg, order_place, ids, n, k, E, (const int32_t *)hist, counts, offsets, rows, pos);
+    return cudaLaunchKernelEx(&cfg, order_place, ids, n, k, E, (const uint16_t *)hist, counts, offsets, rows, pos);
 }
 
 size_t balance_ws_bytes() { return 256 + kBalanceBlocks * sizeof(double); }

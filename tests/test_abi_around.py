@@ -14,7 +14,7 @@ S = ctypes.c_void_p(0)
 
 def test_sizes():
     assert moe.moe_expert_order_workspace_bytes(512, 8, 256) == 0            # few pairs need none
-    assert moe.moe_expert_order_workspace_bytes(65536, 8, 256) % (256 * 4) == 0
+    assert moe.moe_expert_order_workspace_bytes(65536, 8, 256) % (256 * 2) == 0
     assert moe.moe_expert_order_workspace_bytes(65536, 8, 256) > 0
     assert moe.moe_expert_order_workspace_bytes(0, 8, 256) == 0
     assert moe.moe_expert_order_workspace_bytes(1, 0, 256) == 0
@@ -43,7 +43,7 @@ def test_norm_refusals(change, status):
     (dict(T=-1), INVALID), (dict(k=0), INVALID), (dict(k=33), INVALID), (dict(E=0), INVALID), (dict(E=1025), INVALID),
     (dict(T=(1 << 22) // 8 + 1), INVALID), (dict(ids=None), INVALID), (dict(ids=P + 2), INVALID),
     (dict(counts=P + 1), INVALID), (dict(counts=None), INVALID), (dict(T=0, counts=None), 0), (dict(T=10000, ws=None), WS),
-    (dict(T=10000, size=8 * 4 * 10 - 1), WS), (dict(T=10000, ws=P + 4), WS)])
+    (dict(T=10000, size=8 * 2 * 10 - 1), WS), (dict(T=10000, ws=P + 4), WS)])
 def test_order_refusals(change, status):
     a = dict(ids=P, T=4, k=8, E=8, counts=P, ws=P, size=1 << 20)
     a.update(change)
