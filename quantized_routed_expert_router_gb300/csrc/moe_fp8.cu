@@ -19,7 +19,7 @@
 // x, w or K are zero-filled; rows of other groups that a tile happens to load
 // only reach accumulators that are not stored.
 //
-// Large products are persistent blocks, one an SM, over the tiles (BN 256).
+// Large products are persistent blocks, one an SM, over the tiles (BN 192).
 // When there are fewer tiles than SMs, a cluster of S blocks splits the depth of
 // a tile and adds its parts through distributed shared memory in rank order.
 #include <cuda.h>
@@ -35,19 +35,41 @@ constexpr int BM = 128;             // places of a tile (TMEM lanes)
 constexpr int BK = 128;             // bytes of depth of a stage (one scale block)
 constexpr int EPI_FIRST = 4;        // first accumulating warp
 constexpr int HC = 64;              // columns of an accumulating warp
-constexpr int GATHER_LAG = 2;       // stages of gathered rows in flight before one is handed over
+constexpr int GATHER_THREADS = 64;  // warps 2 and 3
 constexpr int RED_PITCH = BM + 1;   // fp32 partial tiles, column by column
-// bound on every device-side wait, in SM clock cycles (under a second)
-constexpr long long FP8_WAIT_CYCLES = 800ll * 1000ll * 1000ll;
+// bound on every device-side wait, in units of 2^16 SM clock cycles (8e8 cycles: under a second)
+constexpr uint32_t FP8_WAIT = 12207;
 
+// What bounds the widest tile is how the sums come back: a TMEM load beside
+// running products takes about 250 cycles however wide it is, so a warp wants
+// all of its 64 columns on their way at once, 64 registers beside its 64 sums.
+// 128 x 192 is the widest tile whose sums and loads fit the register file
+// (12 warps x 152 registers a thread); at 128 x 256 a warp had 16 columns on
+// their way and a block of depth took 950 cycles where its products take 512.
 template <int BN>
 struct Shape {
-    static constexpr int STAGES = BN == 256 ? 4 : 6;
+    static constexpr int STAGES = BN == 192 ? 5 : 6;
     static constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE = A_BYTES + B_BYTES;
     static constexpr int SMEM = STAGES * STAGE + 1024;   // + alignment of the swizzle pattern
     static constexpr int NBUF = 512 / BN;                // TMEM buffers
-    static constexpr int AHEAD = BN == 256 ? 2 : 4;      // 16-column loads on their way in an accumulating warp
     static constexpr int EPI_WARPS = 4 * (BN / HC), THREADS = 32 * (EPI_FIRST + EPI_WARPS);
+    // BN 192: 512 threads are launched with LAUNCH_REGS registers each; the four warps that feed give up what the
+    // others take (128 x FEED_REGS + 384 x EPI_REGS = 512 x LAUNCH_REGS)
+    static constexpr int LAUNCH_REGS = 128, FEED_REGS = 56, EPI_REGS = 152;
+    static constexpr bool MOVE_REGS = BN == 192;
+    static_assert(!MOVE_REGS || 32 * EPI_FIRST * FEED_REGS + 32 * EPI_WARPS * EPI_REGS == THREADS * LAUNCH_REGS, "");
+};
+// position in the ring of stages
+template <int N>
+struct Ring {
+    int i = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++i == N) {
+            i = 0;
+            phase ^= 1;
+        }
+    }
 };
 
 struct Fp8Args {
@@ -58,10 +80,12 @@ struct Fp8Args {
     unsigned *status;
     int X, M, G, N, K, KB, NB, ntn;
     int xbox;      // rows of an x copy (ungathered)
+    int yalign;    // bytes that rows of y are aligned to: 32, 16 or less
 };
 
 struct Ctl {
-    uint64_t full[6], empty[6], dfull[4], dempty[4], drain;
+    uint64_t full[6], done[6];   // a stage is loaded; its products are done (the stage is free, the sums are there)
+    uint64_t dempty[4], drain;   // a TMEM buffer is read
     uint32_t tmem;
     int abort;
     int goff[MOE_MAX_EXPERTS + 1];     // first place of each group, clamped
@@ -80,6 +104,8 @@ __device__ __forceinline__ void bar_expect(uint64_t *b, uint32_t bytes) {
 __device__ __forceinline__ void bar_arrive(uint64_t *b) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(sa(b)) : "memory");
 }
+// bits 16 .. 47 of the cycle counter
+__device__ __forceinline__ uint32_t clock_hi() { return (uint32_t)((unsigned long long)clock64() >> 16); }
 __device__ __forceinline__ bool bar_test(uint64_t *b, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -96,12 +122,14 @@ __device__ __forceinline__ bool elect() {
     return p != 0;
 }
 // wait for a phase; false once this block has given up (the first wait to run
-// out says so to the others and in the status word)
-__device__ __noinline__ bool bar_wait_slow(uint64_t *b, uint32_t parity, Ctl *c, unsigned *status) {
-    const long long t0 = clock64();
+// out says so to the others and in the status word).  Inline: a call would take
+// registers that the accumulating warps do not have.
+__device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, Ctl *c, unsigned *status) {
+    if (bar_test(b, parity)) return true;
+    const uint32_t t0 = clock_hi();
     while (!bar_test(b, parity)) {
         if (*(volatile int *)&c->abort) return false;
-        if (clock64() - t0 > FP8_WAIT_CYCLES) {
+        if (clock_hi() - t0 > FP8_WAIT) {
             *(volatile int *)&c->abort = 1;
             atomicOr(status, MOE_DEV_TIMEOUT);
             return false;
@@ -109,15 +137,12 @@ __device__ __noinline__ bool bar_wait_slow(uint64_t *b, uint32_t parity, Ctl *c,
     }
     return true;
 }
-__device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, Ctl *c, unsigned *status) {
-    return bar_test(b, parity) || bar_wait_slow(b, parity, c, status);
-}
 // wait on the way out of a block that has given up: for its own copies and
 // products in flight, bounded by itself
-__device__ __noinline__ void bar_settle(uint64_t *b, uint32_t parity) {
-    const long long t0 = clock64();
+__device__ __forceinline__ void bar_settle(uint64_t *b, uint32_t parity) {
+    const uint32_t t0 = clock_hi();
     while (!bar_test(b, parity))
-        if (clock64() - t0 > FP8_WAIT_CYCLES) return;
+        if (clock_hi() - t0 > FP8_WAIT) return;
 }
 __device__ __forceinline__ void tma_tile(void *dst, const CUtensorMap *m, int x, int y, uint64_t *bar) {
     asm volatile(
@@ -144,28 +169,24 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t ad, uint64_t bd, u
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(sa(bar)) : "memory");
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t v[16]) {
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t v[32]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15}, [%16];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
         : "r"(addr));
 }
-// waits for this thread's loads; the values pass through it, so that none is used before it
-__device__ __forceinline__ void tmem_ld_wait(uint32_t v[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
-                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
-                 ::"memory");
-}
+// waits for this thread's loads.  What uses their values is volatile too, so that it stays behind the wait.
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// acc (two fp32) += {lo, hi} * {s, s}
-__device__ __forceinline__ void fma2(uint64_t &acc, uint32_t lo, uint32_t hi, uint64_t ss) {
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(d), "l"(ss));
+// acc += d * s, staying behind the wait for d.  (The packed form of two values has the same rate here, and its
+// register pairs cost moves: 147 against 134 us at 8192 x 2048 x 7168.)
+__device__ __forceinline__ void fma1(float &acc, uint32_t d, float s) {
+    asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(acc) : "f"(__uint_as_float(d)), "f"(s));
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -212,46 +233,40 @@ __device__ __forceinline__ Tile tile_at(const Ctl *c, const Fp8Args &a, int t, i
     return r;
 }
 
-template <typename TY>
-__device__ __forceinline__ void store_cols(TY *y, const uint64_t *acc, int cols, bool vec);
-// 32 columns: whole 16-byte pieces where the row is aligned, one by one else
-template <>
-__device__ __forceinline__ void store_cols<float>(float *y, const uint64_t *acc, int cols, bool vec) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float4 v;
-        v.x = __uint_as_float((uint32_t)acc[2 * i]);
-        v.y = __uint_as_float((uint32_t)(acc[2 * i] >> 32));
-        v.z = __uint_as_float((uint32_t)acc[2 * i + 1]);
-        v.w = __uint_as_float((uint32_t)(acc[2 * i + 1] >> 32));
-        if (vec && 4 * i + 4 <= cols) {
-            *reinterpret_cast<float4 *>(y + 4 * i) = v;
-        } else {
-            if (4 * i < cols) y[4 * i] = v.x;
-            if (4 * i + 1 < cols) y[4 * i + 1] = v.y;
-            if (4 * i + 2 < cols) y[4 * i + 2] = v.z;
-            if (4 * i + 3 < cols) y[4 * i + 3] = v.w;
-        }
-    }
+// 32 columns of a row.  Pieces: 32 bytes a lane (whole sectors) where rows are
+// aligned to that, else 16, else value by value; a tile's last columns too.
+__device__ __forceinline__ void store32(void *p, const uint32_t w[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
 }
-template <>
-__device__ __forceinline__ void store_cols<__nv_bfloat16>(__nv_bfloat16 *y, const uint64_t *acc, int cols, bool vec) {
+template <typename TY>
+__device__ __forceinline__ void store_cols(TY *y, const float *acc, int cols, int align) {
+    constexpr int PER = 32 / (int)sizeof(TY);   // values of a 32-byte piece
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        __nv_bfloat162 h[4];
+    for (int i = 0; i < 32 / PER; ++i) {
+        uint32_t w[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint64_t v = acc[4 * i + j];
-            h[j] = __floats2bfloat162_rn(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+        for (int j = 0; j < 8; ++j) {
+            if constexpr (sizeof(TY) == 4) {
+                w[j] = __float_as_uint(acc[8 * i + j]);
+            } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(acc[16 * i + 2 * j], acc[16 * i + 2 * j + 1]);
+                w[j] = *reinterpret_cast<const uint32_t *>(&h);
+            }
         }
-        if (vec && 8 * i + 8 <= cols) {
-            const uint32_t *w = reinterpret_cast<const uint32_t *>(h);
-            *reinterpret_cast<uint4 *>(y + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+        TY *to = y + PER * i;
+        if (align >= 32 && PER * i + PER <= cols) {
+            store32(to, w);
+        } else if (align >= 16 && PER * i + PER <= cols) {
+            *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4 *>(to + PER / 2) = make_uint4(w[4], w[5], w[6], w[7]);
         } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (8 * i + 2 * j < cols) y[8 * i + 2 * j] = h[j].x;
-                if (8 * i + 2 * j + 1 < cols) y[8 * i + 2 * j + 1] = h[j].y;
+            for (int j = 0; j < PER; ++j) {
+                if (PER * i + j >= cols) break;
+                if constexpr (sizeof(TY) == 4) to[j] = __uint_as_float(w[j]);
+                else to[j] = __ushort_as_bfloat16((unsigned short)(w[j / 2] >> (16 * (j & 1))));
             }
         }
     }
@@ -269,20 +284,17 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::STAGES; ++i) {
-            bar_init(&c.full[i], a.rows ? 3 : 1);   // the w copy, and the two gathering warps
-            bar_init(&c.empty[i], 1);
+            bar_init(&c.full[i], a.rows ? 1 + GATHER_THREADS : 1);   // TMA's copies, and the gathered rows
+            bar_init(&c.done[i], 1);
         }
-        for (int i = 0; i < NBUF; ++i) {
-            bar_init(&c.dfull[i], 1);
-            bar_init(&c.dempty[i], S::EPI_WARPS);
-        }
+        for (int i = 0; i < NBUF; ++i) bar_init(&c.dempty[i], S::EPI_WARPS);
         bar_init(&c.drain, 1);
         c.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sa(&c.tmem)),
-                     "n"(NBUF * BN) : "memory");
+                     "n"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     if (!a.offsets) {
@@ -325,110 +337,110 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
     const int t0 = SPLIT ? (int)blockIdx.x / parts : (int)blockIdx.x, dt = SPLIT ? total : (int)gridDim.x;
     const int kb0 = SPLIT ? rank * a.KB / parts : 0, kb1 = SPLIT ? (rank + 1) * a.KB / parts : a.KB;
 
-    if (warp == 0) {
-        const uint32_t bytes = (a.rows ? 0 : a.xbox) * BK + S::B_BYTES;
-        int it = 0;
-        bool ok = true;
-        for (int t = t0; t < total && ok; t += dt) {
-            const Tile tl = tile_at(&c, a, t, BN);
-            const int wrow = __shfl_sync(0xFFFFFFFFu, tl.g * a.N + tl.n0, 0);
-            const int xrow = __shfl_sync(0xFFFFFFFFu, tl.first, 0);
-            for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                const int st = it % S::STAGES;
-                ok = bar_wait(&c.empty[st], ((it / S::STAGES) & 1) ^ 1, &c, a.status);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) break;
-                uint8_t *sx = stages + st * S::STAGE;
-                if (elect()) {
-                    bar_expect(&c.full[st], bytes);
-                    tma_tile(sx + S::A_BYTES, &mw, kb * BK, wrow, &c.full[st]);
-                    if (!a.rows) tma_tile(sx, &mx, kb * BK, xrow, &c.full[st]);
-                }
-                __syncwarp();
-            }
-        }
-        // copies in flight land, and their stages are handed back, before the block ends
-        for (int i = it > S::STAGES ? it - S::STAGES : 0; i < it; ++i)
-            bar_settle(ok ? &c.empty[i % S::STAGES] : &c.full[i % S::STAGES], (i / S::STAGES) & 1);
-        __syncwarp();
-    } else if (warp == 1) {
-        constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
-        int it = 0;
-        bool ok = true;
-        for (int t = t0; t < total && ok; t += dt) {
-            for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                const int st = it % S::STAGES, buf = it % NBUF;
-                ok = bar_wait(&c.dempty[buf], ((it / NBUF) & 1) ^ 1, &c, a.status) &&
-                     bar_wait(&c.full[st], (it / S::STAGES) & 1, &c, a.status);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) break;
-                fence_after();
-                const uint32_t sx = sa(stages) + st * S::STAGE;
-                const uint64_t ad = tile_desc(sx), bd = tile_desc(sx + S::A_BYTES);
-                if (elect()) {
-#pragma unroll
-                    for (int k = 0; k < BK / 32; ++k)   // 32 bytes of depth: 2 units of 16 bytes
-                        mma_e4m3(tmem + buf * BN, ad + 2 * k, bd + 2 * k, idesc, k);
-                    mma_commit(&c.empty[st]);
-                    mma_commit(&c.dfull[buf]);
-                }
-                __syncwarp();
-            }
-        }
-        if (!ok) {   // products in flight end before TMEM is freed
-            if (elect()) mma_commit(&c.drain);
-            __syncwarp();
-            bar_settle(&c.drain, 0);
-        }
-        __syncwarp();
-    } else if (warp < EPI_FIRST) {
-        if (a.rows) {
-            // thread: 16 bytes (piece pc) of rows r0, r0 + 8, ...; the swizzle moves piece p of row r to p ^ (r & 7)
-            const int id = threadIdx.x - 64, pc = id & 7, r0 = id >> 3;
-            const uint32_t to = sa(stages) + r0 * BK + ((pc ^ r0) << 4);
+    if (warp < EPI_FIRST) {
+        if (S::MOVE_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::FEED_REGS));
+        if (warp == 0) {
+            const uint32_t bytes = (a.rows ? 0 : a.xbox) * BK + S::B_BYTES;
+            Ring<S::STAGES> r;
             int it = 0;
             bool ok = true;
             for (int t = t0; t < total && ok; t += dt) {
                 const Tile tl = tile_at(&c, a, t, BN);
-                int row[BM / 8];
-#pragma unroll
-                for (int i = 0; i < BM / 8; ++i) {
-                    const int r = r0 + 8 * i < tl.rows ? a.rows[tl.first + r0 + 8 * i] : 0;
-                    row[i] = (unsigned)r < (unsigned)a.X ? r : 0;
-                }
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const int st = it % S::STAGES;
-                    ok = bar_wait(&c.empty[st], ((it / S::STAGES) & 1) ^ 1, &c, a.status);
+                const int wrow = __shfl_sync(0xFFFFFFFFu, tl.g * a.N + tl.n0, 0);
+                const int xrow = __shfl_sync(0xFFFFFFFFu, tl.first, 0);
+                for (int kb = kb0; kb < kb1; ++kb, ++it, r.next()) {
+                    ok = bar_wait(&c.done[r.i], r.phase ^ 1, &c, a.status);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
-                    const int at = kb * BK + 16 * pc;
-                    const uint32_t bytes = at < a.K ? 16 : 0;
-                    const uint8_t *src = a.x + (bytes ? at : 0);
-#pragma unroll
-                    for (int i = 0; i < BM / 8; ++i)
-                        if (r0 + 8 * i < tl.rows)
-                            copy16(to + st * S::STAGE + i * 8 * BK, src + (size_t)row[i] * a.K, bytes);
-                    asm volatile("cp.async.commit_group;" ::: "memory");
-                    if (it >= GATHER_LAG) {
-                        asm volatile("cp.async.wait_group %0;" ::"n"(GATHER_LAG) : "memory");
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                        if (lane == 0) bar_arrive(&c.full[(it - GATHER_LAG) % S::STAGES]);
+                    uint8_t *sx = stages + r.i * S::STAGE;
+                    if (elect()) {
+                        bar_expect(&c.full[r.i], bytes);
+                        tma_tile(sx + S::A_BYTES, &mw, kb * BK, wrow, &c.full[r.i]);
+                        if (!a.rows) tma_tile(sx, &mx, kb * BK, xrow, &c.full[r.i]);
                     }
+                    __syncwarp();
                 }
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            // copies in flight land, and their products end, before the block ends
+            for (int i = it > S::STAGES ? it - S::STAGES : 0; i < it; ++i)
+                bar_settle(ok ? &c.done[i % S::STAGES] : &c.full[i % S::STAGES], (i / S::STAGES) & 1);
             __syncwarp();
-            if (lane == 0)
-                for (int i = it > GATHER_LAG ? it - GATHER_LAG : 0; i < it; ++i) bar_arrive(&c.full[i % S::STAGES]);
+        } else if (warp == 1) {
+            constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+            Ring<S::STAGES> r;
+            Ring<NBUF> d;
+            bool ok = true;
+            for (int t = t0; t < total && ok; t += dt) {
+                for (int kb = kb0; kb < kb1; ++kb, r.next(), d.next()) {
+                    ok = bar_wait(&c.dempty[d.i], d.phase ^ 1, &c, a.status) && bar_wait(&c.full[r.i], r.phase, &c, a.status);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    // gathered rows were written through the generic proxy, and the wait made them visible here; the
+                    // products read through the async proxy
+                    if (a.rows) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    fence_after();
+                    const uint32_t sx = sa(stages) + r.i * S::STAGE;
+                    const uint64_t ad = tile_desc(sx), bd = tile_desc(sx + S::A_BYTES);
+                    if (elect()) {
+    #pragma unroll
+                        for (int k = 0; k < BK / 32; ++k)   // 32 bytes of depth: 2 units of 16 bytes
+                            mma_e4m3(tmem + d.i * BN, ad + 2 * k, bd + 2 * k, idesc, k);
+                        mma_commit(&c.done[r.i]);
+                    }
+                    __syncwarp();
+                }
+            }
+            if (!ok) {   // products in flight end before TMEM is freed
+                if (elect()) mma_commit(&c.drain);
+                __syncwarp();
+                bar_settle(&c.drain, 0);
+            }
+            __syncwarp();
+        } else {
+            if (a.rows) {
+                // thread: 16 bytes (piece pc) of rows r0, r0 + 8, ...; the swizzle moves piece p of row r to p ^ (r & 7)
+                const int id = threadIdx.x - 64, pc = id & 7, r0 = id >> 3;
+                const uint32_t to = sa(stages) + r0 * BK + ((pc ^ r0) << 4);
+                Ring<S::STAGES> r;
+                bool ok = true;
+                for (int t = t0; t < total && ok; t += dt) {
+                    const Tile tl = tile_at(&c, a, t, BN);
+                    const uint8_t *row[BM / 8];
+#pragma unroll
+                    for (int i = 0; i < BM / 8; ++i) {
+                        const int x = r0 + 8 * i < tl.rows ? a.rows[tl.first + r0 + 8 * i] : 0;
+                        row[i] = a.x + (size_t)((unsigned)x < (unsigned)a.X ? x : 0) * a.K;
+                    }
+                    const int nr = (tl.rows - r0 + 7) >> 3;   // of this thread
+                    for (int kb = kb0; kb < kb1; ++kb, r.next()) {
+                        ok = bar_wait(&c.done[r.i], r.phase ^ 1, &c, a.status);
+                        ok = __all_sync(0xFFFFFFFFu, ok);
+                        if (!ok) break;
+                        const bool in = kb * BK + 16 * pc < a.K;
+                        const uint32_t at = in ? kb * BK + 16 * pc : 0, bytes = in ? 16 : 0, dst = to + r.i * S::STAGE;
+                        if (nr == BM / 8) {
+#pragma unroll
+                            for (int i = 0; i < BM / 8; ++i) copy16(dst + i * 8 * BK, row[i] + at, bytes);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < BM / 8; ++i)
+                                if (i < nr) copy16(dst + i * 8 * BK, row[i] + at, bytes);
+                        }
+                        // this thread's arrival, once its copies have landed; nobody waits here for them
+                        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sa(&c.full[r.i])) : "memory");
+                    }
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+            }
         }
     } else {
+        if (S::MOVE_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::EPI_REGS));
         const int quad = warp & 3, part = (warp - EPI_FIRST) >> 2;   // TMEM lanes and columns of this warp
         const int lrow = 32 * quad + lane;
-        int it = 0;
+        Ring<S::STAGES> r;
+        Ring<NBUF> d;
         bool ok = true;
-        for (int t = t0; t < total && ok; t += dt) {
+        for (int t = t0; t < total; t += dt) {
             const Tile tl = tile_at(&c, a, t, BN);
             const int n0 = tl.n0 + part * HC;
             const bool mine = lrow < tl.rows;
@@ -445,80 +457,70 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
             }
             const float *xs = a.xs + (size_t)row * a.KB;
             const float *ws = a.ws + ((size_t)tl.g * a.NB + (work ? n0 / BK : 0)) * a.KB;
-            uint64_t acc[HC / 2];
+            float acc[HC];
 #pragma unroll
-            for (int i = 0; i < HC / 2; ++i) acc[i] = 0;
-            float nx = 0.f, nw = 0.f;
+            for (int i = 0; i < HC; ++i) acc[i] = 0.f;
+            float nx = 0.f, nw = 0.f, s = 0.f;
             if (work) {
                 nx = xs[kb0];
                 nw = ws[kb0];
             }
-            for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                const int buf = it % NBUF;
-                const float s = nx * nw;
-                if (work && kb + 1 < kb1) {
+            // Nothing in this loop hangs on whether a wait gave up: it ends by itself, its warps stay together,
+            // and nothing is stored.  Half of a block's columns is on its way while the other half is added.
+            uint32_t u[2][32];
+            const uint32_t at0 = tmem + part * HC + ((uint32_t)(32 * quad) << 16);
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (ok) ok = bar_wait(&c.done[r.i], r.phase, &c, a.status);
+                __syncwarp();
+                fence_after();
+                r.next();
+                if (!work) {
+                    if (lane == 0) bar_arrive(&c.dempty[d.i]);
+                    d.next();
+                    continue;
+                }
+                const uint32_t at = at0 + d.i * BN;
+                tmem_ld32(at, u[0]);
+                if (kb > kb0) {   // the block before this one
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) fma1(acc[32 + i], u[1][i], s);
+                }
+                s = nx * nw;
+                if (kb + 1 < kb1) {
                     nx = xs[kb + 1];
                     nw = ws[kb + 1];
                 }
-                ok = bar_wait(&c.dfull[buf], (it / NBUF) & 1, &c, a.status);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) break;
-                fence_after();
-                if (work) {
-                    uint64_t ss;
-                    asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "r"(__float_as_uint(s)));
-                    const uint32_t at = tmem + buf * BN + part * HC + ((uint32_t)(32 * quad) << 16);
-                    // Beside running products a load takes about 250 cycles, however much is on its way, so as
-                    // much is as the registers beside the sums hold: all 64 columns (BN 128), or the next 16
-                    // while 16 are added (BN 256).  The buffer goes back before the last columns are added.
-                    uint32_t u[S::AHEAD][16];
-                    if constexpr (S::AHEAD == 4) {
+                tmem_ld_wait();
+                tmem_ld32(at + 32, u[1]);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) tmem_ld16(at + 16 * j, u[j]);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) tmem_ld_wait(u[j]);
-                    } else {
-                        tmem_ld16(at, u[0]);
-                    }
-#pragma unroll
-                    for (int j = 0; j < HC / 16; ++j) {
-                        uint32_t *v = u[j % S::AHEAD];
-                        if constexpr (S::AHEAD == 2) {
-                            tmem_ld_wait(v);
-                            if (j + 1 < HC / 16) tmem_ld16(at + 16 * (j + 1), u[(j + 1) % 2]);
-                        }
-                        if (j == (S::AHEAD == 4 ? 0 : HC / 16 - 1)) {
-                            fence_before();
-                            if (lane == 0) bar_arrive(&c.dempty[buf]);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) fma2(acc[8 * j + i], v[2 * i], v[2 * i + 1], ss);
-                    }
-                } else if (lane == 0) {
-                    bar_arrive(&c.dempty[buf]);
-                }
+                for (int i = 0; i < 32; ++i) fma1(acc[i], u[0][i], s);
+                tmem_ld_wait();
+                fence_before();
+                if (lane == 0) bar_arrive(&c.dempty[d.i]);
+                d.next();
             }
-            if (!ok) break;
+            if (work) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) fma1(acc[32 + i], u[1][i], s);
+            }
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) continue;
             if (bad) {
 #pragma unroll
-                for (int i = 0; i < HC / 2; ++i) acc[i] = 0;
+                for (int i = 0; i < HC; ++i) acc[i] = 0.f;
             }
             if (SPLIT) {
                 // this block's part, over the stages (every copy and product is done)
                 float *red = reinterpret_cast<float *>(stages);
                 if (mine && work) {
 #pragma unroll
-                    for (int i = 0; i < HC / 2; ++i) {
-                        red[(part * HC + 2 * i) * RED_PITCH + lrow] = __uint_as_float((uint32_t)acc[i]);
-                        red[(part * HC + 2 * i + 1) * RED_PITCH + lrow] = __uint_as_float((uint32_t)(acc[i] >> 32));
-                    }
+                    for (int i = 0; i < HC; ++i) red[(part * HC + i) * RED_PITCH + lrow] = acc[i];
                 }
             } else if (mine && work) {
                 TY *y = static_cast<TY *>(a.y) + (size_t)(tl.first + lrow) * a.N + n0;
-                const bool vec = a.N % (16 / (int)sizeof(TY)) == 0;
 #pragma unroll
                 for (int j = 0; j < HC; j += 32)
-                    if (n0 + j < a.N) store_cols<TY>(y + j, acc + j / 2, a.N - n0 - j, vec);
+                    if (n0 + j < a.N) store_cols<TY>(y + j, acc + j, a.N - n0 - j, a.yalign);
             }
         }
     }
@@ -544,7 +546,7 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
     __syncthreads();
     if (warp == 1) {
         fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(NBUF * BN));
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512));
     }
 }
 
@@ -579,6 +581,14 @@ template <int BN, typename TY, bool SPLIT>
 cudaError_t launch_t(const CUtensorMap &mx, const CUtensorMap &mw, const Fp8Args &a, int grid, int split, cudaStream_t s) {
     constexpr int smem = Shape<BN>::SMEM;
     auto *k = fp8_kernel<BN, TY, SPLIT>;
+    if (Shape<BN>::MOVE_REGS) {
+        // the registers that warps pass on must be there, or they would wait for them without end
+        static const int regs = [&] {
+            cudaFuncAttributes at;
+            return cudaFuncGetAttributes(&at, k) == cudaSuccess ? at.numRegs : 0;
+        }();
+        if (regs != Shape<BN>::LAUNCH_REGS) return cudaErrorNotSupported;
+    }
     cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
@@ -602,20 +612,22 @@ cudaError_t launch_fp8_t(Fp8Args a, const void *x8, const void *w, int K, cudaSt
     // most 128-place tiles there can be: a group's last tile may be short
     const long long sms = num_sms();
     const long long mt = a.offsets ? (long long)(a.M / BM) + (a.G < a.M ? a.G : a.M) : (a.M + BM - 1) / BM;
-    const long long t128 = mt * ((a.N + 127) / 128), t256 = mt * ((a.N + 255) / 256);
-    if (t256 > 0x3FFFFFFF || t128 > 0x3FFFFFFF) return cudaErrorNotSupported;
+    const long long t128 = mt * ((a.N + 127) / 128), t192 = mt * ((a.N + 191) / 192);
+    if (t128 > 0x3FFFFFFF) return cudaErrorNotSupported;
     int split = 1;
     while (split < 8 && t128 * split * 2 <= sms && a.KB >= split * 4) split *= 2;
-    const bool wide = split == 1 && t256 >= sms && a.M >= 64 * mt;
+    const bool wide = split == 1 && t192 >= sms && a.M >= 64 * mt;
     CUtensorMap mx, mw;
     a.xbox = a.M >= BM || a.offsets ? BM : (a.M + 7) / 8 * 8;
+    const size_t rows_at = (size_t)(uintptr_t)a.y | ((size_t)a.N * sizeof(TY));
+    a.yalign = rows_at % 32 == 0 ? 32 : rows_at % 16 == 0 ? 16 : 0;
     if (!encode_fn()) return cudaErrorSymbolNotFound;
     if (!encode(&mx, x8, (size_t)a.X, (size_t)K, a.xbox) ||
-        !encode(&mw, w, (size_t)a.G * a.N, (size_t)K, wide ? 256 : 128))
+        !encode(&mw, w, (size_t)a.G * a.N, (size_t)K, wide ? 192 : 128))
         return cudaErrorInvalidValue;
-    a.ntn = wide ? (a.N + 255) / 256 : (a.N + 127) / 128;
+    a.ntn = wide ? (a.N + 191) / 192 : (a.N + 127) / 128;
     if (split > 1) return launch_t<128, TY, true>(mx, mw, a, (int)(t128 * split), split, s);
-    if (wide) return launch_t<256, TY, false>(mx, mw, a, (int)(t256 < sms ? t256 : sms), 1, s);
+    if (wide) return launch_t<192, TY, false>(mx, mw, a, (int)(t192 < sms ? t192 : sms), 1, s);
     return launch_t<128, TY, false>(mx, mw, a, (int)(t128 < sms ? t128 : sms), 1, s);
 }
 
