@@ -26,6 +26,7 @@
 #include <cuda_bf16.h>
 
 #include "moe_common.cuh"
+#include "moe_fp8.h"
 #include "moe_launch.h"
 
 namespace moe {
@@ -36,7 +37,8 @@ constexpr int BK = 128;             // bytes of depth of a stage (one scale bloc
 constexpr int EPI_FIRST = 4;        // first accumulating warp
 constexpr int HC = 64;              // columns of an accumulating warp
 constexpr int GATHER_THREADS = 64;  // warps 2 and 3
-constexpr int RED_PITCH = BM + 1;   // fp32 partial tiles, column by column
+constexpr int MAX_SPLIT = 8;        // blocks that share a tile's depth
+constexpr int RED_PITCH = BM + 4;   // fp32 partial tiles, column by column; 16-byte pieces free of bank conflicts
 // bound on every device-side wait, in units of 2^16 SM clock cycles (8e8 cycles: under a second)
 constexpr uint32_t FP8_WAIT = 12207;
 
@@ -70,17 +72,6 @@ struct Ring {
             phase ^= 1;
         }
     }
-};
-
-struct Fp8Args {
-    const uint8_t *x;
-    const float *xs, *ws;
-    const int32_t *rows, *offsets;
-    void *y;
-    unsigned *status;
-    int X, M, G, N, K, KB, NB, ntn;
-    int xbox;      // rows of an x copy (ungathered)
-    int yalign;    // bytes that rows of y are aligned to: 32, 16 or less
 };
 
 struct Ctl {
@@ -201,11 +192,12 @@ __device__ __forceinline__ uint32_t cluster_size() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
 }
-__device__ __forceinline__ float ld_peer(uint32_t addr, uint32_t rank) {
+__device__ __forceinline__ float4 ld_peer(uint32_t addr, uint32_t rank) {
     uint32_t at;
-    float v;
+    float4 v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
     return v;
 }
 
@@ -532,12 +524,27 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
             const Tile tl = tile_at(&c, a, t0, BN);
             const int C = BN / parts, c0 = rank * C;
             const uint32_t red = sa(stages);
-            for (int i = threadIdx.x - 32 * EPI_FIRST; i < tl.rows * C; i += S::EPI_WARPS * 32) {
-                const int col = c0 + i % C, r = i / C;
+            for (int i = threadIdx.x - 32 * EPI_FIRST; i < (tl.rows + 3) / 4 * C; i += S::EPI_WARPS * 32) {
+                const int col = c0 + i % C, r = i / C * 4;   // four rows of a column: all parts on their way, then added
+                float4 part[MAX_SPLIT];
+#pragma unroll
+                for (int p = 0; p < MAX_SPLIT; ++p)
+                    if (p < parts) part[p] = ld_peer(red + (col * RED_PITCH + r) * 4, p);
+                float4 v = part[0];
+#pragma unroll
+                for (int p = 1; p < MAX_SPLIT; ++p)
+                    if (p < parts) {
+                        v.x += part[p].x;
+                        v.y += part[p].y;
+                        v.z += part[p].z;
+                        v.w += part[p].w;
+                    }
                 if (tl.n0 + col >= a.N) continue;
-                float v = 0.f;
-                for (int p = 0; p < parts; ++p) v += ld_peer(red + (col * RED_PITCH + r) * 4, p);
-                static_cast<TY *>(a.y)[(size_t)(tl.first + r) * a.N + tl.n0 + col] = (TY)v;
+                TY *y = static_cast<TY *>(a.y) + (size_t)(tl.first + r) * a.N + tl.n0 + col;
+                y[0] = (TY)v.x;
+                if (r + 1 < tl.rows) y[(size_t)a.N] = (TY)v.y;
+                if (r + 2 < tl.rows) y[2 * (size_t)a.N] = (TY)v.z;
+                if (r + 3 < tl.rows) y[3 * (size_t)a.N] = (TY)v.w;
             }
         }
         cluster_sync();   // parts are read before their block ends
@@ -608,22 +615,22 @@ cudaError_t launch_t(const CUtensorMap &mx, const CUtensorMap &mw, const Fp8Args
 }
 
 template <typename TY>
-cudaError_t launch_fp8_t(Fp8Args a, const void *x8, const void *w, int K, cudaStream_t s) {
+cudaError_t launch_fp8_t(Fp8Args a, cudaStream_t s) {
     // most 128-place tiles there can be: a group's last tile may be short
     const long long sms = num_sms();
     const long long mt = a.offsets ? (long long)(a.M / BM) + (a.G < a.M ? a.G : a.M) : (a.M + BM - 1) / BM;
     const long long t128 = mt * ((a.N + 127) / 128), t192 = mt * ((a.N + 191) / 192);
     if (t128 > 0x3FFFFFFF) return cudaErrorNotSupported;
     int split = 1;
-    while (split < 8 && t128 * split * 2 <= sms && a.KB >= split * 4) split *= 2;
+    while (split < MAX_SPLIT && t128 * split * 2 <= sms && a.KB >= split * 4) split *= 2;
     const bool wide = split == 1 && t192 >= sms && a.M >= 64 * mt;
     CUtensorMap mx, mw;
     a.xbox = a.M >= BM || a.offsets ? BM : (a.M + 7) / 8 * 8;
     const size_t rows_at = (size_t)(uintptr_t)a.y | ((size_t)a.N * sizeof(TY));
     a.yalign = rows_at % 32 == 0 ? 32 : rows_at % 16 == 0 ? 16 : 0;
     if (!encode_fn()) return cudaErrorSymbolNotFound;
-    if (!encode(&mx, x8, (size_t)a.X, (size_t)K, a.xbox) ||
-        !encode(&mw, w, (size_t)a.G * a.N, (size_t)K, wide ? 192 : 128))
+    if (!encode(&mx, a.x, (size_t)a.X, (size_t)a.K, a.xbox) ||
+        !encode(&mw, a.w, (size_t)a.G * a.N, (size_t)a.K, wide ? 192 : 128))
         return cudaErrorInvalidValue;
     a.ntn = wide ? (a.N + 191) / 192 : (a.N + 127) / 128;
     if (split > 1) return launch_t<128, TY, true>(mx, mw, a, (int)(t128 * split), split, s);
@@ -638,6 +645,7 @@ cudaError_t launch_fp8(const void *x8, const float *x_scale, int X, const int32_
                        unsigned *status, cudaStream_t s) {
     Fp8Args a = {};
     a.x = static_cast<const uint8_t *>(x8);
+    a.w = static_cast<const uint8_t *>(w);
     a.xs = x_scale;
     a.ws = w_scale;
     a.rows = rows;
@@ -651,7 +659,8 @@ cudaError_t launch_fp8(const void *x8, const float *x_scale, int X, const int32_
     a.K = K;
     a.KB = (K + BK - 1) / BK;
     a.NB = (N + BK - 1) / BK;
-    return ydtype == MOE_DT_BF16 ? launch_fp8_t<__nv_bfloat16>(a, x8, w, K, s) : launch_fp8_t<float>(a, x8, w, K, s);
+    if (fp8_few_rows(a)) return launch_fp8_rows(a, ydtype, s);
+    return ydtype == MOE_DT_BF16 ? launch_fp8_t<__nv_bfloat16>(a, s) : launch_fp8_t<float>(a, s);
 }
 
 }  // namespace moe

@@ -50,7 +50,7 @@ def workspace():
 
 # one block of depth and less, ragged depth and width, every part count of a split depth, tiles of 128 and of 256
 # columns; places around the tile's 128
-DENSE = [(1, 8, 16), (1, 1, 128), (2, 7, 144), (1, 128, 512), (16, 2048, 7168), (1, 7168, 2048), (3, 136, 4096),
+DENSE = [(5, 24, 48), (8, 200, 4112), (9, 1000, 336), (15, 2051, 1008), (1, 8, 16), (1, 1, 128), (2, 7, 144), (1, 128, 512), (16, 2048, 7168), (1, 7168, 2048), (3, 136, 4096),
          (17, 100, 1040), (64, 512, 1024), (127, 257, 272), (128, 128, 128), (129, 384, 640), (130, 1000, 2880),
          (300, 2880, 2880), (333, 4000, 256), (1000, 1536, 4096), (2048, 2560, 272), (2500, 2051, 400),
          (2560, 2304, 1168)]
@@ -76,7 +76,7 @@ def sorted_rows(counts, X, g):
     return offs, rows
 
 
-GROUPED = [((1,), 16, 64), ((0, 3, 0, 1, 0), 100, 272), ((1, 1, 2, 1, 3), 256, 1024), ((128, 129, 0, 127), 384, 528),
+GROUPED = [((0, 9, 0, 4, 3), 328, 4112), ((0,) * 70 + (16,), 100, 208), ((1,), 16, 64), ((0, 3, 0, 1, 0), 100, 272), ((1, 1, 2, 1, 3), 256, 1024), ((128, 129, 0, 127), 384, 528),
            ((5, 0, 300, 1, 0, 0, 77, 260), 1000, 1040), ((700, 900, 0, 1300), 2050, 400), ((0,) * 40 + (2,), 136, 2048),
            (tuple(range(1, 60)), 264, 384)]
 
@@ -109,16 +109,22 @@ def test_grouped(counts, N, K, gathered, dtype):
 def test_rows_of_other_groups_and_columns_of_other_experts_do_not_leak():
     """a tile copies rows and columns past its group's: NaN codes there must stay there"""
     g = torch.Generator(device=DEV).manual_seed(5)
-    x, xs = states(200, 384, g)
+    for counts in ((70, 60, 70), (5, 3, 8)):
+        leaks_nothing(counts, g)
+
+
+def leaks_nothing(counts, g):
+    a, b, n = counts[0], counts[0] + counts[1], sum(counts)
+    x, xs = states(n, 384, g)
     w, ws = matrices(3, 200, 384, g)
-    x.view(torch.uint8)[70:130] = 0x7F                 # the middle group
+    x.view(torch.uint8)[a:b] = 0x7F                    # the middle group
     w.view(torch.uint8)[1] = 0xFF
-    offs = torch.tensor([0, 70, 130, 200], dtype=torch.int32, device=DEV)
-    y = torch.empty(200, 200, device=DEV)
+    offs = torch.tensor([0, a, b, n], dtype=torch.int32, device=DEV)
+    y = torch.empty(n, 200, device=DEV)
     moe.moe_fp8_matmul(x, xs, w, ws, y, workspace(), offsets=offs)
-    check(y[:70], *definition(x[:70], xs[:70], w[0], ws[0]), 384)
-    check(y[130:], *definition(x[130:], xs[130:], w[2], ws[2]), 384)
-    assert bool(torch.isnan(y[70:130]).all())
+    check(y[:a], *definition(x[:a], xs[:a], w[0], ws[0]), 384)
+    check(y[b:], *definition(x[b:], xs[b:], w[2], ws[2]), 384)
+    assert bool(torch.isnan(y[a:b]).all())
 
 
 def test_dense_rows_gathered_and_repeated():
@@ -130,6 +136,28 @@ def test_dense_rows_gathered_and_repeated():
     moe.moe_fp8_matmul(x, xs, w[0], ws[0], y, workspace(), rows=rows)
     check(y, *definition(x[rows.long()], xs[rows.long()], w[0], ws[0]), 640)
     assert torch.equal(y[1], y[2]) and torch.equal(y[0], y[6])
+
+
+def test_indexes_out_of_range_with_few_rows():
+    g = torch.Generator(device=DEV).manual_seed(17)
+    x, xs = states(6, 400, g)
+    w, ws = matrices(3, 136, 400, g)
+    w.view(torch.uint8)[1, 5] = 0x7F                  # a NaN weight: a bad row is zero all the same
+    rows = torch.tensor([0, 5, 6, 1, -1, 2, 3, 2 ** 31 - 1], dtype=torch.int32, device=DEV)
+    offs = torch.tensor([0, 2, 6, 8], dtype=torch.int32, device=DEV)
+    y, st = torch.full((8, 136), 7.0, device=DEV), workspace()
+    moe.moe_fp8_matmul(x, xs, w, ws, y, st, offsets=offs, rows=rows)
+    assert moe.moe_read_device_status(st) == moe.DEV_BAD_ROW
+    for i in (2, 4, 7):
+        assert bool((y[i] == 0).all())
+    check(y[:2], *definition(x[rows[:2].long()], xs[rows[:2].long()], w[0], ws[0]), 400)
+    check(y[6:7], *definition(x[3:4], xs[3:4], w[2], ws[2]), 400)
+    for bad in ([-4, 2, 6, 8], [0, 2, 6, 1000], [0, 5, 3, 8], [9, 9, 9, 9], [-9, -9, -9, -9]):
+        offs = torch.tensor(bad, dtype=torch.int32, device=DEV)
+        y = torch.full((10, 136), 7.0, device=DEV)
+        moe.moe_fp8_matmul(x, xs, w, ws, y[:8], st, offsets=offs, rows=rows.clamp(0, 5))
+        assert moe.moe_read_device_status(st) == moe.DEV_BAD_ROW, bad
+        assert bool((y[8:] == 7.0).all())
 
 
 @pytest.mark.parametrize("N,K", [(264, 272), (2600, 272)])
