@@ -466,7 +466,7 @@ size_t moe_balance_loss_workspace_bytes(int T, int E);
  * bits.  Other sizes (M, N, K, G) may split K in another way and round differently.
  * Row indexes and offsets outside their ranges are never followed (MOE_DEV_BAD_ROW).
  * Limits: X, M in [0, MOE_MAX_ROWS] (M == 0 is a no-op), 1 <= G <=
- * MOE_MAX_EXPERTS, 1 <= N <= 2^20, K % 16 == 0, 16 <= K <= 2^20, G*N <= 2^30.
+ * MOE_MAX_EXPERTS, 1 <= N <= 2^20, K % 16 == 0, 16 <= K <= 2^20, G*N <= 2^30, X*K <= 2^36.
  * Errors: MOE_ERR_INVALID_ARG for limits, types, a NULL buffer, X < M without
  * rows, X == 0, offsets missing with G > 1, or x8, w, y not 16-byte aligned
  * (scales, rows, offsets: 4); MOE_ERR_UNSUPPORTED for a K outside the rule

@@ -270,6 +270,7 @@ moe_status moe_fp8_matmul(const void *x8, const float *x_scale, int X, const int
         return MOE_ERR_INVALID_ARG;
     if (N < 1 || N > (1 << 20) || (long long)G * N > (1ll << 30) || !dtype_ok(ydtype)) return MOE_ERR_INVALID_ARG;
     if (K < 16 || K > (1 << 20) || K % 16) return MOE_ERR_UNSUPPORTED;
+    if ((long long)X * K > (1ll << 36)) return MOE_ERR_INVALID_ARG;
     if (!offsets && G != 1) return MOE_ERR_INVALID_ARG;
     if (M == 0) return MOE_OK;
     if (X == 0 || (!rows && X < M)) return MOE_ERR_INVALID_ARG;

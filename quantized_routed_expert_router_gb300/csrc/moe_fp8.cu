@@ -89,11 +89,16 @@ __device__ __forceinline__ uint32_t sa(const void *p) { return (uint32_t)__cvta_
 __device__ __forceinline__ void bar_init(uint64_t *b, uint32_t n) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(sa(b)), "r"(n) : "memory");
 }
-__device__ __forceinline__ void bar_expect(uint64_t *b, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(sa(b)), "r"(bytes) : "memory");
+__device__ __forceinline__ void bar_expect(uint64_t *b, uint32_t bytes, uint32_t me) {
+    asm volatile(
+        "{\n .reg .pred e;\n setp.ne.u32 e, %2, 0;\n @e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}" ::"r"(
+            sa(b)), "r"(bytes), "r"(me)
+        : "memory");
 }
-__device__ __forceinline__ void bar_arrive(uint64_t *b) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(sa(b)) : "memory");
+__device__ __forceinline__ void bar_arrive(uint64_t *b, uint32_t me) {
+    asm volatile("{\n .reg .pred e;\n setp.ne.u32 e, %1, 0;\n @e mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(sa(b)),
+                 "r"(me)
+                 : "memory");
 }
 // bits 16 .. 47 of the cycle counter
 __device__ __forceinline__ uint32_t clock_hi() { return (uint32_t)((unsigned long long)clock64() >> 16); }
@@ -104,13 +109,15 @@ __device__ __forceinline__ bool bar_test(uint64_t *b, uint32_t parity) {
         : "=r"(ok) : "r"(sa(b)), "r"(parity) : "memory");
     return ok != 0;
 }
-// one lane of a converged warp.  The single-thread instructions (copies, products,
-// commits) sit behind this inside loops that the whole warp runs: behind a
-// test of the lane number one stage's four products took 540-800 cycles to issue.
-__device__ __forceinline__ bool elect() {
+// 1 in one lane of a converged warp.  The single-thread instructions (copies,
+// products, commits, arrivals) are predicated on it in straight code that the
+// whole warp runs: a branch around them costs more than they do (a stage of
+// products took 540 cycles to issue behind a test of the lane number, 260 behind
+// a branch on this, 200 predicated).
+__device__ __forceinline__ uint32_t elect() {
     uint32_t p;
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
-    return p != 0;
+    return p;
 }
 // wait for a phase; false once this block has given up (the first wait to run
 // out says so to the others and in the status word).  Inline: a call would take
@@ -135,10 +142,11 @@ __device__ __forceinline__ void bar_settle(uint64_t *b, uint32_t parity) {
     while (!bar_test(b, parity))
         if (clock_hi() - t0 > FP8_WAIT) return;
 }
-__device__ __forceinline__ void tma_tile(void *dst, const CUtensorMap *m, int x, int y, uint64_t *bar) {
+__device__ __forceinline__ void tma_tile(void *dst, const CUtensorMap *m, int x, int y, uint64_t *bar, uint32_t me) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-            sa(dst)), "l"(m), "r"(x), "r"(y), "r"(sa(bar))
+        "{\n .reg .pred e;\n setp.ne.u32 e, %5, 0;\n"
+        " @e cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n}" ::"r"(
+            sa(dst)), "l"(m), "r"(x), "r"(y), "r"(sa(bar)), "r"(me)
         : "memory");
 }
 // 16 bytes, or 16 zeros where `bytes` is 0
@@ -151,14 +159,18 @@ __device__ __forceinline__ uint64_t tile_desc(uint32_t addr) {
     return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
            ((uint64_t)2 << 61);
 }
-__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t add) {
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t add, uint32_t me) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"(add)
+        "{\n .reg .pred e, p;\n setp.ne.u32 e, %5, 0;\n setp.ne.u32 p, %4, 0;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"(add),
+        "r"(me)
         : "memory");
 }
-__device__ __forceinline__ void mma_commit(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(sa(bar)) : "memory");
+__device__ __forceinline__ void mma_commit(uint64_t *bar, uint32_t me) {
+    asm volatile(
+        "{\n .reg .pred e;\n setp.ne.u32 e, %1, 0;\n"
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(sa(bar)), "r"(me)
+        : "memory");
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t v[32]) {
     asm volatile(
@@ -332,7 +344,7 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
     if (warp < EPI_FIRST) {
         if (S::MOVE_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::FEED_REGS));
         if (warp == 0) {
-            const uint32_t bytes = (a.rows ? 0 : a.xbox) * BK + S::B_BYTES;
+            const uint32_t bytes = (a.rows ? 0 : a.xbox) * BK + S::B_BYTES, me = elect();
             Ring<S::STAGES> r;
             int it = 0;
             bool ok = true;
@@ -345,12 +357,9 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                     uint8_t *sx = stages + r.i * S::STAGE;
-                    if (elect()) {
-                        bar_expect(&c.full[r.i], bytes);
-                        tma_tile(sx + S::A_BYTES, &mw, kb * BK, wrow, &c.full[r.i]);
-                        if (!a.rows) tma_tile(sx, &mx, kb * BK, xrow, &c.full[r.i]);
-                    }
-                    __syncwarp();
+                    bar_expect(&c.full[r.i], bytes, me);
+                    tma_tile(sx + S::A_BYTES, &mw, kb * BK, wrow, &c.full[r.i], me);
+                    if (!a.rows) tma_tile(sx, &mx, kb * BK, xrow, &c.full[r.i], me);
                 }
             }
             // copies in flight land, and their products end, before the block ends
@@ -359,6 +368,7 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
             __syncwarp();
         } else if (warp == 1) {
             constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+            const uint32_t me = elect();
             Ring<S::STAGES> r;
             Ring<NBUF> d;
             bool ok = true;
@@ -373,18 +383,14 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
                     fence_after();
                     const uint32_t sx = sa(stages) + r.i * S::STAGE;
                     const uint64_t ad = tile_desc(sx), bd = tile_desc(sx + S::A_BYTES);
-                    if (elect()) {
-    #pragma unroll
-                        for (int k = 0; k < BK / 32; ++k)   // 32 bytes of depth: 2 units of 16 bytes
-                            mma_e4m3(tmem + d.i * BN, ad + 2 * k, bd + 2 * k, idesc, k);
-                        mma_commit(&c.done[r.i]);
-                    }
-                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < BK / 32; ++k)   // 32 bytes of depth: 2 units of 16 bytes
+                        mma_e4m3(tmem + d.i * BN, ad + 2 * k, bd + 2 * k, idesc, k, me);
+                    mma_commit(&c.done[r.i], me);
                 }
             }
             if (!ok) {   // products in flight end before TMEM is freed
-                if (elect()) mma_commit(&c.drain);
-                __syncwarp();
+                mma_commit(&c.drain, me);
                 bar_settle(&c.drain, 0);
             }
             __syncwarp();
@@ -397,11 +403,11 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
                 bool ok = true;
                 for (int t = t0; t < total && ok; t += dt) {
                     const Tile tl = tile_at(&c, a, t, BN);
-                    const uint8_t *row[BM / 8];
+                    uint32_t row[BM / 8];   // in units of 16 bytes (X K <= 2^36)
 #pragma unroll
                     for (int i = 0; i < BM / 8; ++i) {
                         const int x = r0 + 8 * i < tl.rows ? a.rows[tl.first + r0 + 8 * i] : 0;
-                        row[i] = a.x + (size_t)((unsigned)x < (unsigned)a.X ? x : 0) * a.K;
+                        row[i] = (uint32_t)((unsigned)x < (unsigned)a.X ? x : 0) * (uint32_t)(a.K >> 4);
                     }
                     const int nr = (tl.rows - r0 + 7) >> 3;   // of this thread
                     for (int kb = kb0; kb < kb1; ++kb, r.next()) {
@@ -409,14 +415,15 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
                         ok = __all_sync(0xFFFFFFFFu, ok);
                         if (!ok) break;
                         const bool in = kb * BK + 16 * pc < a.K;
-                        const uint32_t at = in ? kb * BK + 16 * pc : 0, bytes = in ? 16 : 0, dst = to + r.i * S::STAGE;
+                        const uint8_t *src = a.x + (in ? kb * BK + 16 * pc : 0);
+                        const uint32_t bytes = in ? 16 : 0, dst = to + r.i * S::STAGE;
                         if (nr == BM / 8) {
 #pragma unroll
-                            for (int i = 0; i < BM / 8; ++i) copy16(dst + i * 8 * BK, row[i] + at, bytes);
+                            for (int i = 0; i < BM / 8; ++i) copy16(dst + i * 8 * BK, src + 16 * (uint64_t)row[i], bytes);
                         } else {
 #pragma unroll
                             for (int i = 0; i < BM / 8; ++i)
-                                if (i < nr) copy16(dst + i * 8 * BK, row[i] + at, bytes);
+                                if (i < nr) copy16(dst + i * 8 * BK, src + 16 * (uint64_t)row[i], bytes);
                         }
                         // this thread's arrival, once its copies have landed; nobody waits here for them
                         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sa(&c.full[r.i])) : "memory");
@@ -467,7 +474,7 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
                 fence_after();
                 r.next();
                 if (!work) {
-                    if (lane == 0) bar_arrive(&c.dempty[d.i]);
+                    bar_arrive(&c.dempty[d.i], lane == 0);
                     d.next();
                     continue;
                 }
@@ -488,7 +495,7 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
                 for (int i = 0; i < 32; ++i) fma1(acc[i], u[0][i], s);
                 tmem_ld_wait();
                 fence_before();
-                if (lane == 0) bar_arrive(&c.dempty[d.i]);
+                bar_arrive(&c.dempty[d.i], lane == 0);
                 d.next();
             }
             if (work) {

@@ -71,7 +71,7 @@ def test_balance_refusals(change, status):
     (dict(X=-1), INVALID), (dict(M=-1), INVALID), (dict(M=(1 << 24) + 1), INVALID), (dict(G=0), INVALID),
     (dict(G=1025), INVALID), (dict(N=0), INVALID), (dict(N=(1 << 20) + 1), INVALID), (dict(G=1024, N=1 << 20, offs=P), 0),
     (dict(G=1024, N=(1 << 20), M=4, offs=None), INVALID), (dict(K=0), UNSUP), (dict(K=24), UNSUP),
-    (dict(K=(1 << 20) + 16), UNSUP), (dict(yd=3), INVALID), (dict(G=2), INVALID), (dict(X=0), INVALID),
+    (dict(K=(1 << 20) + 16), UNSUP), (dict(X=1 << 17, K=1 << 20), INVALID), (dict(yd=3), INVALID), (dict(G=2), INVALID), (dict(X=0), INVALID),
     (dict(X=3), INVALID), (dict(x=None), INVALID), (dict(xs=None), INVALID), (dict(w=None), INVALID),
     (dict(wsc=None), INVALID), (dict(y=None), INVALID), (dict(x=P + 8), INVALID), (dict(w=P + 8), INVALID),
     (dict(y=P + 8), INVALID), (dict(xs=P + 2), INVALID), (dict(wsc=P + 2), INVALID), (dict(rows=P + 1), INVALID),
