@@ -381,7 +381,7 @@ moe_status moe_sum_partials(const float *parts, int R, size_t n, float *y, cudaS
  *                  inverse would overflow) has scale 0 and codes 0.
  * All outputs are written; apart from residual_out none may overlap an input.
  * Limits: T in [0, MOE_MAX_ROWS] (0 is a no-op); n % 16 == 0, 16 <= n <=
- * MOE_MAX_NORM_WIDTH; eps >= 0; |s| below 2^57 (squares are summed in fp32).
+ * MOE_MAX_NORM_WIDTH; eps > 0; |s| below 2^56 (squares are summed in fp32).
  * Errors: MOE_ERR_INVALID_ARG for limits, types, no output at all, x8 without
  * x8_scale or the reverse, a NULL input or a buffer that is not 16-byte aligned
  * (x8_scale: 4); MOE_ERR_UNSUPPORTED for a width outside the rules above.
@@ -404,7 +404,8 @@ moe_status moe_add_rmsnorm(const void *x, const void *residual, const float *wei
  *   pos     : device int32 [T][k] out: the sorted place of each pair, -1 for one
  *             that takes no part, or NULL
  *   ws      : device workspace of moe_expert_order_workspace_bytes(T, k, E)
- *             bytes, 16-byte aligned; needs no preparation (0 bytes: may be NULL)
+ *             bytes, 16-byte aligned; needs no preparation (0 bytes: may be
+ *             NULL).  Calls that may overlap on the GPU need one each.
  * Limits: T in [0, MOE_MAX_ROWS], 1 <= k <= MOE_MAX_K, T*k <= MOE_MAX_PAIRS,
  * 1 <= E <= MOE_MAX_EXPERTS.  T == 0 writes zero counts and offsets.
  * Errors: MOE_ERR_INVALID_ARG for limits, a NULL ids, a buffer that is not
@@ -422,8 +423,8 @@ size_t moe_expert_order_workspace_bytes(int T, int k, int E);
  * Even counts give alpha.  The counts carry no gradient:
  *   dloss/dlogits[t][e] = alpha k/N * p[t][e] (f_e - sum_j f_j p[t][j])
  * with f_e = E c_e / N, times (1 - sigma(l[t][e])) for sigmoid gating.
- *   logits    : device [T][E] of `dtype`.  -inf marks an expert that a token may
- *               not take (p = 0); a row of nothing but -inf adds nothing.
+ *   logits    : device [T][E] of `dtype`, finite or -inf.  -inf marks an expert that a
+ *               token may not take (p = 0); a row of nothing but -inf adds nothing.
  *   counts    : device int32 [E] >= 0 (moe_expert_order; with expert parallelism
  *               or several micro-batches, of all of them)
  *   valid     : device uint8 [T] or NULL: a token with 0 (padding) adds nothing
@@ -433,7 +434,8 @@ size_t moe_expert_order_workspace_bytes(int T, int k, int E);
  *   dlogits   : device [T][E] of `dtype` out, or NULL.  May be logits.
  *   ws        : device workspace of moe_balance_loss_workspace_bytes(T, E) bytes,
  *               16-byte aligned, zero-filled before its first use; every
- *               completed call leaves it ready for the next one
+ *               completed call leaves it ready for the next one.  Calls that
+ *               may overlap on the GPU (two captured graphs, too) need one each.
  * N == 0 gives loss 0 and gradient 0.  Sums run in a fixed order.
  * Limits: T in [0, MOE_MAX_ROWS] (0: loss 0), 1 <= E <= MOE_MAX_EXPERTS,
  * 1 <= k <= min(E, MOE_MAX_K).
@@ -470,7 +472,7 @@ size_t moe_balance_loss_workspace_bytes(int T, int E);
  * Errors: MOE_ERR_INVALID_ARG for limits, types, a NULL buffer, X < M without
  * rows, X == 0, offsets missing with G > 1, or x8, w, y not 16-byte aligned
  * (scales, rows, offsets: 4); MOE_ERR_UNSUPPORTED for a K outside the rule
- * above; MOE_ERR_WORKSPACE for a missing, short or unaligned ws.
+ * above or more than 2^30 tiles of 128 x 128; MOE_ERR_WORKSPACE for a missing, short or unaligned ws.
  */
 moe_status moe_fp8_matmul(const void *x8, const float *x_scale, int X, const int32_t *rows, int M,
                           const int32_t *offsets, int G, const void *w, const float *w_scale, int N, int K,

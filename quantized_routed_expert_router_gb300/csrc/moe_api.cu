@@ -207,7 +207,7 @@ moe_status moe_add_rmsnorm(const void *x, const void *residual, const float *wei
                            moe_dtype dtype, void *residual_out, void *y, moe_dtype ydtype, void *xq, void *x8,
                            float *x8_scale, cudaStream_t stream) {
     if (T < 0 || T > MOE_MAX_ROWS || !dtype_ok(dtype) || !dtype_ok(ydtype)) return MOE_ERR_INVALID_ARG;
-    if (!(eps >= 0.f) || isinf(eps)) return MOE_ERR_INVALID_ARG;
+    if (!(eps > 0.f) || isinf(eps)) return MOE_ERR_INVALID_ARG;
     if (n < 16 || n > MOE_MAX_NORM_WIDTH || n % 16 || (xq && !act_block(n))) return MOE_ERR_UNSUPPORTED;
     if (T == 0) return MOE_OK;
     if ((x8 == nullptr) != (x8_scale == nullptr)) return MOE_ERR_INVALID_ARG;

@@ -25,7 +25,7 @@ def test_sizes():
 @host_only
 @pytest.mark.parametrize("change,status", [
     (dict(T=-1), INVALID), (dict(T=(1 << 24) + 1), INVALID), (dict(n=0), UNSUP), (dict(n=24), UNSUP),
-    (dict(n=16400), UNSUP), (dict(dtype=2), INVALID), (dict(ydtype=-1), INVALID), (dict(eps=-1e-6), INVALID),
+    (dict(n=16400), UNSUP), (dict(dtype=2), INVALID), (dict(ydtype=-1), INVALID), (dict(eps=-1e-6), INVALID), (dict(eps=0.0), INVALID),
     (dict(eps=float("nan")), INVALID), (dict(eps=float("inf")), INVALID), (dict(x=None), INVALID),
     (dict(w=None), INVALID), (dict(x=P + 8), INVALID), (dict(r=P + 4), INVALID), (dict(y=P + 8), INVALID),
     (dict(x8=P), INVALID), (dict(sc=P), INVALID), (dict(x8=P + 8, sc=P), INVALID), (dict(x8=P, sc=P + 2), INVALID),
