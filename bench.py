@@ -108,9 +108,10 @@ def peaks():
 
 
 def csrc_hash():
+    """Hash of the sources that the layer kernels are compiled from."""
     h = hashlib.sha256()
     d = os.path.join(ROOT, "quantized_routed_expert_router_gb300", "csrc")
-    for f in sorted(os.listdir(d)):
+    for f in sorted(f for f in os.listdir(d) if f.startswith("moe_fused") or f in ("moe_common.cuh", "moe_launch.h")):
         with open(os.path.join(d, f), "rb") as fh:
             h.update(f.encode() + fh.read())
     return h.hexdigest()[:16]

@@ -5,6 +5,7 @@
 
 #include <initializer_list>
 
+#include "moe_around.h"
 #include "moe_common.cuh"
 #include "moe_launch.h"
 

@@ -25,8 +25,8 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include "moe_around.h"
 #include "moe_common.cuh"
-#include "moe_fp8.h"
 #include "moe_launch.h"
 
 namespace moe {

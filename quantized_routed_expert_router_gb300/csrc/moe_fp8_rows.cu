@@ -14,8 +14,8 @@
 // saves the tensor maps, the ring's start and the cluster's exchange.
 #include <cuda_bf16.h>
 
+#include "moe_around.h"
 #include "moe_common.cuh"
-#include "moe_fp8.h"
 #include "moe_launch.h"
 
 namespace moe {

@@ -112,19 +112,6 @@ cudaError_t launch_sum_partials(const float *parts, int R, size_t n, float *y, c
 cudaError_t launch_pack(const uint8_t *src, int qtype, int rows, int cols, uint8_t *dst, cudaStream_t s);
 cudaError_t launch_row_dots(const uint8_t *packed, int qtype, int cols, int row, const uint8_t *xq,
                             int32_t *out, cudaStream_t s);
-cudaError_t launch_norm(const void *x, const void *residual, const float *weight, float eps, int T, int n, int dtype,
-                        void *residual_out, void *y, int ydtype, uint8_t *xq, uint8_t *x8, float *x8_scale,
-                        cudaStream_t s);
-size_t order_ws_bytes(int T, int k, int E);
-cudaError_t launch_order(const int32_t *ids, int T, int k, int E, int32_t *counts, int32_t *offsets, int32_t *rows,
-                         int32_t *pos, void *ws, cudaStream_t s);
-size_t balance_ws_bytes();
-cudaError_t launch_balance(const void *logits, int dtype, const int32_t *counts, const uint8_t *valid, int T, int E,
-                           int k, int gating, float alpha, const float *grad_loss, float *loss, void *dlogits,
-                           void *ws, cudaStream_t s);
-cudaError_t launch_fp8(const void *x8, const float *x_scale, int X, const int32_t *rows, int M, const int32_t *offsets,
-                       int G, const void *w, const float *w_scale, int N, int K, void *y, int ydtype,
-                       unsigned *status, cudaStream_t s);
 // returns cudaErrorInvalidConfiguration if the shape needs more shared memory than a block has
 cudaError_t launch_ffn(const FfnArgs &a, cudaStream_t s);
 

@@ -13,6 +13,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
+#include "moe_around.h"
 #include "moe_common.cuh"
 #include "moe_launch.h"
 

@@ -3,6 +3,7 @@
 // balance loss with its gradient (moe_balance_loss).
 #include <cuda_bf16.h>
 
+#include "moe_around.h"
 #include "moe_launch.h"
 
 namespace moe {
