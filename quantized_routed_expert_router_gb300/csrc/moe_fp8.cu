@@ -11,10 +11,11 @@
 //   warp 0    : TMA copies of w tiles, and of x tiles where the rows are in
 //               order (128 bytes deep, 128-byte swizzle), into a ring of stages
 //   warp 1    : one thread issues the products into one of the TMEM buffers
-//   warps 2-3 : rows that are gathered, by 16-byte asynchronous copies
+//   warps 2-3 : rows that are gathered, by 16-byte asynchronous copies that
+//               signal the stage when they land
 //   warps 4.. : acc += (sx * sw) * D_b, 64 columns a warp.  TMEM gives lane i of
 //               the tile to thread i, so sx is one number a thread and sw one a
-//               warp: the scaling is one (packed) multiply-add a value
+//               warp: the scaling is one multiply-add (half a packed one) a value
 // A tile is 128 places of one group by BN columns.  Blocks beyond the ends of
 // x, w or K are zero-filled; rows of other groups that a tile happens to load
 // only reach accumulators that are not stored.
@@ -42,12 +43,13 @@ constexpr int RED_PITCH = BM + 4;   // fp32 partial tiles, column by column; 16-
 // bound on every device-side wait, in units of 2^16 SM clock cycles (8e8 cycles: under a second)
 constexpr uint32_t FP8_WAIT = 12207;
 
-// What bounds the widest tile is how the sums come back: a TMEM load beside
-// running products takes about 250 cycles however wide it is, so a warp wants
-// all of its 64 columns on their way at once, 64 registers beside its 64 sums.
-// 128 x 192 is the widest tile whose sums and loads fit the register file
-// (12 warps x 152 registers a thread); at 128 x 256 a warp had 16 columns on
-// their way and a block of depth took 950 cycles where its products take 512.
+// What bounds the tiles is how the sums come back: a TMEM load beside running
+// products takes about 250 cycles however wide it is, so a warp has all of its
+// 64 columns on their way at once, 64 registers beside its 64 sums.  128 x 192
+// is the widest tile whose sums and loads fit the register file (12 warps, 122
+// registers); at 128 x 256 a warp could have 16 columns on their way, and a block
+// of depth took 950 cycles where its products take 512.  Moving registers from
+// the feeding warps to the accumulating ones gained 1 to 3% and is not done.
 template <int BN>
 struct Shape {
     static constexpr int STAGES = BN == 192 ? 5 : 6;
@@ -55,11 +57,6 @@ struct Shape {
     static constexpr int SMEM = STAGES * STAGE + 1024;   // + alignment of the swizzle pattern
     static constexpr int NBUF = 512 / BN;                // TMEM buffers
     static constexpr int EPI_WARPS = 4 * (BN / HC), THREADS = 32 * (EPI_FIRST + EPI_WARPS);
-    // BN 192: 512 threads are launched with LAUNCH_REGS registers each; the four warps that feed give up what the
-    // others take (128 x FEED_REGS + 384 x EPI_REGS = 512 x LAUNCH_REGS)
-    static constexpr int LAUNCH_REGS = 128, FEED_REGS = 56, EPI_REGS = 152;
-    static constexpr bool MOVE_REGS = BN == 192;
-    static_assert(!MOVE_REGS || 32 * EPI_FIRST * FEED_REGS + 32 * EPI_WARPS * EPI_REGS == THREADS * LAUNCH_REGS, "");
 };
 // position in the ring of stages
 template <int N>
@@ -186,10 +183,14 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t v[32]) {
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// acc += d * s, staying behind the wait for d.  (The packed form of two values has the same rate here, and its
-// register pairs cost moves: 147 against 134 us at 8192 x 2048 x 7168.)
-__device__ __forceinline__ void fma1(float &acc, uint32_t d, float s) {
-    asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(acc) : "f"(__uint_as_float(d)), "f"(s));
+// two sums += {lo, hi} * {s, s}, staying behind the wait for lo and hi
+__device__ __forceinline__ void fma2(uint64_t &acc, uint32_t lo, uint32_t hi, uint64_t ss) {
+    asm volatile("{\n .reg .b64 d;\n mov.b64 d, {%1, %2};\n fma.rn.f32x2 %0, d, %3, %0;\n}"
+                 : "+l"(acc) : "r"(lo), "r"(hi), "l"(ss));
+}
+// sum i of a warp's packed ones
+__device__ __forceinline__ float sum_of(const uint64_t *acc, int i) {
+    return __uint_as_float((uint32_t)(acc[i / 2] >> (32 * (i & 1))));
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -245,7 +246,7 @@ __device__ __forceinline__ void store32(void *p, const uint32_t w[8]) {
                  : "memory");
 }
 template <typename TY>
-__device__ __forceinline__ void store_cols(TY *y, const float *acc, int cols, int align) {
+__device__ __forceinline__ void store_cols(TY *y, const uint64_t *acc, int cols, int align) {
     constexpr int PER = 32 / (int)sizeof(TY);   // values of a 32-byte piece
 #pragma unroll
     for (int i = 0; i < 32 / PER; ++i) {
@@ -253,9 +254,9 @@ __device__ __forceinline__ void store_cols(TY *y, const float *acc, int cols, in
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             if constexpr (sizeof(TY) == 4) {
-                w[j] = __float_as_uint(acc[8 * i + j]);
+                w[j] = __float_as_uint(sum_of(acc, 8 * i + j));
             } else {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(acc[16 * i + 2 * j], acc[16 * i + 2 * j + 1]);
+                const __nv_bfloat162 h = __floats2bfloat162_rn(sum_of(acc, 16 * i + 2 * j), sum_of(acc, 16 * i + 2 * j + 1));
                 w[j] = *reinterpret_cast<const uint32_t *>(&h);
             }
         }
@@ -342,7 +343,6 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
     const int kb0 = SPLIT ? rank * a.KB / parts : 0, kb1 = SPLIT ? (rank + 1) * a.KB / parts : a.KB;
 
     if (warp < EPI_FIRST) {
-        if (S::MOVE_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::FEED_REGS));
         if (warp == 0) {
             const uint32_t bytes = (a.rows ? 0 : a.xbox) * BK + S::B_BYTES, me = elect();
             Ring<S::STAGES> r;
@@ -433,7 +433,6 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
             }
         }
     } else {
-        if (S::MOVE_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::EPI_REGS));
         const int quad = warp & 3, part = (warp - EPI_FIRST) >> 2;   // TMEM lanes and columns of this warp
         const int lrow = 32 * quad + lane;
         Ring<S::STAGES> r;
@@ -456,70 +455,61 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
             }
             const float *xs = a.xs + (size_t)row * a.KB;
             const float *ws = a.ws + ((size_t)tl.g * a.NB + (work ? n0 / BK : 0)) * a.KB;
-            float acc[HC];
+            uint64_t acc[HC / 2];
 #pragma unroll
-            for (int i = 0; i < HC; ++i) acc[i] = 0.f;
-            float nx = 0.f, nw = 0.f, s = 0.f;
+            for (int i = 0; i < HC / 2; ++i) acc[i] = 0;
+            float nx = 0.f, nw = 0.f;
             if (work) {
                 nx = xs[kb0];
                 nw = ws[kb0];
             }
             // Nothing in this loop hangs on whether a wait gave up: it ends by itself, its warps stay together,
-            // and nothing is stored.  Half of a block's columns is on its way while the other half is added.
-            uint32_t u[2][32];
+            // and nothing is stored.  What need not come after the sums stands between their load and the wait for it.
             const uint32_t at0 = tmem + part * HC + ((uint32_t)(32 * quad) << 16);
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (ok) ok = bar_wait(&c.done[r.i], r.phase, &c, a.status);
                 __syncwarp();
                 fence_after();
                 r.next();
-                if (!work) {
+                if (work) {
+                    // all 64 columns on their way at once; the buffer goes back before they are added
+                    uint32_t u[2][32];
+                    tmem_ld32(at0 + d.i * BN, u[0]);
+                    tmem_ld32(at0 + d.i * BN + 32, u[1]);
+                    uint64_t ss;
+                    asm volatile("mov.b64 %0, {%1, %1};" : "=l"(ss) : "r"(__float_as_uint(nx * nw)));
+                    if (kb + 1 < kb1) {
+                        nx = xs[kb + 1];
+                        nw = ws[kb + 1];
+                    }
+                    tmem_ld_wait();
+                    fence_before();
                     bar_arrive(&c.dempty[d.i], lane == 0);
-                    d.next();
-                    continue;
-                }
-                const uint32_t at = at0 + d.i * BN;
-                tmem_ld32(at, u[0]);
-                if (kb > kb0) {   // the block before this one
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) fma1(acc[32 + i], u[1][i], s);
+                    for (int i = 0; i < 32; ++i) fma2(acc[i], u[i / 16][2 * (i % 16)], u[i / 16][2 * (i % 16) + 1], ss);
+                } else {
+                    bar_arrive(&c.dempty[d.i], lane == 0);
                 }
-                s = nx * nw;
-                if (kb + 1 < kb1) {
-                    nx = xs[kb + 1];
-                    nw = ws[kb + 1];
-                }
-                tmem_ld_wait();
-                tmem_ld32(at + 32, u[1]);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) fma1(acc[i], u[0][i], s);
-                tmem_ld_wait();
-                fence_before();
-                bar_arrive(&c.dempty[d.i], lane == 0);
                 d.next();
-            }
-            if (work) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) fma1(acc[32 + i], u[1][i], s);
             }
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) continue;
             if (bad) {
 #pragma unroll
-                for (int i = 0; i < HC; ++i) acc[i] = 0.f;
+                for (int i = 0; i < HC / 2; ++i) acc[i] = 0;
             }
             if (SPLIT) {
                 // this block's part, over the stages (every copy and product is done)
                 float *red = reinterpret_cast<float *>(stages);
                 if (mine && work) {
 #pragma unroll
-                    for (int i = 0; i < HC; ++i) red[(part * HC + i) * RED_PITCH + lrow] = acc[i];
+                    for (int i = 0; i < HC; ++i) red[(part * HC + i) * RED_PITCH + lrow] = sum_of(acc, i);
                 }
             } else if (mine && work) {
                 TY *y = static_cast<TY *>(a.y) + (size_t)(tl.first + lrow) * a.N + n0;
 #pragma unroll
                 for (int j = 0; j < HC; j += 32)
-                    if (n0 + j < a.N) store_cols<TY>(y + j, acc + j, a.N - n0 - j, a.yalign);
+                    if (n0 + j < a.N) store_cols<TY>(y + j, acc + j / 2, a.N - n0 - j, a.yalign);
             }
         }
     }
@@ -595,14 +585,6 @@ template <int BN, typename TY, bool SPLIT>
 cudaError_t launch_t(const CUtensorMap &mx, const CUtensorMap &mw, const Fp8Args &a, int grid, int split, cudaStream_t s) {
     constexpr int smem = Shape<BN>::SMEM;
     auto *k = fp8_kernel<BN, TY, SPLIT>;
-    if (Shape<BN>::MOVE_REGS) {
-        // the registers that warps pass on must be there, or they would wait for them without end
-        static const int regs = [&] {
-            cudaFuncAttributes at;
-            return cudaFuncGetAttributes(&at, k) == cudaSuccess ? at.numRegs : 0;
-        }();
-        if (regs != Shape<BN>::LAUNCH_REGS) return cudaErrorNotSupported;
-    }
     cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
