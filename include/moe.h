@@ -73,8 +73,8 @@ typedef enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1 } moe_dtype;
 #define MOE_DEV_TIMEOUT 0x4u      /* a bounded wait in moe_layer_forward or moe_fp8_matmul gave up:
                                      y is invalid, zero the workspace before the next call */
 #define MOE_DEV_BAD_ROW 0x8u      /* moe_fp8_matmul: a row index outside x (that row of y is zero) or
-                                     offsets that fall or leave [0, M] (they are taken as the nearest
-                                     end of that range)                                         */
+                                     offsets that fall or leave [0, M] (rows of those groups are left
+                                     out or computed with one group or another)                 */
 
 /* Limits of this build. */
 #define MOE_MAX_TOKENS 16          /* T per call (small-batch decode)        */

@@ -2,7 +2,8 @@
 
 Argument marshalling only: every step of the path runs in the CUDA library
 ``_moe.so`` (C ABI, ``include/moe.h``); this module passes tensor addresses,
-sizes and the current CUDA stream through ctypes.  PyTorch supplies device
+sizes and the current CUDA stream through ctypes (the calls around the experts:
+through ``_calls.so``, a compiled binding of the same ABI).  PyTorch supplies device
 memory and streams.  Importing works without a GPU; the library must have
 been built (``_build.build()``) - there is no fallback path.
 """
@@ -263,51 +264,20 @@ def moe_sum_partials(parts, y, stream=None):
 
 # --------------------------------------------------- around the experts
 #
-# These calls check shapes, types, devices and layouts here (ValueError) and run
-# on the device that holds the tensors, on its current stream unless one is given.
+# These calls check shapes, types, layouts and devices of their tensors (ValueError, csrc/binding.cpp) and run on
+# the device that holds them, on its current stream unless one is given.
 
-_DT = {torch.float32: DT_F32, torch.bfloat16: DT_BF16}
-_E4M3 = (torch.float8_e4m3fn, torch.uint8)
-
-
-def _expect(name, t, shape, dtypes, dev):
-    """t is a contiguous tensor of this shape and one of these types on device `dev`; None passes."""
-    if t is not None and (t.dtype not in dtypes or t.shape != shape or not t.is_contiguous() or t.get_device() != dev):
-        raise ValueError(f"{name}: want a contiguous {' or '.join(map(str, dtypes))} tensor {tuple(shape)} on device "
-                         f"{dev}, got {t.dtype} {tuple(t.shape)}{'' if t.is_contiguous() else ', not contiguous,'} on "
-                         f"device {t.get_device()}")
+_bound = None
 
 
-def _ws(ws, dev):
-    """(address, bytes) of a workspace; it lies where the inputs lie"""
-    if ws is None:
-        return None, 0
-    if ws.get_device() != dev or not ws.is_contiguous():
-        raise ValueError(f"ws: want a contiguous tensor on device {dev}")
-    return ws.data_ptr(), ws.nbytes
-
-
-def _launch(call: str, dev: int, args, stream):
-    """the library's `call` with the tensors' device current, on its current stream unless one is given"""
-    if dev < 0:
-        raise ValueError(f"{call}: tensors must be on a CUDA device")
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(dev)   # current_stream(dev).cuda_stream without the object
-    elif stream.device_index != dev:
-        raise ValueError(f"{call}: the stream belongs to another device than the tensors")
-    else:
-        handle = stream.cuda_stream
-    fn = getattr(_lib_handle or lib(), call)
-    if dev == torch.cuda.current_device():
-        s = fn(*args, handle)
-    else:
-        with torch.cuda.device(dev):
-            s = fn(*args, handle)
-    if s:
-        raise MoeError(s, call)
-
-
-_F32, _I32, _F32_BF16 = (torch.float32,), (torch.int32,), (torch.float32, torch.bfloat16)
+def _native():
+    """The compiled binding of the calls below.  Raises if the library has not been built."""
+    global _bound
+    if _bound is None:
+        lib()
+        from . import _calls
+        _bound = _calls
+    return _bound
 
 
 def moe_add_rmsnorm(x, residual, weight, eps: float, residual_out=None, y=None, xq=None, x8=None, x8_scale=None,
@@ -317,23 +287,9 @@ def moe_add_rmsnorm(x, residual, weight, eps: float, residual_out=None, y=None, 
     x, residual, residual_out (s; may be x or residual): [T, n] fp32 or bf16.  y (v): [T, n] fp32 or bf16.
     xq: q8 records of v (device_bytes(T * moe_q8_row_bytes(n))).  x8, x8_scale: e4m3 [T, n] and its fp32
     scales [T, ceil(n / 128)].  Give the outputs that are wanted."""
-    if x.dim() != 2 or x.dtype not in _DT or not x.is_contiguous():
-        raise ValueError("x: want a contiguous fp32 or bf16 tensor [T, n]")
-    shape, dev = x.shape, x.get_device()
-    T, n = shape
-    same = (x.dtype,)
-    _expect("residual", residual, shape, same, dev)
-    _expect("weight", weight, (n,), _F32, dev)
-    _expect("residual_out", residual_out, shape, same, dev)
-    _expect("y", y, shape, _F32_BF16, dev)
-    _expect("x8", x8, shape, _E4M3, dev)
-    _expect("x8_scale", x8_scale, (T, -(-n // FP8_GROUP)), _F32, dev)
-    if xq is not None and (xq.get_device() != dev or not xq.is_contiguous() or
-                           xq.nbytes < T * moe_q8_row_bytes(n)):
-        raise ValueError(f"xq: want at least {T} x {moe_q8_row_bytes(n)} contiguous bytes on device {dev}")
-    _launch("moe_add_rmsnorm", dev,
-            (x.data_ptr(), _ptr(residual), _ptr(weight), eps, T, n, _DT[x.dtype], _ptr(residual_out), _ptr(y),
-             DT_F32 if y is None else _DT[y.dtype], _ptr(xq), _ptr(x8), _ptr(x8_scale)), stream)
+    s = (_bound or _native()).add_rmsnorm(x, residual, weight, eps, residual_out, y, xq, x8, x8_scale, stream)
+    if s:
+        raise MoeError(s, "moe_add_rmsnorm")
 
 
 def moe_expert_order_workspace_bytes(T: int, k: int, E: int) -> int:
@@ -344,16 +300,9 @@ def moe_expert_order(ids, E: int, ws=None, counts=None, offsets=None, rows=None,
     """The (token, slot) pairs of ids [T, k] sorted by expert: counts [E], offsets [E + 1], the token of each
     sorted place rows [T * k] (-1 past the last) and the sorted place of each pair pos [T, k] (-1: takes no
     part, its id is not in [0, E)).  All int32; give the outputs that are wanted."""
-    if ids.dim() != 2 or ids.dtype != torch.int32 or not ids.is_contiguous():
-        raise ValueError("ids: want a contiguous int32 tensor [T, k]")
-    shape, dev = ids.shape, ids.get_device()
-    T, k = shape
-    _expect("counts", counts, (E,), _I32, dev)
-    _expect("offsets", offsets, (E + 1,), _I32, dev)
-    _expect("rows", rows, (T * k,), _I32, dev)
-    _expect("pos", pos, shape, _I32, dev)
-    _launch("moe_expert_order", dev,
-            (ids.data_ptr(), T, k, E, _ptr(counts), _ptr(offsets), _ptr(rows), _ptr(pos), *_ws(ws, dev)), stream)
+    s = (_bound or _native()).expert_order(ids, E, ws, counts, offsets, rows, pos, stream)
+    if s:
+        raise MoeError(s, "moe_expert_order")
 
 
 def moe_balance_loss_workspace_bytes(T: int, E: int) -> int:
@@ -365,18 +314,9 @@ def moe_balance_loss(logits, counts, k: int, gating: int, alpha: float, ws, loss
     """The balance loss alpha * sum_e (E c_e / N)(mean p_e) of logits [T, E] (fp32 or bf16) and counts [E]
     (moe_expert_order) into loss [1], and grad_loss [1] times its gradient into dlogits [T, E]; either may be
     None.  valid: uint8 or bool [T], 0 for padded tokens."""
-    if logits.dim() != 2 or logits.dtype not in _DT or not logits.is_contiguous():
-        raise ValueError("logits: want a contiguous fp32 or bf16 tensor [T, E]")
-    shape, dev = logits.shape, logits.get_device()
-    T, E = shape
-    _expect("counts", counts, (E,), _I32, dev)
-    _expect("valid", valid, (T,), (torch.uint8, torch.bool), dev)
-    _expect("grad_loss", grad_loss, (1,), _F32, dev)
-    _expect("loss", loss, (1,), _F32, dev)
-    _expect("dlogits", dlogits, shape, (logits.dtype,), dev)
-    _launch("moe_balance_loss", dev,
-            (logits.data_ptr(), _DT[logits.dtype], _ptr(counts), _ptr(valid), T, E, k, gating, alpha, _ptr(grad_loss),
-             _ptr(loss), _ptr(dlogits), *_ws(ws, dev)), stream)
+    s = (_bound or _native()).balance_loss(logits, counts, k, gating, alpha, ws, loss, dlogits, valid, grad_loss, stream)
+    if s:
+        raise MoeError(s, "moe_balance_loss")
 
 
 def moe_fp8_matmul_workspace_bytes() -> int:
@@ -388,24 +328,11 @@ def moe_fp8_matmul(x8, x_scale, w, w_scale, y, ws, offsets=None, rows=None, stre
 
     x8 [X, K] e4m3, x_scale [X, ceil(K/128)] fp32; w [N, K] or [G, N, K] e4m3, w_scale [ceil(N/128),
     ceil(K/128)] or [G, ...] fp32; y [M, N] fp32 or bf16.  offsets int32 [G + 1]: the places of y of each
-    group (moe_expert_order); rows int32 [M]: the row of x8 of each place (None: the place itself)."""
-    if x8.dim() != 2 or x8.dtype not in _E4M3 or not x8.is_contiguous():
-        raise ValueError("x8: want a contiguous e4m3 tensor [X, K]")
-    if w.dim() not in (2, 3) or y.dim() != 2:
-        raise ValueError("w: want [N, K] or [G, N, K]; y: [M, N]")
-    (X, K), dev = x8.shape, x8.get_device()
-    lead = w.shape[:-2]
-    N, M, G = w.shape[-2], y.shape[0], lead[0] if lead else 1
-    kb, nb = -(-K // FP8_GROUP), -(-N // FP8_GROUP)
-    _expect("x_scale", x_scale, (X, kb), _F32, dev)
-    _expect("w", w, (*lead, N, K), _E4M3, dev)
-    _expect("w_scale", w_scale, (*lead, nb, kb), _F32, dev)
-    _expect("y", y, (M, N), _F32_BF16, dev)
-    _expect("offsets", offsets, (G + 1,), _I32, dev)
-    _expect("rows", rows, (M,), _I32, dev)
-    _launch("moe_fp8_matmul", dev,
-            (x8.data_ptr(), _ptr(x_scale), X, _ptr(rows), M, _ptr(offsets), G, w.data_ptr(), _ptr(w_scale),
-             N, K, y.data_ptr(), _DT[y.dtype], *_ws(ws, dev)), stream)
+    group (moe_expert_order); rows int32 [M]: the row of x8 of each place (None: the place itself).  e4m3
+    tensors are torch.float8_e4m3fn or uint8."""
+    s = (_bound or _native()).fp8_matmul(x8, x_scale, w, w_scale, y, ws, offsets, rows, stream)
+    if s:
+        raise MoeError(s, "moe_fp8_matmul")
 
 
 def moe_debug_set_exchange_wait(cycles: int):

@@ -1,13 +1,16 @@
-"""Build the CUDA library (_moe.so) in-tree for sm_103a with nvcc.
+"""Build the CUDA library (_moe.so) in-tree for sm_103a with nvcc, and the
+torch binding of the calls around the experts (_calls.so) with g++.
 
 Translation units compile in parallel; the link step produces one shared
-object exporting the C ABI of include/moe.h.
+object exporting the C ABI of include/moe.h.  _calls.so is a Python extension
+that links against it.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import os
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -15,6 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 SO = os.path.join(PKG, "_moe.so")
+CALLS_SO = os.path.join(PKG, "_calls.so")
 SOURCES = ["moe_api.cu", "moe_kernels.cu", "moe_ffn.cu", "moe_noalloc.cu", "moe_fused_api.cu",
            "moe_fused_q4k.cu", "moe_fused_q2k.cu", "moe_fused_q80.cu", "moe_fused_mx4.cu", "moe_fused_q6k.cu",
            "moe_fused_q3k.cu", "moe_norm.cu", "moe_router_stats.cu", "moe_fp8.cu",
@@ -36,10 +40,37 @@ def _deps() -> list[str]:
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(SO):
+    if not os.path.exists(SO) or not os.path.exists(CALLS_SO):
         return False
-    t = os.path.getmtime(SO)
+    t = min(os.path.getmtime(SO), os.path.getmtime(CALLS_SO))
     return all(os.path.getmtime(f) <= t for f in _deps())
+
+
+def _compile_binding() -> str:
+    """binding.cpp against torch's headers; a host object, no CUDA code"""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"), INCLUDE]
+    obj = os.path.join(OUT_DIR, "binding.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{p}" for p in inc), "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = CALLS_SO + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, SO, f"-L{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the binding failed:\n{r.stderr}")
+    os.replace(tmp, CALLS_SO)
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
@@ -60,14 +91,17 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
             print(r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(compile_one, SOURCES))
+        binding = binding.result()
     tmp = SO + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"]
+    cmd = [nvcc, *ARCH, "-shared", "-Xlinker", "-soname,_moe.so", "-o", tmp, *objs, "-lcudart"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, SO)
+    _link_binding(binding)
     return SO
 
 

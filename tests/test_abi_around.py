@@ -100,3 +100,27 @@ def test_the_binding_checks_tensors_before_the_call():
     with pytest.raises(ValueError, match="x_scale"):
         moe.moe_fp8_matmul(x.to(torch.float8_e4m3fn), torch.zeros(2, 2), torch.zeros(8, 64, dtype=torch.float8_e4m3fn),
                            torch.zeros(1, 1), torch.zeros(2, 8), torch.zeros(256, dtype=torch.uint8))
+
+
+def test_the_binding_refuses_what_is_no_tensor_or_number():
+    torch = pytest.importorskip("torch")
+    x, w, y = torch.zeros(2, 64), torch.ones(64), torch.zeros(2, 64)
+    with pytest.raises(ValueError, match="x: want a tensor"):
+        moe.moe_add_rmsnorm([1.0], None, w, 1e-6, y=y)
+    with pytest.raises(ValueError, match="y: want a tensor or None"):
+        moe.moe_add_rmsnorm(x, None, w, 1e-6, y=3)
+    with pytest.raises(TypeError):
+        moe.moe_add_rmsnorm(x, None, w, "small", y=y)
+    ids = torch.zeros(2, 4, dtype=torch.int32)
+    for E in (2 ** 40, 2 ** 70):
+        with pytest.raises((ValueError, OverflowError)):
+            moe.moe_expert_order(ids, E)
+    with pytest.raises(TypeError):
+        moe.moe_expert_order(ids, None)
+    with pytest.raises(ValueError, match="contiguous"):
+        moe.moe_add_rmsnorm(x, None, w, 1e-6, y=torch.zeros(64, 2).t())
+    with pytest.raises(TypeError, match="arguments"):
+        moe._native().add_rmsnorm(x)
+    with pytest.raises(ValueError, match="w: want"):
+        moe.moe_fp8_matmul(x.to(torch.float8_e4m3fn), torch.zeros(2, 1), torch.zeros(8), torch.zeros(1, 1), y,
+                           torch.zeros(256, dtype=torch.uint8))

@@ -170,6 +170,14 @@ def test_captured_and_on_another_stream():
     assert torch.equal(y, want)
 
 
+def test_a_stream_is_a_stream():
+    x, r, w = make(2, 64, torch.float32, 1)
+    y = torch.full_like(x, 7.0)
+    with pytest.raises(AttributeError):
+        moe.moe_add_rmsnorm(x, r, w, 1e-6, y=y, stream=5)
+    assert bool((y == 7.0).all())
+
+
 def test_refusals_leave_outputs_alone():
     x, r, w = make(2, 64, torch.float32, 1)
     y = torch.full_like(x, 7.0)
