@@ -57,6 +57,8 @@ struct Shape {
     static constexpr int SMEM = STAGES * STAGE + 1024;   // + alignment of the swizzle pattern
     static constexpr int NBUF = 512 / BN;                // TMEM buffers
     static constexpr int EPI_WARPS = 4 * (BN / HC), THREADS = 32 * (EPI_FIRST + EPI_WARPS);
+    // a split tile's part and the sums of a block's share lie over the stages
+    static_assert(4 * (BN * RED_PITCH + BM * (BN / 2 + 4)) <= STAGES * STAGE, "");
 };
 // position in the ring of stages
 template <int N>
@@ -274,6 +276,25 @@ __device__ __forceinline__ void store_cols(TY *y, const uint64_t *acc, int cols,
                 else to[j] = __ushort_as_bfloat16((unsigned short)(w[j / 2] >> (16 * (j & 1))));
             }
         }
+    }
+}
+
+// 4 columns of a row, of which `cols` are there
+template <typename TY>
+__device__ __forceinline__ void store4(TY *y, float4 v, int cols, bool aligned) {
+    if (aligned && cols >= 4) {
+        if constexpr (sizeof(TY) == 4) {
+            *reinterpret_cast<float4 *>(y) = v;
+        } else {
+            const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+            *reinterpret_cast<uint2 *>(y) =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+        }
+    } else {
+        if (cols > 0) y[0] = (TY)v.x;
+        if (cols > 1) y[1] = (TY)v.y;
+        if (cols > 2) y[2] = (TY)v.z;
+        if (cols > 3) y[3] = (TY)v.w;
     }
 }
 
@@ -517,31 +538,50 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
         __syncwarp();
         cluster_sync();
         if (warp >= EPI_FIRST && t0 < total && !*(volatile int *)&c.abort) {
-            // each block adds its share of the columns over the cluster, in rank order
+            // Each block adds its share of the columns over the cluster, in rank order: a warp a column, four rows a
+            // lane (512 bytes of a part in a piece: with columns side by side a tile of 128 rows in 8 parts took 6 us
+            // to add), then from its own shared memory to y with columns side by side.
             const Tile tl = tile_at(&c, a, t0, BN);
-            const int C = BN / parts, c0 = rank * C;
-            const uint32_t red = sa(stages);
-            for (int i = threadIdx.x - 32 * EPI_FIRST; i < (tl.rows + 3) / 4 * C; i += S::EPI_WARPS * 32) {
-                const int col = c0 + i % C, r = i / C * 4;   // four rows of a column: all parts on their way, then added
-                float4 part[MAX_SPLIT];
+            const int lc = 31 - __clz(BN / parts), C = 1 << lc, c0 = rank * C;   // parts: a power of two
+            const int pitch = C + 4;
+            const uint32_t red = sa(stages) + (c0 * RED_PITCH + 4 * lane) * 4;
+            float *sum = reinterpret_cast<float *>(stages) + BN * RED_PITCH;
+            // (two columns at a time; otherwise short code, as it runs once, from a cold cache)
+#pragma unroll 1
+            for (int col = warp - EPI_FIRST; col < C; col += 2 * S::EPI_WARPS) {
+                if (4 * lane >= tl.rows) continue;
+                float4 part[2][MAX_SPLIT];
 #pragma unroll
-                for (int p = 0; p < MAX_SPLIT; ++p)
-                    if (p < parts) part[p] = ld_peer(red + (col * RED_PITCH + r) * 4, p);
-                float4 v = part[0];
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int p = 1; p < MAX_SPLIT; ++p)
-                    if (p < parts) {
-                        v.x += part[p].x;
-                        v.y += part[p].y;
-                        v.z += part[p].z;
-                        v.w += part[p].w;
-                    }
-                if (tl.n0 + col >= a.N) continue;
-                TY *y = static_cast<TY *>(a.y) + (size_t)(tl.first + r) * a.N + tl.n0 + col;
-                y[0] = (TY)v.x;
-                if (r + 1 < tl.rows) y[(size_t)a.N] = (TY)v.y;
-                if (r + 2 < tl.rows) y[2 * (size_t)a.N] = (TY)v.z;
-                if (r + 3 < tl.rows) y[3 * (size_t)a.N] = (TY)v.w;
+                    for (int p = 0; p < MAX_SPLIT; ++p)
+                        if (p < parts) part[h][p] = ld_peer(red + (col + h * S::EPI_WARPS) * RED_PITCH * 4, p);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float4 v = part[h][0];
+#pragma unroll
+                    for (int p = 1; p < MAX_SPLIT; ++p)
+                        if (p < parts) {
+                            v.x += part[h][p].x;
+                            v.y += part[h][p].y;
+                            v.z += part[h][p].z;
+                            v.w += part[h][p].w;
+                        }
+                    float *to = sum + 4 * lane * pitch + col + h * S::EPI_WARPS;
+                    to[0] = v.x;
+                    to[pitch] = v.y;
+                    to[2 * pitch] = v.z;
+                    to[3 * pitch] = v.w;
+                }
+            }
+            asm volatile("bar.sync 1, %0;" ::"n"(S::EPI_WARPS * 32) : "memory");   // the accumulating warps
+            TY *y = static_cast<TY *>(a.y) + (size_t)tl.first * a.N + tl.n0 + c0;
+            const int cols = min(C, a.N - tl.n0 - c0);
+#pragma unroll 1
+            for (int i = 4 * (threadIdx.x - 32 * EPI_FIRST); i < tl.rows << lc; i += 4 * S::EPI_WARPS * 32) {
+                const int r = i >> lc, col = i & (C - 1);
+                const float4 v = *reinterpret_cast<const float4 *>(sum + r * pitch + col);
+                store4(y + (size_t)r * a.N + col, v, cols - col, a.yalign >= 16);
             }
         }
         cluster_sync();   // parts are read before their block ends

@@ -50,7 +50,7 @@ def workspace():
 
 # one block of depth and less, ragged depth and width, every part count of a split depth, tiles of 128 and of 256
 # columns; places around the tile's 128
-DENSE = [(5, 24, 48), (8, 200, 4112), (9, 1000, 336), (15, 2051, 1008), (1, 8, 16), (1, 1, 128), (2, 7, 144), (1, 128, 512), (16, 2048, 7168), (1, 7168, 2048), (3, 136, 4096),
+DENSE = [(100, 333, 2048), (70, 1026, 4096), (40, 136, 8192), (21, 130, 1536), (5, 24, 48), (8, 200, 4112), (9, 1000, 336), (15, 2051, 1008), (1, 8, 16), (1, 1, 128), (2, 7, 144), (1, 128, 512), (16, 2048, 7168), (1, 7168, 2048), (3, 136, 4096),
          (17, 100, 1040), (64, 512, 1024), (127, 257, 272), (128, 128, 128), (129, 384, 640), (130, 1000, 2880),
          (300, 2880, 2880), (333, 4000, 256), (1000, 1536, 4096), (2048, 2560, 272), (2500, 2051, 400),
          (2560, 2304, 1168)]
