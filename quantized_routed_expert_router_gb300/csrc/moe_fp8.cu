@@ -20,9 +20,9 @@
 // x, w or K are zero-filled; rows of other groups that a tile happens to load
 // only reach accumulators that are not stored.
 //
-// Large products are persistent blocks, one an SM, over the tiles (BN 192).
-// When there are fewer tiles than SMs, a cluster of S blocks splits the depth of
-// a tile and adds its parts through distributed shared memory in rank order.
+// Large products are persistent blocks, one an SM, over the tiles.  When there
+// are too few tiles for the SMs, a cluster of S blocks splits the depth of a
+// tile and adds its parts through distributed shared memory in rank order.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -240,8 +240,8 @@ __device__ __forceinline__ Tile tile_at(const Ctl *c, const Fp8Args &a, int t, i
     return r;
 }
 
-// 32 columns of a row.  Pieces: 32 bytes a lane (whole sectors) where rows are
-// aligned to that, else 16, else value by value; a tile's last columns too.
+// 32 columns of a row of which `align` bytes are aligned, 32 or 16: 32 bytes a lane
+// (whole sectors) or 16; a tile's last columns value by value.
 __device__ __forceinline__ void store32(void *p, const uint32_t w[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
                  "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
@@ -265,7 +265,7 @@ __device__ __forceinline__ void store_cols(TY *y, const uint64_t *acc, int cols,
         TY *to = y + PER * i;
         if (align >= 32 && PER * i + PER <= cols) {
             store32(to, w);
-        } else if (align >= 16 && PER * i + PER <= cols) {
+        } else if (PER * i + PER <= cols) {
             *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
             *reinterpret_cast<uint4 *>(to + PER / 2) = make_uint4(w[4], w[5], w[6], w[7]);
         } else {
@@ -275,6 +275,39 @@ __device__ __forceinline__ void store_cols(TY *y, const uint64_t *acc, int cols,
                 if constexpr (sizeof(TY) == 4) to[j] = __uint_as_float(w[j]);
                 else to[j] = __ushort_as_bfloat16((unsigned short)(w[j / 2] >> (16 * (j & 1))));
             }
+        }
+    }
+}
+
+// The sums of a warp where rows of y are not aligned to 16 bytes (an odd N): 32 rows
+// by 8 words at a time turn in shared memory and leave value by value, columns side
+// by side.  Straight from the lanes each store touched 32 rows: 3221 x 6993 x 768
+// took 219 us, and takes 49.
+constexpr int TURN_PITCH = 9;   // words, free of bank conflicts
+template <typename TY>
+__device__ __forceinline__ void store_turned(TY *y, size_t N, const uint64_t *acc, int rows, int cols, uint32_t *turn,
+                                             int lane) {
+    constexpr int PER = 32 / (int)sizeof(TY);   // values of a row's 8 words
+#pragma unroll
+    for (int i = 0; i < HC / PER; ++i) {
+        if (PER * i >= cols) break;
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if constexpr (sizeof(TY) == 4) {
+                turn[TURN_PITCH * lane + j] = __float_as_uint(sum_of(acc, 8 * i + j));
+            } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(sum_of(acc, 16 * i + 2 * j), sum_of(acc, 16 * i + 2 * j + 1));
+                turn[TURN_PITCH * lane + j] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+        }
+        __syncwarp();
+        const int col = lane % PER;
+        if (PER * i + col < cols) {
+#pragma unroll 4
+            for (int r = lane / PER; r < 32; r += 32 / PER)
+                if (r < rows)
+                    y[r * N + PER * i + col] = reinterpret_cast<const TY *>(turn + TURN_PITCH * r)[col];
         }
     }
 }
@@ -298,18 +331,19 @@ __device__ __forceinline__ void store4(TY *y, float4 v, int cols, bool aligned) 
     }
 }
 
-template <int BN, typename TY, bool SPLIT>
+template <int BN, typename TY, bool SPLIT, bool TURN>
 __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
     fp8_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw, const Fp8Args a) {
     using S = Shape<BN>;
-    constexpr int THREADS = S::THREADS, NBUF = S::NBUF;
+    constexpr int THREADS = S::THREADS, NBUF = S::NBUF, STAGES = S::STAGES - (TURN ? 1 : 0);
+    static_assert(!TURN || 4 * 32 * TURN_PITCH * S::EPI_WARPS <= S::STAGE, "");
     extern __shared__ uint8_t raw[];
     __shared__ Ctl c;
     uint8_t *stages = raw + ((1024 - (sa(raw) & 1023)) & 1023);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < S::STAGES; ++i) {
+        for (int i = 0; i < STAGES; ++i) {
             bar_init(&c.full[i], a.rows ? 1 + GATHER_THREADS : 1);   // TMA's copies, and the gathered rows
             bar_init(&c.done[i], 1);
         }
@@ -366,7 +400,7 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
     if (warp < EPI_FIRST) {
         if (warp == 0) {
             const uint32_t bytes = (a.rows ? 0 : a.xbox) * BK + S::B_BYTES, me = elect();
-            Ring<S::STAGES> r;
+            Ring<STAGES> r;
             int it = 0;
             bool ok = true;
             for (int t = t0; t < total && ok; t += dt) {
@@ -384,13 +418,13 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
                 }
             }
             // copies in flight land, and their products end, before the block ends
-            for (int i = it > S::STAGES ? it - S::STAGES : 0; i < it; ++i)
-                bar_settle(ok ? &c.done[i % S::STAGES] : &c.full[i % S::STAGES], (i / S::STAGES) & 1);
+            for (int i = it > STAGES ? it - STAGES : 0; i < it; ++i)
+                bar_settle(ok ? &c.done[i % STAGES] : &c.full[i % STAGES], (i / STAGES) & 1);
             __syncwarp();
         } else if (warp == 1) {
             constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
             const uint32_t me = elect();
-            Ring<S::STAGES> r;
+            Ring<STAGES> r;
             Ring<NBUF> d;
             bool ok = true;
             for (int t = t0; t < total && ok; t += dt) {
@@ -420,7 +454,7 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
                 // thread: 16 bytes (piece pc) of rows r0, r0 + 8, ...; the swizzle moves piece p of row r to p ^ (r & 7)
                 const int id = threadIdx.x - 64, pc = id & 7, r0 = id >> 3;
                 const uint32_t to = sa(stages) + r0 * BK + ((pc ^ r0) << 4);
-                Ring<S::STAGES> r;
+                Ring<STAGES> r;
                 bool ok = true;
                 for (int t = t0; t < total && ok; t += dt) {
                     const Tile tl = tile_at(&c, a, t, BN);
@@ -456,7 +490,7 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
     } else {
         const int quad = warp & 3, part = (warp - EPI_FIRST) >> 2;   // TMEM lanes and columns of this warp
         const int lrow = 32 * quad + lane;
-        Ring<S::STAGES> r;
+        Ring<STAGES> r;
         Ring<NBUF> d;
         bool ok = true;
         for (int t = t0; t < total; t += dt) {
@@ -526,6 +560,14 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < HC; ++i) red[(part * HC + i) * RED_PITCH + lrow] = sum_of(acc, i);
                 }
+            } else if (TURN) {
+                // in shared memory beside the stages in use
+                if (work)
+                    store_turned<TY>(static_cast<TY *>(a.y) + (size_t)(tl.first + 32 * quad) * a.N + n0, (size_t)a.N, acc,
+                                     tl.rows - 32 * quad, a.N - n0,
+                                     reinterpret_cast<uint32_t *>(stages + STAGES * S::STAGE) +
+                                         (warp - EPI_FIRST) * 32 * TURN_PITCH,
+                                     lane);
             } else if (mine && work) {
                 TY *y = static_cast<TY *>(a.y) + (size_t)(tl.first + lrow) * a.N + n0;
 #pragma unroll
@@ -621,10 +663,10 @@ bool encode(CUtensorMap *m, const void *p, size_t rows, size_t depth, int box) {
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, typename TY, bool SPLIT>
+template <int BN, typename TY, bool SPLIT, bool TURN>
 cudaError_t launch_t(const CUtensorMap &mx, const CUtensorMap &mw, const Fp8Args &a, int grid, int split, cudaStream_t s) {
     constexpr int smem = Shape<BN>::SMEM;
-    auto *k = fp8_kernel<BN, TY, SPLIT>;
+    auto *k = fp8_kernel<BN, TY, SPLIT, TURN>;
     cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
@@ -650,8 +692,15 @@ cudaError_t launch_fp8_t(Fp8Args a, cudaStream_t s) {
     const long long mt = a.offsets ? (long long)(a.M / BM) + (a.G < a.M ? a.G : a.M) : (a.M + BM - 1) / BM;
     const long long t128 = mt * ((a.N + 127) / 128), t192 = mt * ((a.N + 191) / 192);
     if (t128 > 0x3FFFFFFF) return cudaErrorNotSupported;
+    // Depth in parts while all parts still have an SM of their own and 4 blocks of depth.  Whole tiles leave SMs idle
+    // and each takes a whole depth's time (us in parts, and whole): 256 x 2048 x 7168 11.5, 21.6; 64 x 2048 x 7168
+    // 14.2, 21.4; 512 x 1000 x 4096 9.7, 15.1.  At the shallow end, 64 x 7168 x 2048, it is 9.1 and 8.7.
     int split = 1;
     while (split < MAX_SPLIT && t128 * split * 2 <= sms && a.KB >= split * 4) split *= 2;
+    // 192 columns where that leaves a tile for every SM and the tiles are at least half full on average: fewer reads of x
+    // and w a product.  us with 192, and with 128: 8192 x 2048 x 7168 118, 136; 8192 x 7168 x 2048 131, 149; 128 experts
+    // of 1536 x 4096, 65536 rows 498, 565; 32 of 2880 x 2880, 4096 rows 65, 77.  Below the bounds: 1024 x 2048 x 7168
+    // (88 tiles) 25.7, 21.8; 256 experts of 512 x 2048, 16384 rows 57.9, 54.5; but 128 of 1536 x 4096, 6216 rows 136, 145.
     const bool wide = split == 1 && t192 >= sms && a.M >= 64 * mt;
     CUtensorMap mx, mw;
     a.xbox = a.M >= BM || a.offsets ? BM : (a.M + 7) / 8 * 8;
@@ -662,9 +711,11 @@ cudaError_t launch_fp8_t(Fp8Args a, cudaStream_t s) {
         !encode(&mw, a.w, (size_t)a.G * a.N, (size_t)a.K, wide ? 192 : 128))
         return cudaErrorInvalidValue;
     a.ntn = wide ? (a.N + 191) / 192 : (a.N + 127) / 128;
-    if (split > 1) return launch_t<128, TY, true>(mx, mw, a, (int)(t128 * split), split, s);
-    if (wide) return launch_t<192, TY, false>(mx, mw, a, (int)(t192 < sms ? t192 : sms), 1, s);
-    return launch_t<128, TY, false>(mx, mw, a, (int)(t128 < sms ? t128 : sms), 1, s);
+    if (split > 1) return launch_t<128, TY, true, false>(mx, mw, a, (int)(t128 * split), split, s);
+    const int grid = (int)(wide ? (t192 < sms ? t192 : sms) : (t128 < sms ? t128 : sms));
+    if (a.yalign < 16)
+        return wide ? launch_t<192, TY, false, true>(mx, mw, a, grid, 1, s) : launch_t<128, TY, false, true>(mx, mw, a, grid, 1, s);
+    return wide ? launch_t<192, TY, false, false>(mx, mw, a, grid, 1, s) : launch_t<128, TY, false, false>(mx, mw, a, grid, 1, s);
 }
 
 }  // namespace

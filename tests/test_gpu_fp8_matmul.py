@@ -69,6 +69,23 @@ def test_dense(M, N, K, dtype):
     assert bool((y[M] == 7.0).all()) and moe.moe_read_device_status(st) == 0
 
 
+# rows of y that start off a 16-byte boundary: tiles of 128 columns, of 192, depth in parts, last tiles of 1 to 191 columns
+@pytest.mark.parametrize("M,N,K", [(1000, 1283, 400), (1001, 1409, 272), (2500, 2052, 400), (2497, 2305, 272),
+                                   (2500, 2111, 144), (200, 515, 1040)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_unaligned_rows(M, N, K, dtype):
+    g = torch.Generator(device=DEV).manual_seed(M + N + K)
+    x, xs = states(M, K, g)
+    w, ws = matrices(1, N, K, g)
+    room = torch.full((M * N + 16,), 7.0, dtype=dtype, device=DEV)
+    y = room[8:8 + M * N].view(M, N)
+    st = workspace()
+    moe.moe_fp8_matmul(x, xs, w[0], ws[0], y, st)
+    check(y, *definition(x, xs, w[0], ws[0]), K)
+    assert bool((room[:8] == 7.0).all()) and bool((room[8 + M * N:] == 7.0).all())
+    assert moe.moe_read_device_status(st) == 0
+
+
 def sorted_rows(counts, X, g):
     """offsets and random rows for these group sizes"""
     offs = torch.tensor([0] + list(torch.tensor(counts).cumsum(0)), dtype=torch.int32, device=DEV)
