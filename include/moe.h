@@ -378,7 +378,8 @@ moe_status moe_sum_partials(const float *parts, int R, size_t n, float *y, cudaS
  *                  neither: per group of 128 values (the last one may be short)
  *                  amax = max|v|, scale = amax/448, code = e4m3(v * (448/amax)),
  *                  nearest, ties to even.  A group with amax < 2^-119 (the
- *                  inverse would overflow) has scale 0 and codes 0.
+ *                  inverse would overflow) has scale 0 and codes 0; one that holds
+ *                  a NaN has scale NaN and codes NaN.
  * All outputs are written; apart from residual_out none may overlap an input.
  * Limits: T in [0, MOE_MAX_ROWS] (0 is a no-op); n % 16 == 0, 16 <= n <=
  * MOE_MAX_NORM_WIDTH; eps > 0; |s| below 2^56 (squares are summed in fp32).
@@ -425,6 +426,7 @@ size_t moe_expert_order_workspace_bytes(int T, int k, int E);
  * with f_e = E c_e / N, times (1 - sigma(l[t][e])) for sigmoid gating.
  *   logits    : device [T][E] of `dtype`, finite or -inf.  -inf marks an expert that a
  *               token may not take (p = 0); a row of nothing but -inf adds nothing.
+ *               A NaN makes its row's gradient and the loss NaN.
  *   counts    : device int32 [E] >= 0 (moe_expert_order; with expert parallelism
  *               or several micro-batches, of all of them)
  *   valid     : device uint8 [T] or NULL: a token with 0 (padding) adds nothing

@@ -60,16 +60,23 @@ __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16 *p, const fl
 // smallest maximum whose inverse 448/amax is finite with room to spare
 constexpr float kFp8MinAmax = 0x1p-119f;
 
-// e4m3 codes of a lane's 8 values, the scale shared by its 16 lanes
+// (a NaN is the larger one)
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+
+// e4m3 codes of a lane's 8 values, the scale shared by its 16 lanes.  A NaN stays one in the scale and its codes.
 __device__ __forceinline__ void fp8_store8(const float v[8], bool active, int e0, uint8_t *row, float *scale,
                                            int lane) {
     float am = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) am = fmaxf(am, fabsf(v[i]));
+    for (int i = 0; i < 8; ++i) am = max_nan(am, fabsf(v[i]));
 #pragma unroll
-    for (int off = 8; off >= 1; off >>= 1) am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, off));
+    for (int off = 8; off >= 1; off >>= 1) am = max_nan(am, __shfl_xor_sync(0xFFFFFFFFu, am, off));
     float d = 0.f, inv = 0.f;
-    if (am >= kFp8MinAmax) {
+    if (!(am < kFp8MinAmax)) {
         d = __fdiv_rn(am, 448.f);
         inv = __fdiv_rn(448.f, am);
     }

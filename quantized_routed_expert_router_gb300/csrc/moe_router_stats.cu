@@ -233,9 +233,15 @@ __device__ __forceinline__ float warp_sum(float v) {
     for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
     return v;
 }
+// maxima to which a NaN is the largest: a row with one is not taken for a row of nothing but -inf
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
 __device__ __forceinline__ float warp_max(float v) {
     float m;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
     return m;
 }
 
@@ -338,7 +344,7 @@ __global__ void __launch_bounds__(32 * kBalanceWarps, balance_per_sm(VEC * J)) b
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
                     p[j][i] = e < E ? next[j].value(i) : -INFINITY;
-                    m = fmaxf(m, p[j][i]);
+                    m = max_nan(m, p[j][i]);
                 }
             }
         }

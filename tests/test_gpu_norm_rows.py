@@ -195,3 +195,24 @@ def test_refusals_leave_outputs_alone():
     with pytest.raises(ValueError):
         moe.moe_add_rmsnorm(x, r.bfloat16(), w, 1e-6, y=y)
     assert bool((y == 7.0).all())
+
+
+@pytest.mark.parametrize("n", [16, 400, 7168])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_rows_keep_nan(n, bad):
+    """a NaN in x (a NaN or infinity once normed) shows in y and in the e4m3 row's scale and codes; other rows stay"""
+    x, r, w = make(5, n, torch.float32, 3)
+    out = [torch.empty(5, n, device=DEV), torch.empty(5, n, dtype=torch.uint8, device=DEV),
+           torch.empty(5, -(-n // 128), device=DEV)]
+    moe.moe_add_rmsnorm(x, r, w, 1e-6, y=out[0], x8=out[1], x8_scale=out[2])
+    want = [o.clone() for o in out]
+    x[3, n // 2] = bad
+    moe.moe_add_rmsnorm(x, r, w, 1e-6, y=out[0], x8=out[1], x8_scale=out[2])
+    keep = [0, 1, 2, 4]
+    assert all(torch.equal(o[keep], v[keep]) for o, v in zip(out, want))
+    # an infinity makes the others 0 and itself NaN
+    g = n // 2 // 128
+    assert bool(torch.isnan(out[0][3, n // 2])) and bool(torch.isnan(out[2][3, g]))
+    assert bool(((out[1][3, 128 * g:128 * g + 128] & 0x7F) == 0x7F).all())
+    if bad != bad:
+        assert bool(torch.isnan(out[0][3]).all()) and bool(torch.isnan(out[2][3]).all())

@@ -215,6 +215,26 @@ def test_balance_masks(gating, E):
     assert torch.equal(loss, loss2) and torch.equal(d, d2)
 
 
+@pytest.mark.parametrize("gating", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [1, 40, 97, 256])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_balance_keeps_nan(gating, E, dtype):
+    """a NaN in a row that counts shows in the loss and in that row's gradient alone, whatever is beside it"""
+    G = moe.SOFTMAX if gating == "softmax" else moe.SIGMOID
+    logits, counts = case(30, E, 1, 9)
+    logits = logits.to(dtype)
+    clean, want = balance(logits, counts, 1, G)
+    logits[2, E // 2] = float("nan")
+    logits[11] = float("nan")
+    logits[20] = -float("inf")
+    logits[20, E - 1] = float("nan")
+    loss, d = balance(logits, counts, 1, G)
+    rows = torch.zeros(30, dtype=torch.bool, device=DEV)
+    rows[[2, 11, 20]] = True
+    assert bool(torch.isfinite(clean).all()) and bool(torch.isnan(loss).all())
+    assert bool(torch.isnan(d[rows]).all()) and torch.equal(d[~rows], want[~rows])
+
+
 def test_balance_scale_parts_in_place_and_repeat():
     logits, counts = case(500, 64, 6, 3)
     ws = torch.zeros(moe.moe_balance_loss_workspace_bytes(500, 64), dtype=torch.uint8, device=DEV)
