@@ -171,13 +171,13 @@ __global__ void __launch_bounds__(VPT == 4 ? 512 : 1024) norm_kernel(const NormA
 template <typename TX, typename TY>
 cudaError_t launch_norm_t(const NormArgs &a, int T, cudaStream_t s) {
     const int chunks = (a.n + 255) / 256;
-    // Few rows: one chunk a warp, so that a row's loads are all in flight at
-    // once over as many warps as it has chunks.  Many rows: up to four chunks
-    // a warp, so that several rows share an SM and one loads while another
-    // waits at its sum.
-    const int most = T <= num_sms() ? 32 : 8;
-    if (chunks <= most) norm_kernel<TX, TY, 1><<<T, 32 * chunks, 0, s>>>(a);
-    else if (chunks <= 2 * most) norm_kernel<TX, TY, 2><<<T, 32 * ((chunks + 1) / 2), 0, s>>>(a);
+    // A row an SM or fewer: one chunk a warp (two past 8192), so that a row's loads are all in flight at once over as
+    // many warps as it has chunks: 16 x 7168 3.5 us, with four a warp 4.4.  More rows: up to 16 chunks one a warp as
+    // well (16384 x 4096 113 us, with two 124; 32768 x 2880 159 and 168), and four a warp beyond, so that several rows
+    // share an SM and one loads while another waits at its sum: 8192 x 7168 fp32 out 99.7 us, with two 125, with one 118.
+    const bool few = T <= num_sms();
+    if (chunks <= (few ? 32 : 16)) norm_kernel<TX, TY, 1><<<T, 32 * chunks, 0, s>>>(a);
+    else if (few) norm_kernel<TX, TY, 2><<<T, 32 * ((chunks + 1) / 2), 0, s>>>(a);
     else norm_kernel<TX, TY, 4><<<T, 32 * ((chunks + 3) / 4), 0, s>>>(a);
     return cudaGetLastError();
 }

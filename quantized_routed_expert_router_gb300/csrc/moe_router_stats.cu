@@ -285,8 +285,10 @@ __device__ __forceinline__ void store_vec(T *p, const float v[VEC]) {
     }
 }
 
-// J vectors of VEC values a lane: value i of vector j is expert 32*VEC*j + VEC*lane + i
-// blocks of a launch that share an SM (one row, its d and the next row take 3 to 4 registers a value)
+// J vectors of VEC values a lane: value i of vector j is expert 32*VEC*j + VEC*lane + i.
+// Blocks of a launch that share an SM (one row, its d and the next row take 3 to 4 registers a value), 65536 rows fp32:
+// E = 256, 8 values: 28.0 us with 4, 31.9 with 2; E = 257, 16 values: 37.4 with 2, 87.5 with 4 (spills); E = 64,
+// 2 values: 15.9 with 4, 17.0 with 8.
 constexpr int balance_per_sm(int values) { return values <= 8 ? 4 : 2; }
 
 template <typename T, bool SIGMOID, int VEC, int J>
@@ -455,7 +457,13 @@ void launch_balance_k(const BalanceArgs &a, cudaStream_t s) {
 
 template <typename T, bool SIGMOID>
 cudaError_t launch_balance_t(const BalanceArgs &a, cudaStream_t s) {
-    // rows whose length is a multiple of 4 are read 4 values at a time
+    // up to 64 experts: every lane has one or two (65536 x 64: 15.9 us; with 4 a lane half of them idle, 18.2)
+    if (a.E <= 64) {
+        launch_balance_k<T, SIGMOID, 1, 2>(a, s);
+        return cudaGetLastError();
+    }
+    // rows whose length is a multiple of 4 are read 4 values at a time (16384 x 1024: 36 us, value by value 47;
+    // 65536 x 256 bf16: 25.3, 26.8; fp32: 28.0, 28.1)
     if (a.E % 4 == 0) {
         if (a.E <= 128) launch_balance_k<T, SIGMOID, 4, 1>(a, s);
         else if (a.E <= 256) launch_balance_k<T, SIGMOID, 4, 2>(a, s);
