@@ -48,7 +48,7 @@ def workspace():
     return torch.zeros(moe.moe_fp8_matmul_workspace_bytes(), dtype=torch.uint8, device=DEV)
 
 
-# one block of depth and less, ragged depth and width, every part count of a split depth, tiles of 128 and of 256
+# one block of depth and less, ragged depth and width, every part count of a split depth, tiles of 128 and of 192
 # columns; places around the tile's 128
 DENSE = [(100, 333, 2048), (70, 1026, 4096), (40, 136, 8192), (21, 130, 1536), (5, 24, 48), (8, 200, 4112), (9, 1000, 336), (15, 2051, 1008), (1, 8, 16), (1, 1, 128), (2, 7, 144), (1, 128, 512), (16, 2048, 7168), (1, 7168, 2048), (3, 136, 4096),
          (17, 100, 1040), (64, 512, 1024), (127, 257, 272), (128, 128, 128), (129, 384, 640), (130, 1000, 2880),
@@ -325,3 +325,54 @@ def test_prefill_of_a_layer():
     f = counts.double() * E / (T * k)
     assert abs(float(loss) - 0.01 * float((f * p.mean(0)).sum())) <= 1e-6 * 0.01 * E
     assert moe.moe_read_device_status(st) == 0
+
+
+def codes(*shape):
+    """random finite codes, both signs, made in place (float values of such a size would not be small)"""
+    c = torch.empty(shape, dtype=torch.uint8, device=DEV).random_(0, 0x70)
+    c[..., ::3] += 0x80
+    return c
+
+
+@pytest.mark.parametrize("M", [12, 300])
+def test_rows_beyond_32_bits(M):
+    """x past 2^32 bytes, gathered: by the calls for few rows and by tiles"""
+    X, K, N = 540000, 8192, 200
+    torch.manual_seed(M)
+    x, xs = codes(X, K), torch.rand(X, K // 128, device=DEV) * 0.02
+    w, ws = matrices(1, N, K, torch.Generator(device=DEV).manual_seed(1))
+    rows = torch.randint(X - 2000, X, (M,), device=DEV, dtype=torch.int32)
+    rows[0], rows[1] = X - 1, 0
+    y, st = torch.empty(M, N, device=DEV), workspace()
+    moe.moe_fp8_matmul(x, xs, w[0], ws[0], y, st, rows=rows)
+    r = rows.long()
+    check(y, *definition(x[r].view(E4M3), xs[r], w[0], ws[0]), K)
+    assert moe.moe_read_device_status(st) == 0
+
+
+@pytest.mark.parametrize("each", [3, 70])
+def test_matrices_beyond_32_bits(each):
+    G, N, K = 70, 8192, 8192
+    torch.manual_seed(each)
+    w, ws = codes(G, N, K), torch.rand(G, N // 128, K // 128, device=DEV) * 1e-4
+    x, xs = states(2 * each, K, torch.Generator(device=DEV).manual_seed(2))
+    offs = torch.zeros(G + 1, dtype=torch.int32, device=DEV)
+    offs[G - 1], offs[G] = each, 2 * each                  # the last two experts
+    y, st = torch.empty(2 * each, N, device=DEV), workspace()
+    moe.moe_fp8_matmul(x, xs, w, ws, y, st, offsets=offs)
+    for e in range(2):
+        a = slice(e * each, (e + 1) * each)
+        check(y[a], *definition(x[a], xs[a], w[G - 2 + e].view(E4M3), ws[G - 2 + e]), K)
+    assert moe.moe_read_device_status(st) == 0
+
+
+@pytest.mark.parametrize("N", [16384, 16387])
+def test_results_beyond_32_bits(N):
+    M, K = 140000, 16
+    g = torch.Generator(device=DEV).manual_seed(N)
+    x, xs = states(M, K, g)
+    w, ws = matrices(1, N, K, g)
+    y = torch.full((M, N), 7.0, device=DEV)
+    moe.moe_fp8_matmul(x, xs, w[0], ws[0], y, workspace())
+    for a in (slice(0, 40), slice(M // 2, M // 2 + 40), slice(M - 200, M)):
+        check(y[a], *definition(x[a], xs[a], w[0], ws[0]), K)

@@ -216,3 +216,16 @@ def test_rows_keep_nan(n, bad):
     assert bool(((out[1][3, 128 * g:128 * g + 128] & 0x7F) == 0x7F).all())
     if bad != bad:
         assert bool(torch.isnan(out[0][3]).all()) and bool(torch.isnan(out[2][3]).all())
+
+
+def test_rows_beyond_32_bits():
+    T, n = 140000, 16384
+    x = torch.empty(T, n, dtype=torch.bfloat16, device=DEV).normal_()
+    w = torch.rand(n, device=DEV) + 0.5
+    y, x8 = torch.empty_like(x), torch.empty(T, n, dtype=torch.uint8, device=DEV)
+    scale = torch.empty(T, n // 128, device=DEV)
+    moe.moe_add_rmsnorm(x, None, w, 1e-6, y=y, x8=x8, x8_scale=scale)
+    for a in (slice(0, 3), slice(T // 2, T // 2 + 3), slice(T - 3, T)):
+        _, v = definition(x[a], None, w, 1e-6)
+        assert bool(((y[a].double() - v).abs() <= v.abs() * (2.0 ** -8 * 1.01 + V_TOL)).all())
+        check_rows8(x8[a], scale[a], v)

@@ -303,3 +303,38 @@ def test_refusals():
     with pytest.raises(ValueError):
         moe.moe_expert_order(ids.long(), 8, None, counts=c)
     assert float(loss) == 7.0 and bool((c == 7).all())
+
+
+def test_balance_rows_beyond_32_bits():
+    T, E = 2200000, 1024
+    logits = torch.empty(T, E, dtype=torch.bfloat16, device=DEV).normal_()
+    counts = torch.randint(0, 40000, (E,), dtype=torch.int32, device=DEV)
+    loss, d = balance(logits, counts, 8, moe.SOFTMAX)
+    assert bool(torch.isfinite(loss).all())
+    for a in (slice(0, 50), slice(T // 2, T // 2 + 50), slice(T - 50, T)):      # a row's gradient needs only the counts
+        assert torch.equal(balance(logits[a], counts, 8, moe.SOFTMAX)[1], d[a])
+
+
+def test_order_calls_in_a_row_share_a_workspace():
+    """each call's second launch starts early; the next call still finds the workspace free"""
+    sets = [draw_ids(20000, 8, 256, s).to(DEV) for s in range(6)]
+    want = [order(i, 256) for i in sets]
+    ws = torch.empty(moe.moe_expert_order_workspace_bytes(20000, 8, 256), dtype=torch.uint8, device=DEV)
+    names = ("counts", "offsets", "rows", "pos")
+    outs = [{n: torch.full_like(v, -9) for n, v in zip(names, w)} for w in want]
+
+    def calls():
+        for ids, out in zip(sets, outs):
+            moe.moe_expert_order(ids, 256, ws, **out)
+    calls()
+    for out, w in zip(outs, want):
+        assert all(torch.equal(out[n], v) for n, v in zip(names, w))
+        for v in out.values():
+            v.fill_(-9)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        calls()
+    for _ in range(3):
+        g.replay()
+    for out, w in zip(outs, want):
+        assert all(torch.equal(out[n], v) for n, v in zip(names, w))
