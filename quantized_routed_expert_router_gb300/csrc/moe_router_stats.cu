@@ -33,6 +33,10 @@ constexpr int kOrderChunk = kOrderThreads * kOrderIters;   // 4096; counts in a 
 
 // counts of a chunk in hist: 16 bits each, rows of whole 16-byte pieces
 __host__ __device__ constexpr int hist_pitch(int E) { return (E + 7) & ~7; }
+// dynamic shared memory of order_place: base and total in 32 bits, the runs in 16 (72 KB at E = 1024)
+constexpr int order_place_smem(int E) {
+    return hist_pitch(E) * (int)(2 * sizeof(int32_t) + kOrderWarps * sizeof(uint16_t));
+}
 
 __global__ void __launch_bounds__(kOrderThreads) order_count(const int32_t *__restrict__ ids, int n, int E,
                                                    uint16_t *__restrict__ hist) {
@@ -490,11 +494,13 @@ cudaError_t launch_order(const int32_t *ids, int T, int k, int E, int32_t *count
     const int n = T * k;
     const int chunks = n > 0 ? (n + kOrderChunk - 1) / kOrderChunk : 1;
     uint16_t *hist = chunks > 1 ? static_cast<uint16_t *>(ws) : nullptr;
-    // 72 KB at E = 1024
-    const size_t smem = (size_t)hist_pitch(E) * (2 * sizeof(int32_t) + kOrderWarps * sizeof(uint16_t));
+    const size_t smem = (size_t)order_place_smem(E);
     cudaError_t err = cudaSuccess;
+    // The limit belongs to the kernel, not to the launch: one value whatever E is, so that a call on another host
+    // thread cannot lower it between here and the launch.
     if (smem > 48 * 1024)
-        err = cudaFuncSetAttribute(order_place, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        err = cudaFuncSetAttribute(order_place, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   order_place_smem(MOE_MAX_EXPERTS));
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)chunks);
