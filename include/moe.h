@@ -368,7 +368,8 @@ moe_status moe_sum_partials(const float *parts, int R, size_t n, float *y, cudaS
  * products take, in one pass: per row of n values
  *   s = x + residual                  (residual NULL: s = x)
  *   v = s * (1 / sqrt(mean(s*s) + eps)) * weight
- * in fp32, from the sum before its rounding to `dtype`.
+ * in fp32, from the sum before its rounding to `dtype`.  A row has the same bits
+ * whatever T is.
  *   x, residual  : device [T][n] of `dtype`; weight: device fp32 [n]
  *   residual_out : device [T][n] of `dtype` out: s, or NULL.  May be x or residual.
  *   y            : device [T][n] of `ydtype` out: v, or NULL (fp32 for an F32 router)

@@ -100,12 +100,41 @@ struct NormArgs {
     size_t xq_row;
 };
 
+// Sums over a warp of VPT chunks' numbers at once: number j ends up in the lanes from 32 / VPT * j on.  Where there are
+// several, half of the lanes go on with each half of them.  Each is added by the same tree (lanes 16, 8, 4, 2, 1 apart)
+// whatever VPT, so a chunk's sum has the same bits in every layout.
+template <int VPT>
+__device__ __forceinline__ float chunk_sums(const float s[VPT], int lane) {
+    float v;
+    if constexpr (VPT == 1) {
+        v = s[0] + __shfl_xor_sync(0xFFFFFFFFu, s[0], 16);
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
+    } else if constexpr (VPT == 2) {
+        const bool up = lane & 16;
+        v = (up ? s[1] : s[0]) + __shfl_xor_sync(0xFFFFFFFFu, up ? s[0] : s[1], 16);
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
+    } else {
+        static_assert(VPT == 4, "");
+        const bool up = lane & 16, odd = lane & 8;
+        const float a = (up ? s[2] : s[0]) + __shfl_xor_sync(0xFFFFFFFFu, up ? s[0] : s[2], 16);
+        const float b = (up ? s[3] : s[1]) + __shfl_xor_sync(0xFFFFFFFFu, up ? s[1] : s[3], 16);
+        v = (odd ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 8);
+    }
+#pragma unroll
+    for (int off = 4; off >= 1; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+    return v;
+}
+
+constexpr int kMaxChunks = MOE_MAX_NORM_WIDTH / 256;
+
 // One row per block.  Warp w takes the 256-value chunks w, w + W, ...: at most
-// VPT of them.  x and residual are read through plain loads: residual_out may
+// VPT of them.  The squares of each chunk are added by themselves, then the
+// chunks in their order, so a row's bits do not hang on its layout and with it
+// on the number of rows.  x and residual are read through plain loads: residual_out may
 // be either of them, and a thread writes only where it has read.
 template <typename TX, typename TY, int VPT>
 __global__ void __launch_bounds__(VPT == 4 ? 512 : 1024) norm_kernel(const NormArgs a) {
-    __shared__ float part[32];
+    __shared__ float part[kMaxChunks];   // a chunk's sum of squares
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5, n = a.n;
     const size_t at = (size_t)blockIdx.x * n;
     const TX *x = static_cast<const TX *>(a.x) + at;
@@ -130,14 +159,16 @@ __global__ void __launch_bounds__(VPT == 4 ? 512 : 1024) norm_kernel(const NormA
             }
         }
     }
-    float ss = 0.f;
+    float sq[VPT];
 #pragma unroll
-    for (int j = 0; j < VPT; ++j)
+    for (int j = 0; j < VPT; ++j) {
+        sq[j] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(s[j][i], s[j][i], ss);
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, off);
-    if (lane == 0) part[warp] = ss;
+        for (int i = 0; i < 8; ++i) sq[j] = fmaf(s[j][i], s[j][i], sq[j]);
+    }
+    constexpr int PER = 32 / VPT;   // lanes that hold a chunk's sum
+    const float sum = chunk_sums<VPT>(sq, lane);
+    if (lane % PER == 0) part[warp + lane / PER * W] = sum;
     if (a.residual_out) {
         TX *out = static_cast<TX *>(a.residual_out) + at;
 #pragma unroll
@@ -147,7 +178,9 @@ __global__ void __launch_bounds__(VPT == 4 ? 512 : 1024) norm_kernel(const NormA
         }
     }
     __syncthreads();
-    ss = lane < W ? part[lane] : 0.f;
+    const int parts = VPT * W;   // past the row's last chunk: zeros
+    float ss = lane < parts ? part[lane] : 0.f;
+    if (VPT > 1 && lane + 32 < parts) ss += part[lane + 32];
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, off);
     const float rstd = __fdiv_rn(1.f, __fsqrt_rn(fmaf(ss, a.inv_n, a.eps)));
