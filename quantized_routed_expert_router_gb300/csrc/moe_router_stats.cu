@@ -210,10 +210,13 @@ __global__ void __launch_bounds__(kOrderThreads) order_place(const int32_t *__re
 // its d_e stay in registers, and it walks over the rows, the next row's loads
 // under way while it adds up one.  Bandwidth bounds it.
 //
-// Sums: a row and a warp's few rows in fp32 (a count holds the ones of 1 + q),
-// a block's warps and the blocks in double, in order (the last block to finish
-// adds the blocks).  Double arithmetic stays out of the loop: this part has few
-// units for it, and one addition a row cost a third of the kernel's time.
+// Sums: a row in fp32, a warp's rows in fp32 with the rounding of each addition
+// carried over to the next (a count holds the ones of 1 + q), a block's warps
+// and the blocks in double, in order (the last block to finish adds the
+// blocks).  A plain fp32 sum of a warp's rows (3,450 of 2^24) was off by up to
+// 500 u where the rows are alike, u = 2^-24; the carried one by 2.  This part has
+// few units for double arithmetic: an addition a row cost a third of the
+// kernel's time, and one for every 32 rows, behind a branch, a tenth at E = 8.
 // exp and the reciprocal of sigma are the machine's own, flushing below 2^-126
 // (exp is off by 2 ulp and |l - m| u, the reciprocal by 1 ulp): with the library
 // functions the kernel was bound by issue slots (350 instructions a row of 256).
@@ -336,8 +339,8 @@ __global__ void __launch_bounds__(32 * kBalanceWarps, balance_per_sm(VEC * J)) b
 #pragma unroll
         for (int i = 0; i < VEC; ++i) d[j][i] = (float)((long long)__float_as_int(d[j][i]) * E - N) * invN;
 
-    float sum = 0.f;   // of q
-    int rows = 0;      // rows that count
+    float sum = 0.f, over = 0.f;   // of q; by how much it is too large
+    int rows = 0;                  // rows that count
     for (; t < a.T; t += step) {
         T *out = a.dlogits ? static_cast<T *>(a.dlogits) + (size_t)t * E : nullptr;
         float p[J][VEC];
@@ -409,7 +412,9 @@ __global__ void __launch_bounds__(32 * kBalanceWarps, balance_per_sm(VEC * J)) b
         q = warp_sum(q);
         const float inv = __fdiv_rn(1.f, s);
         q *= inv;
-        sum += q;
+        const float term = q - over, up = sum + term;
+        over = (up - sum) - term;
+        sum = up;
         ++rows;
         if (out) {
             const float g = gcoef * inv;
@@ -423,7 +428,7 @@ __global__ void __launch_bounds__(32 * kBalanceWarps, balance_per_sm(VEC * J)) b
         }
     }
     if (!a.loss) return;
-    if (lane == 0) part[warp] = (double)sum + rows;
+    if (lane == 0) part[warp] = (double)(sum - over) + rows;
     __syncthreads();
     if (threadIdx.x == 0) {
         double b = 0.0;
