@@ -513,6 +513,21 @@ moe_status moe_debug_row_dots(const void *packed, moe_qtype qtype, int rows, int
  */
 moe_status moe_debug_set_exchange_wait(long long cycles);
 
+/*
+ * Test hook: makes the waits of moe_fp8_matmul launches made after this call
+ * run out (those of more than 16 places; fewer wait for nothing).
+ *   hold   : 0 off (the default); 1: each stage's copies wait for one arrival
+ *            more, which never comes; 2: each stage's products do
+ *   cycles : the bound on waits, in SM clock cycles, taken in units of 65536;
+ *            0 restores the default (8e8 cycles)
+ * A held launch records MOE_DEV_TIMEOUT, stores nothing after it gave up, lets
+ * its copies and products in flight end (for which it waits up to 8e8 cycles)
+ * and returns.  Host-side setting of this process, read when a launch is made
+ * (a captured graph keeps the value it was captured with).  Errors:
+ * MOE_ERR_INVALID_ARG for another hold or cycles < 0.
+ */
+moe_status moe_debug_hold_fp8_matmul(int hold, long long cycles);
+
 const char *moe_status_str(moe_status s);
 
 #ifdef __cplusplus

@@ -283,6 +283,12 @@ moe_status moe_fp8_matmul(const void *x8, const float *x_scale, int X, const int
                                   stream));
 }
 
+moe_status moe_debug_hold_fp8_matmul(int hold, long long cycles) {
+    if (hold < 0 || hold > 2 || cycles < 0) return MOE_ERR_INVALID_ARG;
+    hold_fp8(hold, cycles);
+    return MOE_OK;
+}
+
 moe_status moe_read_device_status(void *ws, int clear, uint32_t *flags, cudaStream_t stream) {
     if (!ws || !flags) return MOE_ERR_INVALID_ARG;
     uint32_t v = 0;

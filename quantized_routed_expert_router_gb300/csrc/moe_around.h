@@ -35,10 +35,14 @@ struct Fp8Args {
     int ntn;       // column tiles
     int xbox;      // rows of an x copy (ungathered)
     int yalign;    // bytes that rows of y are aligned to: 32, 16 or less
+    // test hook: bound on waits in units of 2^16 cycles; arrivals that never come at a stage's copies, at its products
+    uint32_t wait;
+    int hold_copies, hold_products;
 };
 cudaError_t launch_fp8(const void *x8, const float *x_scale, int X, const int32_t *rows, int M, const int32_t *offsets,
                        int G, const void *w, const float *w_scale, int N, int K, void *y, int ydtype,
                        unsigned *status, cudaStream_t s);
+void hold_fp8(int hold, long long cycles);   // moe_debug_hold_fp8_matmul
 bool fp8_few_rows(const Fp8Args &a);
 cudaError_t launch_fp8_rows(const Fp8Args &a, int ydtype, cudaStream_t s);
 

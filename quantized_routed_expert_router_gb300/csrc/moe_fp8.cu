@@ -40,7 +40,8 @@ constexpr int HC = 64;              // columns of an accumulating warp
 constexpr int GATHER_THREADS = 64;  // warps 2 and 3
 constexpr int MAX_SPLIT = 8;        // blocks that share a tile's depth
 constexpr int RED_PITCH = BM + 4;   // fp32 partial tiles, column by column; 16-byte pieces free of bank conflicts
-// bound on every device-side wait, in units of 2^16 SM clock cycles (8e8 cycles: under a second)
+// bound on every device-side wait, in units of 2^16 SM clock cycles (8e8 cycles: under a second), unless the test
+// hook shortens it; waits for copies and products in flight on the way out keep it
 constexpr uint32_t FP8_WAIT = 12207;
 
 // What bounds the tiles is how the sums come back: a TMEM load beside running
@@ -121,23 +122,22 @@ __device__ __forceinline__ uint32_t elect() {
 // wait for a phase; false once this block has given up (the first wait to run
 // out says so to the others and in the status word).  Inline: a call would take
 // registers that the accumulating warps do not have.
-__device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, Ctl *c, unsigned *status) {
+__device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, Ctl *c, const Fp8Args &a) {
     if (bar_test(b, parity)) return true;
     const uint32_t t0 = clock_hi();
     while (!bar_test(b, parity)) {
         if (*(volatile int *)&c->abort) return false;
-        if (clock_hi() - t0 > FP8_WAIT) {
+        if (clock_hi() - t0 > a.wait) {
             *(volatile int *)&c->abort = 1;
-            atomicOr(status, MOE_DEV_TIMEOUT);
+            atomicOr(a.status, MOE_DEV_TIMEOUT);
             return false;
         }
     }
     return true;
 }
-// wait on the way out of a block that has given up: for its own copies and
-// products in flight, bounded by itself
-__device__ __forceinline__ void bar_settle(uint64_t *b, uint32_t parity) {
-    const uint32_t t0 = clock_hi();
+// wait on the way out of a block: for its own copies and products in flight,
+// until FP8_WAIT after t0 at most
+__device__ __forceinline__ void bar_settle(uint64_t *b, uint32_t parity, uint32_t t0) {
     while (!bar_test(b, parity))
         if (clock_hi() - t0 > FP8_WAIT) return;
 }
@@ -344,8 +344,8 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
-            bar_init(&c.full[i], a.rows ? 1 + GATHER_THREADS : 1);   // TMA's copies, and the gathered rows
-            bar_init(&c.done[i], 1);
+            bar_init(&c.full[i], (a.rows ? 1 + GATHER_THREADS : 1) + a.hold_copies);   // TMA's copies, and the gathered rows
+            bar_init(&c.done[i], 1 + a.hold_products);
         }
         for (int i = 0; i < NBUF; ++i) bar_init(&c.dempty[i], S::EPI_WARPS);
         bar_init(&c.drain, 1);
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
                 const int wrow = __shfl_sync(0xFFFFFFFFu, tl.g * a.N + tl.n0, 0);
                 const int xrow = __shfl_sync(0xFFFFFFFFu, tl.first, 0);
                 for (int kb = kb0; kb < kb1; ++kb, ++it, r.next()) {
-                    ok = bar_wait(&c.done[r.i], r.phase ^ 1, &c, a.status);
+                    ok = bar_wait(&c.done[r.i], r.phase ^ 1, &c, a);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                     uint8_t *sx = stages + r.i * S::STAGE;
@@ -418,8 +418,9 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
                 }
             }
             // copies in flight land, and their products end, before the block ends
+            const uint32_t t_out = clock_hi();
             for (int i = it > STAGES ? it - STAGES : 0; i < it; ++i)
-                bar_settle(ok ? &c.done[i % STAGES] : &c.full[i % STAGES], (i / STAGES) & 1);
+                bar_settle(ok ? &c.done[i % STAGES] : &c.full[i % STAGES], (i / STAGES) & 1, t_out);
             __syncwarp();
         } else if (warp == 1) {
             constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
@@ -429,7 +430,7 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
             bool ok = true;
             for (int t = t0; t < total && ok; t += dt) {
                 for (int kb = kb0; kb < kb1; ++kb, r.next(), d.next()) {
-                    ok = bar_wait(&c.dempty[d.i], d.phase ^ 1, &c, a.status) && bar_wait(&c.full[r.i], r.phase, &c, a.status);
+                    ok = bar_wait(&c.dempty[d.i], d.phase ^ 1, &c, a) && bar_wait(&c.full[r.i], r.phase, &c, a);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                     // gathered rows were written through the generic proxy, and the wait made them visible here; the
@@ -446,7 +447,7 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
             }
             if (!ok) {   // products in flight end before TMEM is freed
                 mma_commit(&c.drain, me);
-                bar_settle(&c.drain, 0);
+                bar_settle(&c.drain, 0, clock_hi());
             }
             __syncwarp();
         } else {
@@ -466,7 +467,7 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
                     }
                     const int nr = (tl.rows - r0 + 7) >> 3;   // of this thread
                     for (int kb = kb0; kb < kb1; ++kb, r.next()) {
-                        ok = bar_wait(&c.done[r.i], r.phase ^ 1, &c, a.status);
+                        ok = bar_wait(&c.done[r.i], r.phase ^ 1, &c, a);
                         ok = __all_sync(0xFFFFFFFFu, ok);
                         if (!ok) break;
                         const bool in = kb * BK + 16 * pc < a.K;
@@ -522,7 +523,7 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
             // and nothing is stored.  What need not come after the sums stands between their load and the wait for it.
             const uint32_t at0 = tmem + part * HC + ((uint32_t)(32 * quad) << 16);
             for (int kb = kb0; kb < kb1; ++kb) {
-                if (ok) ok = bar_wait(&c.done[r.i], r.phase, &c, a.status);
+                if (ok) ok = bar_wait(&c.done[r.i], r.phase, &c, a);
                 __syncwarp();
                 fence_after();
                 r.next();
@@ -720,6 +721,13 @@ cudaError_t launch_fp8_t(Fp8Args a, cudaStream_t s) {
 
 }  // namespace
 
+static long long g_wait = 0;   // 0: the kernel's own bound
+static int g_hold = 0;
+void hold_fp8(int hold, long long cycles) {
+    g_hold = hold;
+    g_wait = cycles;
+}
+
 cudaError_t launch_fp8(const void *x8, const float *x_scale, int X, const int32_t *rows, int M, const int32_t *offsets,
                        int G, const void *w, const float *w_scale, int N, int K, void *y, int ydtype,
                        unsigned *status, cudaStream_t s) {
@@ -739,6 +747,9 @@ cudaError_t launch_fp8(const void *x8, const float *x_scale, int X, const int32_
     a.K = K;
     a.KB = (K + BK - 1) / BK;
     a.NB = (N + BK - 1) / BK;
+    a.wait = g_wait > 0 && (g_wait >> 16) < FP8_WAIT ? (uint32_t)(g_wait >> 16) : FP8_WAIT;
+    a.hold_copies = g_hold == 1;
+    a.hold_products = g_hold == 2;
     if (fp8_few_rows(a)) return launch_fp8_rows(a, ydtype, s);
     return ydtype == MOE_DT_BF16 ? launch_fp8_t<__nv_bfloat16>(a, s) : launch_fp8_t<float>(a, s);
 }
