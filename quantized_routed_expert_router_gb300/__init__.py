@@ -274,10 +274,14 @@ _bound = None
 
 
 def _native():
-    """The compiled binding of the calls below.  Raises if the library has not been built."""
+    """The compiled binding of the calls below.  Raises if it has not been built, or for another torch or Python."""
     global _bound
     if _bound is None:
         lib()
+        have, want = _build.built_calls_stamp(), _build.calls_stamp()
+        if have != want or not os.path.exists(_build.CALLS_SO):
+            raise RuntimeError(f"{_build.CALLS_SO} is not built for this Python and torch ({want}; built: {have}): run "
+                               "__graft_entry__.build()")
         from . import _calls
         _bound = _calls
     return _bound

@@ -3,7 +3,9 @@ torch binding of the calls around the experts (_calls.so) with g++.
 
 Translation units compile in parallel; the link step produces one shared
 object exporting the C ABI of include/moe.h.  _calls.so is a Python extension
-that links against it.
+that links against it; it holds for the torch and the Python that it was
+compiled against, which a stamp beside the objects names.  _moe.so needs
+neither and is in place before the binding is linked.
 """
 from __future__ import annotations
 
@@ -33,17 +35,48 @@ def _nvcc() -> str:
     return "nvcc"
 
 
-def _deps() -> list[str]:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(INCLUDE, "moe.h"))
-    return files
+BINDING = "binding.cpp"
+
+
+def _current(so: str, files: list[str]) -> bool:
+    if not os.path.exists(so):
+        return False
+    t = os.path.getmtime(so)
+    return all(os.path.getmtime(f) <= t for f in files)
+
+
+def lib_up_to_date() -> bool:
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != BINDING]
+    return _current(SO, [*files, os.path.join(INCLUDE, "moe.h")])
+
+
+def calls_stamp() -> str:
+    """What the binding is compiled against: torch and its C++ ABI, and Python's."""
+    import torch
+    return (f"torch {torch.__version__}, cxx11 abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)}, "
+            f"{sysconfig.get_config_var('SOABI')}")
+
+
+def _stamp_file() -> str:
+    return os.path.join(OUT_DIR, "calls.stamp")
+
+
+def built_calls_stamp() -> str | None:
+    """calls_stamp() of the binding that is there."""
+    try:
+        with open(_stamp_file()) as f:
+            return f.read()
+    except FileNotFoundError:
+        return None
+
+
+def calls_up_to_date() -> bool:
+    files = [os.path.join(CSRC, BINDING), os.path.join(INCLUDE, "moe.h")]
+    return _current(CALLS_SO, files) and built_calls_stamp() == calls_stamp()
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(SO) or not os.path.exists(CALLS_SO):
-        return False
-    t = min(os.path.getmtime(SO), os.path.getmtime(CALLS_SO))
-    return all(os.path.getmtime(f) <= t for f in _deps())
+    return lib_up_to_date() and calls_up_to_date()
 
 
 def _compile_binding() -> str:
@@ -54,7 +87,7 @@ def _compile_binding() -> str:
            sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"), INCLUDE]
     obj = os.path.join(OUT_DIR, "binding.o")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           *(f"-I{p}" for p in inc), "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+           *(f"-I{p}" for p in inc), "-c", os.path.join(CSRC, BINDING), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stderr}")
@@ -70,7 +103,11 @@ def _link_binding(obj: str) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link of the binding failed:\n{r.stderr}")
+    if os.path.exists(_stamp_file()):
+        os.remove(_stamp_file())
     os.replace(tmp, CALLS_SO)
+    with open(_stamp_file(), "w") as f:
+        f.write(calls_stamp())
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
@@ -92,16 +129,21 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
         return obj
 
     with cf.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
-        binding = ex.submit(_compile_binding)
-        objs = list(ex.map(compile_one, SOURCES))
-        binding = binding.result()
-    tmp = SO + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-Xlinker", "-soname,_moe.so", "-o", tmp, *objs, "-lcudart"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stderr}")
-    os.replace(tmp, SO)
-    _link_binding(binding)
+        binding = ex.submit(_compile_binding) if force or not calls_up_to_date() else None
+        if force or not lib_up_to_date():
+            objs = list(ex.map(compile_one, SOURCES))
+            tmp = SO + f".tmp{os.getpid()}"
+            cmd = [nvcc, *ARCH, "-shared", "-Xlinker", "-soname,_moe.so", "-o", tmp, *objs, "-lcudart"]
+            r = subprocess.run(cmd, capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"link failed:\n{r.stderr}")
+            os.replace(tmp, SO)
+        if binding:
+            try:
+                _link_binding(binding.result())
+            except Exception as e:
+                raise RuntimeError(f"{SO} is built; the binding of the calls around the experts ({CALLS_SO}) is not: "
+                                   f"{e}") from e
     return SO
 
 
