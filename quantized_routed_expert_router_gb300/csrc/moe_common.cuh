@@ -14,6 +14,9 @@
 #include <stdint.h>
 #include <stddef.h>
 
+#include <atomic>
+#include <mutex>
+
 #include "moe.h"
 
 namespace moe {
@@ -22,14 +25,19 @@ constexpr int WARP = 32;
 
 // Raises a kernel's dynamic shared memory limit only when a launch needs more
 // than the last value set (per device), so steady-state launches, including
-// those recorded into a CUDA graph, make no attribute calls.
+// those recorded into a CUDA graph, make no attribute calls.  Under a lock: of
+// two host threads' first launches the smaller one would otherwise lower the
+// limit again before the larger one's launch.
 template <auto kernel>
 inline cudaError_t ensure_smem(size_t bytes) {
-    static int set_bytes[64] = {0};   // one table per kernel
+    static std::atomic<int> set_bytes[64];   // one table per kernel
+    static std::mutex lock;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if ((int)bytes <= set_bytes[dev]) return cudaSuccess;
+    const std::lock_guard<std::mutex> held(lock);
     if ((int)bytes <= set_bytes[dev]) return cudaSuccess;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e == cudaSuccess) set_bytes[dev] = (int)bytes;
