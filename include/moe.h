@@ -374,7 +374,8 @@ moe_status moe_sum_partials(const float *parts, int R, size_t n, float *y, cudaS
  *   residual_out : device [T][n] of `dtype` out: s, or NULL.  May be x or residual.
  *   y            : device [T][n] of `ydtype` out: v, or NULL (fp32 for an F32 router)
  *   xq           : device out, T q8 records of v (moe_quantize_q8K's rule, bit for
- *                  bit, of the fp32 v), or NULL; needs n % 32 == 0
+ *                  bit, of the fp32 v), or NULL; needs n % 32 == 0.  These cannot hold
+ *                  a NaN: a block with one has scale 0 and codes 0
  *   x8, x8_scale : device out, e4m3 [T][n] and fp32 [T][ceil(n/128)], both or
  *                  neither: per group of 128 values (the last one may be short)
  *                  amax = max|v|, scale = amax/448, code = e4m3(v * (448/amax)),
@@ -440,6 +441,10 @@ size_t moe_expert_order_workspace_bytes(int T, int k, int E);
  *               completed call leaves it ready for the next one.  Calls that
  *               may overlap on the GPU (two captured graphs, too) need one each.
  * N == 0 gives loss 0 and gradient 0.  Sums run in a fixed order.
+ * Arithmetic is fp32 (the sum of the rows: fp32 that carries its roundings over,
+ * then double).  With u = 2^-24, exp(x) is the machine's and off by (4 + 1.3 |x|) u
+ * of itself, x a logit less its row's largest one (sigmoid: also the logit itself),
+ * and the inverse of 1 + exp by 2 u; what lies below 2^-126 counts as 0.
  * Limits: T in [0, MOE_MAX_ROWS] (0: loss 0), 1 <= E <= MOE_MAX_EXPERTS,
  * 1 <= k <= min(E, MOE_MAX_K).
  * Errors: MOE_ERR_INVALID_ARG for limits, types, gating, a NULL input, no

@@ -694,14 +694,16 @@ cudaError_t launch_fp8_t(Fp8Args a, cudaStream_t s) {
     const long long t128 = mt * ((a.N + 127) / 128), t192 = mt * ((a.N + 191) / 192);
     if (t128 > 0x3FFFFFFF) return cudaErrorNotSupported;
     // Depth in parts while all parts still have an SM of their own and 4 blocks of depth.  Whole tiles leave SMs idle
-    // and each takes a whole depth's time (us in parts, and whole): 256 x 2048 x 7168 11.5, 21.6; 64 x 2048 x 7168
-    // 14.2, 21.4; 512 x 1000 x 4096 9.7, 15.1.  At the shallow end, 64 x 7168 x 2048, it is 9.1 and 8.7.
+    // and each takes a whole depth's time (us in parts, and whole): 256 x 2048 x 7168 11.8, 19.6; 64 x 2048 x 7168
+    // 14.4, 19.2; 512 x 1000 x 4096 10.0, 13.7.  At the shallow end, 64 x 7168 x 2048, it is 9.1 and 8.1.
     int split = 1;
     while (split < MAX_SPLIT && t128 * split * 2 <= sms && a.KB >= split * 4) split *= 2;
     // 192 columns where that leaves a tile for every SM and the tiles are at least half full on average: fewer reads of x
-    // and w a product.  us with 192, and with 128: 8192 x 2048 x 7168 118, 136; 8192 x 7168 x 2048 131, 149; 128 experts
-    // of 1536 x 4096, 65536 rows 498, 565; 32 of 2880 x 2880, 4096 rows 65, 77.  Below the bounds: 1024 x 2048 x 7168
-    // (88 tiles) 25.7, 21.8; 256 experts of 512 x 2048, 16384 rows 57.9, 54.5; but 128 of 1536 x 4096, 6216 rows 136, 145.
+    // and w a product.  us with 192, and with 128: 8192 x 2048 x 7168 121, 126; 8192 x 7168 x 2048 131, 140; 128 experts
+    // of 1536 x 4096, 65536 rows 499, 525; 32 of 2880 x 2880, 4096 rows 66, 70.  Below the bounds: 1024 x 2048 x 7168
+    // (88 tiles) 26.1, 20.8; 256 experts of 512 x 2048, 16384 rows 58.4, 52.6; but 128 of 1536 x 4096, 6216 rows 136, 142.
+    // (Tiles are counted as if the rows fell on as many groups as there can be: a batch whose rows fall on few groups
+    // has fewer, and its depth stays whole.)
     const bool wide = split == 1 && t192 >= sms && a.M >= 64 * mt;
     CUtensorMap mx, mw;
     a.xbox = a.M >= BM || a.offsets ? BM : (a.M + 7) / 8 * 8;

@@ -205,9 +205,10 @@ template <typename TX, typename TY>
 cudaError_t launch_norm_t(const NormArgs &a, int T, cudaStream_t s) {
     const int chunks = (a.n + 255) / 256;
     // A row an SM or fewer: one chunk a warp (two past 8192), so that a row's loads are all in flight at once over as
-    // many warps as it has chunks: 16 x 7168 3.5 us, with four a warp 4.4.  More rows: up to 16 chunks one a warp as
-    // well (16384 x 4096 113 us, with two 124; 32768 x 2880 159 and 168), and four a warp beyond, so that several rows
-    // share an SM and one loads while another waits at its sum: 8192 x 7168 fp32 out 99.7 us, with two 125, with one 118.
+    // many warps as it has chunks: 16 x 7168 bf16 3.1 us, with two a warp 3.4.  More rows: up to 16 chunks one a warp as
+    // well (fp32 out, 16384 x 4096: 113 us, with two 122, with four 110; 32768 x 2880: 158, 166, 153), and four a warp
+    // beyond, so that several rows share an SM and one loads while another waits at its sum: 8192 x 7168 fp32 out 99.1 us,
+    // with two 122, with one 117.
     const bool few = T <= num_sms();
     if (chunks <= (few ? 32 : 16)) norm_kernel<TX, TY, 1><<<T, 32 * chunks, 0, s>>>(a);
     else if (few) norm_kernel<TX, TY, 2><<<T, 32 * ((chunks + 1) / 2), 0, s>>>(a);

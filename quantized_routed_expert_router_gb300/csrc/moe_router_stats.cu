@@ -24,8 +24,11 @@ namespace {
 // order_place starts while order_count still runs (its votes need only the
 // ids) and waits for it before it reads hist.  One chunk needs no hist:
 // order_place counts it itself, in one launch.
-// Few pairs: the launches and the chain of votes bound it; many: the votes
-// and the 4-byte scatter of rows.
+// Few pairs: the launch and the chain of votes bound it.  Many: the votes, the
+// 4-byte scatter of rows, and the counts of the chunks, all of which each block
+// reads: 2 MB of hist by 1024 blocks for 2^22 pairs over 1024 experts, 2.1 GB in
+// all.  524288 pairs over 256 experts take 11.5 us on the device, 2^20 22, 2^22
+// 110; 2^22 over 64 experts 70, over 1024 272.
 constexpr int kOrderWarps = 32;
 constexpr int kOrderThreads = 32 * kOrderWarps;
 constexpr int kOrderIters = 4;
@@ -208,7 +211,9 @@ __global__ void __launch_bounds__(kOrderThreads) order_place(const int32_t *__re
 // counts: both are close to 1).  The counts are known before the pass, so
 // loss and gradient come from one reading of the logits: a warp holds a row,
 // its d_e stay in registers, and it walks over the rows, the next row's loads
-// under way while it adds up one.  Bandwidth bounds it.
+// under way while it adds up one.  The instructions of a row and the chain of
+// its reductions bound it: at 65536 x 256 fp32 58% of the issue slots are taken
+// and 38% of the DRAM rate, and half the bytes (bf16) take 22.1 us instead of 28.5.
 //
 // Sums: a row in fp32, a warp's rows in fp32 with the rounding of each addition
 // carried over to the next (a count holds the ones of 1 + q), a block's warps
@@ -294,8 +299,8 @@ __device__ __forceinline__ void store_vec(T *p, const float v[VEC]) {
 
 // J vectors of VEC values a lane: value i of vector j is expert 32*VEC*j + VEC*lane + i.
 // Blocks of a launch that share an SM (one row, its d and the next row take 3 to 4 registers a value), 65536 rows fp32:
-// E = 256, 8 values: 28.0 us with 4, 31.9 with 2; E = 257, 16 values: 37.4 with 2, 87.5 with 4 (spills); E = 64,
-// 2 values: 15.9 with 4, 17.0 with 8.
+// E = 256, 8 values: 28.5 us with 4, 31.9 with 2; E = 257, 16 values: 37.6 with 2, 87.5 with 4 (spills); E = 64,
+// 2 values: 16.0 with 4, 17.0 with 8.
 constexpr int balance_per_sm(int values) { return values <= 8 ? 4 : 2; }
 
 template <typename T, bool SIGMOID, int VEC, int J>
@@ -466,13 +471,13 @@ void launch_balance_k(const BalanceArgs &a, cudaStream_t s) {
 
 template <typename T, bool SIGMOID>
 cudaError_t launch_balance_t(const BalanceArgs &a, cudaStream_t s) {
-    // up to 64 experts: every lane has one or two (65536 x 64: 15.9 us; with 4 a lane half of them idle, 18.2)
+    // up to 64 experts: every lane has one or two (65536 x 64: 16.0 us; with 4 a lane half of them idle, 18.2)
     if (a.E <= 64) {
         launch_balance_k<T, SIGMOID, 1, 2>(a, s);
         return cudaGetLastError();
     }
     // rows whose length is a multiple of 4 are read 4 values at a time (16384 x 1024: 36 us, value by value 47;
-    // 65536 x 256 bf16: 25.3, 26.8; fp32: 28.0, 28.1)
+    // 65536 x 256 bf16: 25.4, 26.8)
     if (a.E % 4 == 0) {
         if (a.E <= 128) launch_balance_k<T, SIGMOID, 4, 1>(a, s);
         else if (a.E <= 256) launch_balance_k<T, SIGMOID, 4, 2>(a, s);
