@@ -392,7 +392,9 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
     __syncthreads();
     fence_after();
     const uint32_t tmem = c.tmem;
-    const int total = c.tstart[a.G] * a.ntn;
+    // Rising offsets have fewer than 2^30 tiles (the launch checks it).  Falling ones let groups overlap and can have up to
+    // G / 2 times as many: no more than 2^30 of them, so that tile numbers stay in 32 bits.
+    const int total = (int)min((long long)c.tstart[a.G] * a.ntn, 0x3FFFFFFFll);
     const int rank = SPLIT ? (int)cluster_rank() : 0, parts = SPLIT ? (int)cluster_size() : 1;
     const int t0 = SPLIT ? (int)blockIdx.x / parts : (int)blockIdx.x, dt = SPLIT ? total : (int)gridDim.x;
     const int kb0 = SPLIT ? rank * a.KB / parts : 0, kb1 = SPLIT ? (rank + 1) * a.KB / parts : a.KB;
