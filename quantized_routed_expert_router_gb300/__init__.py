@@ -278,11 +278,10 @@ def _native():
     global _bound
     if _bound is None:
         lib()
-        have, want = _build.built_calls_stamp(), _build.calls_stamp()
-        if have != want or not os.path.exists(_build.CALLS_SO):
-            raise RuntimeError(f"{_build.CALLS_SO} is not built for this Python and torch ({want}; built: {have}): run "
-                               "__graft_entry__.build()")
         from . import _calls
+        have, want = _calls.built_for, _build.calls_stamp()
+        if have != want:
+            raise RuntimeError(f"{_build.CALLS_SO} is built for {have}, this is {want}: run __graft_entry__.build()")
         _bound = _calls
     return _bound
 

@@ -4,8 +4,9 @@ torch binding of the calls around the experts (_calls.so) with g++.
 Translation units compile in parallel; the link step produces one shared
 object exporting the C ABI of include/moe.h.  _calls.so is a Python extension
 that links against it; it holds for the torch and the Python that it was
-compiled against, which a stamp beside the objects names.  _moe.so needs
-neither and is in place before the binding is linked.
+compiled against, which it names (built_for), as does a stamp beside the objects
+for the next build.  _moe.so needs neither and is in place before the binding is
+linked.
 """
 from __future__ import annotations
 
@@ -87,6 +88,7 @@ def _compile_binding() -> str:
            sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"), INCLUDE]
     obj = os.path.join(OUT_DIR, "binding.o")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DCALLS_STAMP="{calls_stamp()}"',
            *(f"-I{p}" for p in inc), "-c", os.path.join(CSRC, BINDING), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

@@ -257,4 +257,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nul
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__calls() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__calls() {
+    PyObject *m = PyModule_Create(&module);
+    // what this object was compiled against, as the build names it
+    if (m && PyModule_AddStringConstant(m, "built_for", CALLS_STAMP) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}
