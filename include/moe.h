@@ -525,9 +525,8 @@ moe_status moe_debug_set_exchange_wait(long long cycles);
  *            more, which never comes; 2: each stage's products do
  *   cycles : the bound on waits, in SM clock cycles, taken in units of 65536;
  *            0 restores the default (8e8 cycles)
- * A held launch records MOE_DEV_TIMEOUT, stores nothing after it gave up, lets
- * its copies and products in flight end (for which it waits up to 8e8 cycles)
- * and returns.  Host-side setting of this process, read when a launch is made
+ * A held launch records MOE_DEV_TIMEOUT, stores nothing, lets its copies and
+ * products in flight end (for which it waits up to 8e8 cycles) and returns.  Host-side setting of this process, read when a launch is made
  * (a captured graph keeps the value it was captured with).  Errors:
  * MOE_ERR_INVALID_ARG for another hold or cycles < 0.
  */

@@ -159,9 +159,9 @@ cudaError_t launch_t(const Fp8Args &a, int ydtype, dim3 grid, cudaStream_t s) {
 
 // Up to 16 places: one matrix of 2048 x 7168 takes 4.6 us for one row and 6.6 for 16 where tiles take 11.8 and 12.4
 // (7168 x 2048: 4.4 and 5.6 against 8.2 and 8.5); experts of 1536 x 4096, 8 rows over 8 of them: 14.9 against 14.9, 16
-// over 16: 23.7 against 27.5; of 512 x 2048, 8 over 8: 5.2 against 8.0; but of 4096 x 1536: 17.0 against 14.8.  At 24 rows and more a second reading of the weights brings them level (one
-// matrix: 8.4 against 7.5) and, over many experts, short blocks fall behind the tiles' queues of copies (64 rows over
-// 48 experts of 1536 x 4096: 61 against 52).
+// over 16: 23.7 against 27.5; of 512 x 2048, 8 over 8: 5.2 against 8.0; but of 4096 x 1536: 17.0 against 14.8.  At 24
+// rows and more a second reading of the weights brings them level (one matrix: 8.4 against 7.5) and, over many experts,
+// short blocks fall behind the tiles' queues of copies (64 rows over 48 experts of 1536 x 4096: 61 against 52).
 bool fp8_few_rows(const Fp8Args &a) {
     return a.M <= 16;
 }

@@ -41,7 +41,9 @@ torch.cuda.synchronize()
 assert not wrong, wrong
 for T, x, ids, w, logits, ws, stream in work:
     want = x.double() @ router.double().t()
-    assert float((logits.double() - want).abs().max()) <= 1e-3
+    # fp32 dots of 1024 values: each of at most 64 additions in a row and the product rounded, of the magnitudes' sum
+    tol = 65 * 2.0 ** -24 * (x.double().abs() @ router.double().abs().t())
+    assert bool(((logits.double() - want).abs() <= tol).all())
 print("alright")
 """
 
