@@ -64,17 +64,28 @@ typedef enum {
 
 typedef enum { MOE_GATE_SOFTMAX = 0, MOE_GATE_SIGMOID = 1 } moe_gating;
 
-/* Element types of the calls around the experts (norm, balance loss, e4m3 product). */
+/* Element types of the calls around the experts. */
 typedef enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1 } moe_dtype;
+
+/* What moe_matmul does with its products (v: the product plus the bias). */
+typedef enum {
+    MOE_ACT_NONE = 0,        /* v                                                              */
+    MOE_ACT_SILU = 1,        /* v sigma(v)                                                     */
+    MOE_ACT_GELU = 2,        /* v Phi(v), Phi(v) = (1 + erf(v / sqrt 2)) / 2                   */
+    MOE_ACT_SWIGLU = 3,      /* silu(gate) up: v has 2N columns, gate then up                  */
+    MOE_ACT_SILU_GRAD = 4,   /* v silu'(z)                                                     */
+    MOE_ACT_GELU_GRAD = 5,   /* v gelu'(z)                                                     */
+    MOE_ACT_SWIGLU_GRAD = 6  /* z = [gate up], 2N columns: y = [v up silu'(gate), v silu(gate)] */
+} moe_act;
 
 /* Device status word bits (moe_read_device_status). */
 #define MOE_DEV_BAD_ID 0x1u       /* an expert id outside [0, E): that slot was skipped     */
 #define MOE_DEV_DUP_ID 0x2u       /* an id repeated within one token: the repeat was skipped */
-#define MOE_DEV_TIMEOUT 0x4u      /* a bounded wait in moe_layer_forward or moe_fp8_matmul gave up:
-                                     y is invalid, zero the workspace before the next call */
-#define MOE_DEV_BAD_ROW 0x8u      /* moe_fp8_matmul: a row index outside x (that row of y is zero) or
-                                     offsets that fall or leave [0, M] (rows of those groups are left
-                                     out or computed with one group or another)                 */
+#define MOE_DEV_TIMEOUT 0x4u      /* a bounded wait in moe_layer_forward, moe_fp8_matmul or moe_matmul gave
+                                     up: y is invalid, zero the workspace before the next call */
+#define MOE_DEV_BAD_ROW 0x8u      /* moe_fp8_matmul, moe_matmul: a row index outside x (its products are
+                                     zero) or offsets that fall or leave [0, M] (rows of those groups
+                                     are left out or computed with one group or another)        */
 
 /* Limits of this build. */
 #define MOE_MAX_TOKENS 16          /* T per call (small-batch decode)        */
@@ -82,7 +93,7 @@ typedef enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1 } moe_dtype;
 #define MOE_MAX_EXPERTS 1024       /* E                                      */
 #define MOE_MAX_RANKS 64           /* partial outputs summed by moe_sum_partials */
 #define MOE_MAX_ROWS (1 << 24)     /* T, M, X of the calls around the experts  */
-#define MOE_MAX_PAIRS (1 << 22)    /* T*k of moe_expert_order                  */
+#define MOE_MAX_PAIRS (1 << 22)    /* T*k of moe_expert_order and the row calls */
 #define MOE_MAX_NORM_WIDTH 16384   /* n of moe_add_rmsnorm                     */
 #define MOE_FP8_GROUP 128          /* values that share a scale of an e4m3 row */
 
@@ -488,8 +499,149 @@ moe_status moe_fp8_matmul(const void *x8, const float *x_scale, int X, const int
 size_t moe_fp8_matmul_workspace_bytes(void);
 
 /*
+ * The experts of each token and their gating weights, from the logits of any
+ * number of tokens (moe_route's choice and weights): the k largest logits of a
+ * row in falling order, equal ones by the lower index, and with g = exp(l)
+ * (softmax) or sigma(l) (sigmoid)
+ *   renormalize : w_e = g_e / sum of g over the chosen
+ *   otherwise   : w_e = g_e / sum of g over all E (softmax), g_e (sigmoid)
+ *   logits  : device [T][E] of `dtype`.  -inf marks an expert that a token may
+ *             not take; where fewer than k are left, the last slots have id -1 and
+ *             weight 0.  A NaN counts as larger than any number, so it is chosen
+ *             and makes its weights NaN (so does +inf, where weights are ratios).
+ *   valid   : device uint8 [T] or NULL: a token with 0 (padding) has ids -1 and
+ *             weights 0; its logits are not looked at
+ *   ids     : device int32 [T][k] out (moe_expert_order's input)
+ *   weights : device fp32 [T][k] out, or NULL
+ * Arithmetic is fp32.  The softmax over all E takes the machine's exp, off by
+ * (4 + 1.3 |x|) u of itself for x a logit less the row's largest (u = 2^-24);
+ * what lies below 2^-126 counts as 0.
+ * Limits: T in [0, MOE_MAX_ROWS], 1 <= E <= MOE_MAX_EXPERTS, 1 <= k <= min(E, MOE_MAX_K).
+ * Errors: MOE_ERR_INVALID_ARG for limits, types, gating, NULL logits or ids, or
+ * logits that are not 16-byte aligned (ids, weights: 4).
+ */
+moe_status moe_topk(const void *logits, moe_dtype dtype, const uint8_t *valid, int T, int E, int k, moe_gating gating,
+                    int renormalize, int32_t *ids, float *weights, cudaStream_t stream);
+
+/*
+ * The gradient of moe_topk's weights: dlogits = addend + sum over the slots of
+ * dweights dw/dlogits, with the choice held fixed.  With d = dweights, sums over
+ * the row's slots:
+ *   softmax, renormalised  : w_e (d_e - sum w d) for the chosen, 0 for others
+ *   softmax over all E     : w_e (d_e - sum w d), d_e = 0 for others
+ *   sigmoid, renormalised  : (1 - sigma(l_e)) w_e (d_e - sum w d) for the chosen
+ *   sigmoid                : (1 - w_e) w_e d_e for the chosen
+ *   logits   : device [T][E] of `dtype`, as moe_topk had them
+ *   ids      : device int32 [T][k]; a slot whose id lies outside [0, E) takes no
+ *              part (its dweights are not looked at).  An id that comes twice in
+ *              a row counts as two slots.
+ *   dweights : device fp32 [T][k] (moe_combine_grad)
+ *   addend   : device [T][E] of `dtype` (the balance loss's gradient), or NULL (0)
+ *   dlogits  : device [T][E] of `dtype` out.  May be logits or addend.
+ * A logit of -inf has weight 0 and gradient 0.  Arithmetic as moe_topk's.
+ * Limits as moe_topk's.
+ * Errors: MOE_ERR_INVALID_ARG for limits, types, gating, a NULL input or output,
+ * or logits, addend, dlogits that are not 16-byte aligned (ids, dweights: 4).
+ */
+moe_status moe_topk_grad(const void *logits, moe_dtype dtype, const int32_t *ids, const float *dweights, int T, int E,
+                         int k, moe_gating gating, int renormalize, const void *addend, void *dlogits,
+                         cudaStream_t stream);
+
+/*
+ * Token rows to their places in the order by expert (moe_expert_order's pos):
+ *   xs[pos[t][s]] = x[t]
+ *   x   : device [T][n] of `dtype`
+ *   pos : device int32 [T][k]; a pair whose place lies outside [0, M) takes no
+ *         part.  No place comes twice.
+ *   xs  : device [M][n] of `dtype` out; rows of no pair keep their values.  Must
+ *         not overlap x.
+ * The gradient is moe_combine_rows without weights.
+ * Limits: T, M in [0, MOE_MAX_ROWS], 1 <= k <= MOE_MAX_K, T*k <= MOE_MAX_PAIRS,
+ * 1 <= n <= 65536, T*n and M*n <= 2^36.  T == 0 is a no-op.
+ * Errors: MOE_ERR_INVALID_ARG for limits, types, a NULL buffer, or rows that
+ * are not 16-byte aligned (pos: 4).
+ */
+moe_status moe_dispatch_rows(const void *x, moe_dtype dtype, const int32_t *pos, int T, int k, int n, int M, void *xs,
+                             cudaStream_t stream);
+
+/*
+ * Rows in the order by expert back to their tokens:
+ *   y[t] = addend[t] + sum_s weights[t][s] o[pos[t][s]]
+ * added in fp32 from the addend on, in the order of the slots.
+ *   o       : device [M][n] of `dtype`
+ *   pos     : device int32 [T][k]; a pair whose place lies outside [0, M) adds nothing
+ *   weights : device fp32 [T][k], or NULL (1)
+ *   addend  : device [T][n] of `ydtype`, or NULL (0).  May be y.
+ *   y       : device [T][n] of `ydtype` out.  Must not overlap o.
+ * Limits, errors (weights: 4) as moe_dispatch_rows's; with M == 0 o may be NULL.
+ */
+moe_status moe_combine_rows(const void *o, moe_dtype dtype, const int32_t *pos, const float *weights, int T, int k,
+                            int n, int M, const void *addend, void *y, moe_dtype ydtype, cudaStream_t stream);
+
+/*
+ * The gradient of moe_combine_rows:
+ *   d_o[pos[t][s]] = weights[t][s] dy[t],   dweights[t][s] = sum_j o[pos[t][s]][j] dy[t][j]
+ *   dy       : device [T][n] of `ydtype`
+ *   pos      : device int32 [T][k]; a pair whose place lies outside [0, M) has no
+ *              row and dweights 0.  No place comes twice.
+ *   weights  : device fp32 [T][k], or NULL (1)
+ *   o        : device [M][n] of `dtype`; NULL without dweights
+ *   d_o      : device [M][n] of `dtype` out, or NULL; rows of no pair keep their
+ *              values.  May be o.
+ *   dweights : device fp32 [T][k] out, or NULL
+ * dweights are fp32 sums in one order for given sizes.  (The addend's gradient is dy.)
+ * Limits, errors (weights, dweights: 4) as moe_dispatch_rows's; MOE_ERR_INVALID_ARG
+ * also for no output or dweights without o.  With M == 0 o and d_o are not looked at.
+ */
+moe_status moe_combine_grad(const void *dy, moe_dtype ydtype, const int32_t *pos, const float *weights, int T, int k,
+                            int n, int M, const void *o, moe_dtype dtype, void *d_o, float *dweights,
+                            cudaStream_t stream);
+
+/*
+ * Products of bf16 rows with bf16 matrices on the tensor cores, with bias,
+ * activation and residual.  Grouped by expert, or one matrix for all rows: with
+ *   v[i][n] = bias[g][n] + sum_k x[r][k] w[g][n][k],   r = rows ? rows[i] : i
+ * for the places i of each group g, offsets[g] <= i < offsets[g+1],
+ *   y[i] = act(v[i]) + residual[i]
+ * for MOE_ACT_NONE to MOE_ACT_SWIGLU, and y[i] = v[i] act'(z[i]) for the gradients
+ * (moe_act; the product is then the gradient that comes back through the next
+ * matrix, and y is that of v as the forward call had it).
+ *   x        : device bf16 [X][K]
+ *   rows     : device int32 [M], values in [0, X), or NULL (needs X >= M)
+ *   offsets  : device int32 [G+1], rising, in [0, M], or NULL (G == 1, all M)
+ *   w        : device bf16 [G][N][K] (MOE_ACT_SWIGLU: [G][2N][K], gate rows, then
+ *              up rows), or with transposed != 0 [G][K][N]: a matrix as the forward
+ *              call has it takes gradients back
+ *   bias     : device fp32 [G][N] ([G][2N]), or NULL; not with the gradients
+ *   residual : device [M][N] of `ydtype`, or NULL; not with the gradients.  May be y.
+ *   z        : device [M][N] ([M][2N]) of `ydtype`: v, out, or NULL; not with
+ *              MOE_ACT_NONE.  The gradients need it, as an input; there it may be y.
+ *   y        : device [M][N] ([M][2N] with MOE_ACT_SWIGLU_GRAD) of `ydtype` out.
+ *              Rows of no group keep their values (z too).
+ *   ws       : device workspace of moe_matmul_workspace_bytes() bytes (the status
+ *              word, moe_read_device_status), zero-filled before its first use.
+ *              Calls that overlap on the GPU may share it.
+ * Sums are fp32, in one order for given sizes: equal calls give equal bits, other
+ * sizes may add up in another order.  Activations are fp32, of the unrounded v.
+ * Row indexes and offsets outside their ranges are never followed (MOE_DEV_BAD_ROW);
+ * the product of such a row is 0.
+ * Limits: X, M in [0, MOE_MAX_ROWS] (M == 0 is a no-op), 1 <= G <=
+ * MOE_MAX_EXPERTS, 1 <= N <= 2^20, 8 <= K <= 2^20, K % 8 == 0; transposed: N % 8 == 0;
+ * MOE_ACT_SWIGLU: N % 16 == 0, not transposed; G*N <= 2^30, X*K <= 2^36.
+ * Errors: MOE_ERR_INVALID_ARG for limits, types, act, a NULL buffer, X < M without
+ * rows, X == 0, offsets missing with G > 1, bias, residual or z where they have no
+ * place, z missing, or x, w, y, z, residual not 16-byte aligned (bias, rows,
+ * offsets: 4); MOE_ERR_UNSUPPORTED for K or N outside the rules above or more than
+ * 2^30 tiles of 128 x 16; MOE_ERR_WORKSPACE for a missing, short or unaligned ws.
+ */
+moe_status moe_matmul(const void *x, int X, const int32_t *rows, int M, const int32_t *offsets, int G, const void *w,
+                      int transposed, const float *bias, moe_act act, const void *residual, void *z, int N, int K,
+                      void *y, moe_dtype ydtype, void *ws, size_t ws_bytes, cudaStream_t stream);
+size_t moe_matmul_workspace_bytes(void);
+
+/*
  * Reads (and, if clear != 0, zeroes) the device status word at the start of
- * an FFN, layer or e4m3 product workspace (all keep it in their first 4 bytes).
+ * an FFN, layer or product workspace (all keep it in their first 4 bytes).
  * Synchronises `stream`.  *flags receives MOE_DEV_* bits.
  * Returns MOE_ERR_DEVICE_STATUS if any bit was set, MOE_OK otherwise.
  */

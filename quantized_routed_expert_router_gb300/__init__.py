@@ -27,10 +27,12 @@ EXPORTS = ["moe_act_block", "moe_q8_row_bytes", "moe_packed_bytes", "moe_pack_we
            "moe_layer_forward", "moe_layer_workspace_bytes", "moe_sum_partials", "moe_debug_set_exchange_wait",
            "moe_add_rmsnorm", "moe_expert_order", "moe_expert_order_workspace_bytes", "moe_balance_loss",
            "moe_balance_loss_workspace_bytes", "moe_fp8_matmul", "moe_fp8_matmul_workspace_bytes",
-           "moe_debug_hold_fp8_matmul"]
+           "moe_debug_hold_fp8_matmul", "moe_topk", "moe_topk_grad", "moe_dispatch_rows", "moe_combine_rows",
+           "moe_combine_grad", "moe_matmul", "moe_matmul_workspace_bytes"]
 LAYER_OVERLAP_PREVIOUS = 0x1
 DEV_TIMEOUT, DEV_BAD_ROW = 0x4, 0x8
 DT_F32, DT_BF16 = 0, 1
+ACT_NONE, ACT_SILU, ACT_GELU, ACT_SWIGLU, ACT_SILU_GRAD, ACT_GELU_GRAD, ACT_SWIGLU_GRAD = range(7)
 FP8_GROUP = 128          # values that share a scale of an e4m3 row
 
 _P = ctypes.c_void_p
@@ -112,6 +114,20 @@ def lib():
         L.moe_fp8_matmul.argtypes = [_P, _P, i, _P, i, _P, i, _P, _P, i, i, _P, i, _P, sz, _P]
         L.moe_fp8_matmul_workspace_bytes.restype = sz
         L.moe_fp8_matmul_workspace_bytes.argtypes = []
+        L.moe_topk.restype = i
+        L.moe_topk.argtypes = [_P, i, _P, i, i, i, i, i, _P, _P, _P]
+        L.moe_topk_grad.restype = i
+        L.moe_topk_grad.argtypes = [_P, i, _P, _P, i, i, i, i, i, _P, _P, _P]
+        L.moe_dispatch_rows.restype = i
+        L.moe_dispatch_rows.argtypes = [_P, i, _P, i, i, i, i, _P, _P]
+        L.moe_combine_rows.restype = i
+        L.moe_combine_rows.argtypes = [_P, i, _P, _P, i, i, i, i, _P, _P, i, _P]
+        L.moe_combine_grad.restype = i
+        L.moe_combine_grad.argtypes = [_P, i, _P, _P, i, i, i, i, _P, i, _P, _P, _P]
+        L.moe_matmul.restype = i
+        L.moe_matmul.argtypes = [_P, i, _P, i, _P, i, _P, i, _P, i, _P, _P, i, i, _P, i, _P, sz, _P]
+        L.moe_matmul_workspace_bytes.restype = sz
+        L.moe_matmul_workspace_bytes.argtypes = []
         L.moe_debug_set_exchange_wait.restype = i
         L.moe_debug_set_exchange_wait.argtypes = [ctypes.c_longlong]
         L.moe_debug_hold_fp8_matmul.restype = i
@@ -339,6 +355,65 @@ def moe_fp8_matmul(x8, x_scale, w, w_scale, y, ws, offsets=None, rows=None, stre
     s = (_bound or _native()).fp8_matmul(x8, x_scale, w, w_scale, y, ws, offsets, rows, stream)
     if s:
         raise MoeError(s, "moe_fp8_matmul")
+
+
+def moe_topk(logits, gating: int, renormalize: bool, ids, weights=None, valid=None, stream=None):
+    """The k experts of each token, the largest logits first, and their gating weights, as moe_route chooses and weighs
+    them, for any number of tokens: logits [T, E] fp32 or bf16 -> ids int32 [T, k], weights fp32 [T, k].
+    valid: uint8 or bool [T], 0 for padded tokens (ids -1, weights 0)."""
+    s = (_bound or _native()).topk(logits, gating, renormalize, ids, weights, valid, stream)
+    if s:
+        raise MoeError(s, "moe_topk")
+
+
+def moe_topk_grad(logits, ids, dweights, gating: int, renormalize: bool, dlogits, addend=None, stream=None):
+    """dlogits = addend (None: 0) + the gradient of moe_topk's weights, from dweights [T, k], with the choice held
+    fixed.  logits, addend, dlogits: [T, E] of one type; dlogits may be either of the others."""
+    s = (_bound or _native()).topk_grad(logits, ids, dweights, gating, renormalize, dlogits, addend, stream)
+    if s:
+        raise MoeError(s, "moe_topk_grad")
+
+
+def moe_dispatch_rows(x, pos, xs, stream=None):
+    """xs[pos[t, s]] = x[t]: token rows [T, n] to their places [M, n] in the order by expert (moe_expert_order's
+    pos [T, k]; -1: takes no part).  Its gradient is moe_combine_rows without weights."""
+    s = (_bound or _native()).dispatch_rows(x, pos, xs, stream)
+    if s:
+        raise MoeError(s, "moe_dispatch_rows")
+
+
+def moe_combine_rows(o, pos, y, weights=None, addend=None, stream=None):
+    """y[t] = addend[t] + sum_s weights[t, s] o[pos[t, s]] (None: 0 and 1), added in fp32 in the order of the slots.
+    o [M, n], y [T, n], addend [T, n] of y's type (may be y), weights fp32 [T, k]."""
+    s = (_bound or _native()).combine_rows(o, pos, y, weights, addend, stream)
+    if s:
+        raise MoeError(s, "moe_combine_rows")
+
+
+def moe_combine_grad(dy, pos, weights=None, o=None, do=None, dweights=None, stream=None):
+    """The gradient of moe_combine_rows: do[pos[t, s]] = weights[t, s] dy[t] and dweights[t, s] = <o[pos[t, s]], dy[t]>;
+    either may be None, and o without dweights.  do may be o."""
+    s = (_bound or _native()).combine_grad(dy, pos, weights, o, do, dweights, stream)
+    if s:
+        raise MoeError(s, "moe_combine_grad")
+
+
+def moe_matmul_workspace_bytes() -> int:
+    return lib().moe_matmul_workspace_bytes()
+
+
+def moe_matmul(x, w, y, ws, act: int = ACT_NONE, bias=None, residual=None, z=None, offsets=None, rows=None,
+               transposed: bool = False, stream=None):
+    """y = act(x @ w.T + bias) + residual, dense or grouped by expert; with an ACT_*_GRAD y = (x @ w.T) act'(z).
+
+    x [X, K] bf16; w [N, K] or [G, N, K] bf16 (transposed: [K, N], [G, K, N]); y [M, N] fp32 or bf16; bias fp32
+    [N] or [G, N]; residual [M, N] of y's type (may be y).  ACT_SWIGLU: w and bias have 2 N rows, gate then up.
+    z of y's type: what the activation takes, out ([M, N], ACT_SWIGLU [M, 2 N]); the gradients' input.
+    ACT_SWIGLU_GRAD: y is [M, 2 N].  offsets int32 [G + 1]: the places of y of each group (moe_expert_order);
+    rows int32 [M]: the row of x of each place (None: the place itself)."""
+    s = (_bound or _native()).matmul(x, w, y, ws, act, bias, residual, z, offsets, rows, transposed, stream)
+    if s:
+        raise MoeError(s, "moe_matmul")
 
 
 def moe_debug_set_exchange_wait(cycles: int):

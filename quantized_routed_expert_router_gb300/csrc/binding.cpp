@@ -251,8 +251,142 @@ PyObject *fp8_matmul(PyObject *, PyObject *const *a, Py_ssize_t have) {
     });
 }
 
+// logits, gating, renormalize, ids, weights, valid, stream
+PyObject *topk(PyObject *, PyObject *const *a, Py_ssize_t have) {
+    return entry(have, 7, [&] {
+        const at::Tensor &l = *tensor(a[0], "logits"), &ids = *tensor(a[3], "ids");
+        lead(l, "logits", 2, {F32, BF16}, "[T, E]");
+        lead(ids, "ids", 2, {I32}, "[T, k]");
+        const int64_t T = l.size(0), E = l.size(1), k = ids.size(1);
+        const int dev = (int)l.get_device(), gating = integer(a[1], "gating"), renorm = integer(a[2], "renormalize");
+        void *out = expect(a[3], "ids", {T, k}, {I32}, dev);
+        void *w = expect(a[4], "weights", {T, k}, {F32}, dev);
+        void *valid = expect(a[5], "valid", {T}, {U8, ScalarType::Bool}, dev);
+        return launch("moe_topk", dev, a[6], [&](cudaStream_t s) {
+            return moe_topk(l.data_ptr(), dtype_of(&l), (const uint8_t *)valid, size_of(T), size_of(E), size_of(k),
+                            (moe_gating)gating, renorm, (int32_t *)out, (float *)w, s);
+        });
+    });
+}
+
+// logits, ids, dweights, gating, renormalize, dlogits, addend, stream
+PyObject *topk_grad(PyObject *, PyObject *const *a, Py_ssize_t have) {
+    return entry(have, 8, [&] {
+        const at::Tensor &l = *tensor(a[0], "logits"), &ids = *tensor(a[1], "ids");
+        lead(l, "logits", 2, {F32, BF16}, "[T, E]");
+        lead(ids, "ids", 2, {I32}, "[T, k]");
+        const int64_t T = l.size(0), E = l.size(1), k = ids.size(1);
+        const int dev = (int)l.get_device();
+        void *in = expect(a[1], "ids", {T, k}, {I32}, dev);
+        void *dw = expect(a[2], "dweights", {T, k}, {F32}, dev);
+        const int gating = integer(a[3], "gating"), renorm = integer(a[4], "renormalize");
+        void *d = expect(a[5], "dlogits", l.sizes(), {l.scalar_type()}, dev);
+        void *add = expect(a[6], "addend", l.sizes(), {l.scalar_type()}, dev);
+        return launch("moe_topk_grad", dev, a[7], [&](cudaStream_t s) {
+            return moe_topk_grad(l.data_ptr(), dtype_of(&l), (const int32_t *)in, (const float *)dw, size_of(T), size_of(E),
+                                 size_of(k), (moe_gating)gating, renorm, add, d, s);
+        });
+    });
+}
+
+// x, pos, xs, stream
+PyObject *dispatch_rows(PyObject *, PyObject *const *a, Py_ssize_t have) {
+    return entry(have, 4, [&] {
+        const at::Tensor &x = *tensor(a[0], "x"), &pos = *tensor(a[1], "pos"), &xs = *tensor(a[2], "xs");
+        lead(x, "x", 2, {F32, BF16}, "[T, n]");
+        lead(pos, "pos", 2, {I32}, "[T, k]");
+        lead(xs, "xs", 2, {x.scalar_type()}, "[M, n]");
+        const int64_t T = x.size(0), n = x.size(1), k = pos.size(1), M = xs.size(0);
+        const int dev = (int)x.get_device();
+        void *p = expect(a[1], "pos", {T, k}, {I32}, dev);
+        void *to = expect(a[2], "xs", {M, n}, {x.scalar_type()}, dev);
+        return launch("moe_dispatch_rows", dev, a[3], [&](cudaStream_t s) {
+            return moe_dispatch_rows(x.data_ptr(), dtype_of(&x), (const int32_t *)p, size_of(T), size_of(k), size_of(n),
+                                     size_of(M), to, s);
+        });
+    });
+}
+
+// o, pos, y, weights, addend, stream
+PyObject *combine_rows(PyObject *, PyObject *const *a, Py_ssize_t have) {
+    return entry(have, 6, [&] {
+        const at::Tensor &o = *tensor(a[0], "o"), &pos = *tensor(a[1], "pos"), &y = *tensor(a[2], "y");
+        lead(o, "o", 2, {F32, BF16}, "[M, n]");
+        lead(pos, "pos", 2, {I32}, "[T, k]");
+        lead(y, "y", 2, {F32, BF16}, "[T, n]");
+        const int64_t T = pos.size(0), k = pos.size(1), n = o.size(1), M = o.size(0);
+        const int dev = (int)o.get_device();
+        void *p = expect(a[1], "pos", {T, k}, {I32}, dev);
+        void *out = expect(a[2], "y", {T, n}, {F32, BF16}, dev);
+        void *w = expect(a[3], "weights", {T, k}, {F32}, dev);
+        void *add = expect(a[4], "addend", {T, n}, {y.scalar_type()}, dev);
+        return launch("moe_combine_rows", dev, a[5], [&](cudaStream_t s) {
+            return moe_combine_rows(o.data_ptr(), dtype_of(&o), (const int32_t *)p, (const float *)w, size_of(T), size_of(k),
+                                    size_of(n), size_of(M), add, out, dtype_of(&y), s);
+        });
+    });
+}
+
+// dy, pos, weights, o, d_o, dweights, stream
+PyObject *combine_grad(PyObject *, PyObject *const *a, Py_ssize_t have) {
+    return entry(have, 7, [&] {
+        const at::Tensor &dy = *tensor(a[0], "dy"), &pos = *tensor(a[1], "pos");
+        lead(dy, "dy", 2, {F32, BF16}, "[T, n]");
+        lead(pos, "pos", 2, {I32}, "[T, k]");
+        const int64_t T = dy.size(0), n = dy.size(1), k = pos.size(1);
+        const int dev = (int)dy.get_device();
+        const at::Tensor *o = tensor(a[3], "o", true), *d = tensor(a[4], "do", true);
+        const at::Tensor *rows = o ? o : d;   // whose rows the places are
+        if (!rows) refuse("do: want do, or dweights with o");
+        lead(*rows, o ? "o" : "do", 2, {F32, BF16}, "[M, n]");
+        const int64_t M = rows->size(0);
+        void *p = expect(a[1], "pos", {T, k}, {I32}, dev);
+        void *w = expect(a[2], "weights", {T, k}, {F32}, dev);
+        void *op = expect(a[3], "o", {M, n}, {rows->scalar_type()}, dev);
+        void *dp = expect(a[4], "do", {M, n}, {rows->scalar_type()}, dev);
+        void *dw = expect(a[5], "dweights", {T, k}, {F32}, dev);
+        return launch("moe_combine_grad", dev, a[6], [&](cudaStream_t s) {
+            return moe_combine_grad(dy.data_ptr(), dtype_of(&dy), (const int32_t *)p, (const float *)w, size_of(T),
+                                    size_of(k), size_of(n), size_of(M), op, dtype_of(rows), dp, (float *)dw, s);
+        });
+    });
+}
+
+// x, w, y, ws, act, bias, residual, z, offsets, rows, transposed, stream
+PyObject *matmul(PyObject *, PyObject *const *a, Py_ssize_t have) {
+    return entry(have, 12, [&] {
+        const at::Tensor &x = *tensor(a[0], "x"), &w = *tensor(a[1], "w"), &y = *tensor(a[2], "y");
+        lead(x, "x", 2, {BF16}, "[X, K]");
+        lead(y, "y", 2, {F32, BF16}, "[M, N] ([M, 2 N] with ACT_SWIGLU_GRAD)");
+        if (w.dim() != 2 && w.dim() != 3) refuse("w: want [N, K] or [G, N, K] (transposed: [K, N] or [G, K, N])");
+        const int act = integer(a[4], "act"), transposed = integer(a[10], "transposed");
+        const int64_t X = x.size(0), K = x.size(1), M = y.size(0), G = w.dim() == 3 ? w.size(0) : 1;
+        const int64_t wide = w.size(transposed ? -1 : -2);   // columns of the product
+        if (act == MOE_ACT_SWIGLU && wide % 2) refuse("w: want gate rows and as many up rows");
+        const int64_t N = act == MOE_ACT_SWIGLU ? wide / 2 : wide, yn = act == MOE_ACT_SWIGLU_GRAD ? 2 * N : N;
+        const int64_t zn = act == MOE_ACT_SWIGLU || act == MOE_ACT_SWIGLU_GRAD ? 2 * N : N;
+        const int dev = (int)x.get_device();
+        const int64_t ws3[3] = {G, transposed ? K : wide, transposed ? wide : K}, b2[2] = {G, wide};
+        const size_t skip = w.dim() == 3 ? 0 : 1;
+        void *wp = expect(a[1], "w", at::IntArrayRef(ws3 + skip, 3 - skip), {BF16}, dev);
+        void *yp = expect(a[2], "y", {M, yn}, {F32, BF16}, dev);
+        const Bytes ws = buffer(a[3], "ws", dev);
+        void *bias = expect(a[5], "bias", at::IntArrayRef(b2 + skip, 2 - skip), {F32}, dev);
+        void *res = expect(a[6], "residual", {M, N}, {y.scalar_type()}, dev);
+        void *z = expect(a[7], "z", {M, zn}, {y.scalar_type()}, dev);
+        void *offsets = expect(a[8], "offsets", {G + 1}, {I32}, dev);
+        void *rows = expect(a[9], "rows", {M}, {I32}, dev);
+        return launch("moe_matmul", dev, a[11], [&](cudaStream_t s) {
+            return moe_matmul(x.data_ptr(), size_of(X), (const int32_t *)rows, size_of(M), (const int32_t *)offsets,
+                              size_of(G), wp, transposed, (const float *)bias, (moe_act)act, res, z, size_of(N), size_of(K),
+                              yp, dtype_of(&y), ws.p, ws.n, s);
+        });
+    });
+}
+
 #define CALL(f) {#f, (PyCFunction)(void (*)(void))f, METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {CALL(add_rmsnorm), CALL(expert_order), CALL(balance_loss), CALL(fp8_matmul), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {CALL(add_rmsnorm), CALL(expert_order), CALL(balance_loss), CALL(fp8_matmul), CALL(topk),
+                         CALL(topk_grad), CALL(dispatch_rows), CALL(combine_rows), CALL(combine_grad), CALL(matmul), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -8,6 +8,7 @@
 #include "moe_around.h"
 #include "moe_common.cuh"
 #include "moe_launch.h"
+#include "moe_matmul.cuh"
 
 using namespace moe;
 
@@ -65,6 +66,17 @@ bool pool_ok(const moe_pool *p, bool shared) {
 bool pool_shape_ok(const moe_pool *p) {
     if (!cols_ok(p->qtype, p->H) || !cols_ok(p->qtype, p->I)) return false;
     return act_block(p->H) != 0 && act_block(p->I) != 0;
+}
+
+bool topk_ok(int T, int E, int k, int dtype, int gating) {
+    if (T < 0 || T > MOE_MAX_ROWS || E < 1 || E > MOE_MAX_EXPERTS || k < 1 || k > E || k > MOE_MAX_K) return false;
+    return dtype_ok(dtype) && (gating == MOE_GATE_SOFTMAX || gating == MOE_GATE_SIGMOID);
+}
+
+bool rows_ok(int T, int k, int n, int M) {
+    if (T < 0 || T > MOE_MAX_ROWS || M < 0 || M > MOE_MAX_ROWS || k < 1 || k > MOE_MAX_K) return false;
+    if (n < 1 || n > 65536 || (long long)T * k > MOE_MAX_PAIRS) return false;
+    return (long long)T * n <= (1ll << 36) && (long long)M * n <= (1ll << 36);
 }
 
 }  // namespace
@@ -281,6 +293,99 @@ moe_status moe_fp8_matmul(const void *x8, const float *x_scale, int X, const int
     if (!ws || ws_bytes < moe_fp8_matmul_workspace_bytes() || !aligned16(ws)) return MOE_ERR_WORKSPACE;
     return cuda_status(launch_fp8(x8, x_scale, X, rows, M, offsets, G, w, w_scale, N, K, y, ydtype, (unsigned *)ws,
                                   stream));
+}
+
+moe_status moe_topk(const void *logits, moe_dtype dtype, const uint8_t *valid, int T, int E, int k, moe_gating gating,
+                    int renormalize, int32_t *ids, float *weights, cudaStream_t stream) {
+    if (!topk_ok(T, E, k, dtype, gating)) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if (!logits || !aligned16(logits) || !ids || !aligned4(ids) || !aligned4(weights)) return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_topk(logits, dtype, valid, T, E, k, gating, renormalize, ids, weights, stream));
+}
+
+moe_status moe_topk_grad(const void *logits, moe_dtype dtype, const int32_t *ids, const float *dweights, int T, int E,
+                         int k, moe_gating gating, int renormalize, const void *addend, void *dlogits,
+                         cudaStream_t stream) {
+    if (!topk_ok(T, E, k, dtype, gating)) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if (!logits || !ids || !dweights || !dlogits) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(logits) || !aligned16(addend) || !aligned16(dlogits)) return MOE_ERR_INVALID_ARG;
+    if (!aligned4(ids) || !aligned4(dweights)) return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_topk_grad(logits, dtype, ids, dweights, T, E, k, gating, renormalize, addend, dlogits,
+                                        stream));
+}
+
+moe_status moe_dispatch_rows(const void *x, moe_dtype dtype, const int32_t *pos, int T, int k, int n, int M, void *xs,
+                             cudaStream_t stream) {
+    if (!rows_ok(T, k, n, M) || !dtype_ok(dtype)) return MOE_ERR_INVALID_ARG;
+    if (T == 0 || M == 0) return MOE_OK;
+    if (!x || !pos || !xs || !aligned16(x) || !aligned4(pos) || !aligned16(xs)) return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_dispatch_rows(x, dtype, pos, T, k, n, M, xs, stream));
+}
+
+moe_status moe_combine_rows(const void *o, moe_dtype dtype, const int32_t *pos, const float *weights, int T, int k,
+                            int n, int M, const void *addend, void *y, moe_dtype ydtype, cudaStream_t stream) {
+    if (!rows_ok(T, k, n, M) || !dtype_ok(dtype) || !dtype_ok(ydtype)) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if ((!o && M > 0) || !pos || !y) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(o) || !aligned16(addend) || !aligned16(y)) return MOE_ERR_INVALID_ARG;
+    if (!aligned4(pos) || !aligned4(weights)) return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_combine_rows(o, dtype, pos, weights, T, k, n, M, addend, y, ydtype, stream));
+}
+
+moe_status moe_combine_grad(const void *dy, moe_dtype ydtype, const int32_t *pos, const float *weights, int T, int k,
+                            int n, int M, const void *o, moe_dtype dtype, void *d_o, float *dweights,
+                            cudaStream_t stream) {
+    if (!rows_ok(T, k, n, M) || !dtype_ok(dtype) || !dtype_ok(ydtype)) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if (!d_o && !dweights) return M == 0 ? MOE_OK : MOE_ERR_INVALID_ARG;
+    if (!dy || !pos || (dweights && !o && M > 0)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(dy) || !aligned16(o) || !aligned16(d_o)) return MOE_ERR_INVALID_ARG;
+    if (!aligned4(pos) || !aligned4(weights) || !aligned4(dweights)) return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_combine_grad(dy, ydtype, pos, weights, T, k, n, M, o, dtype, d_o, dweights, stream));
+}
+
+size_t moe_matmul_workspace_bytes(void) { return 256; }
+
+moe_status moe_matmul(const void *x, int X, const int32_t *rows, int M, const int32_t *offsets, int G, const void *w,
+                      int transposed, const float *bias, moe_act act, const void *residual, void *z, int N, int K,
+                      void *y, moe_dtype ydtype, void *ws, size_t ws_bytes, cudaStream_t stream) {
+    if (X < 0 || X > MOE_MAX_ROWS || M < 0 || M > MOE_MAX_ROWS || G < 1 || G > MOE_MAX_EXPERTS)
+        return MOE_ERR_INVALID_ARG;
+    if (act < MOE_ACT_NONE || act > MOE_ACT_SWIGLU_GRAD || !dtype_ok(ydtype)) return MOE_ERR_INVALID_ARG;
+    if (N < 1 || N > (1 << 20) || (long long)G * N > (1ll << 30)) return MOE_ERR_INVALID_ARG;
+    if (K < 8 || K > (1 << 20) || K % 8 || (transposed && N % 8)) return MOE_ERR_UNSUPPORTED;
+    if (act == MOE_ACT_SWIGLU && (transposed || N % 16)) return MOE_ERR_UNSUPPORTED;
+    if ((long long)X * K > (1ll << 36)) return MOE_ERR_INVALID_ARG;
+    if (!offsets && G != 1) return MOE_ERR_INVALID_ARG;
+    const bool grad = act >= MOE_ACT_SILU_GRAD;
+    if (grad ? bias || residual : act == MOE_ACT_NONE && z != nullptr) return MOE_ERR_INVALID_ARG;
+    if (M == 0) return MOE_OK;
+    if (X == 0 || (!rows && X < M)) return MOE_ERR_INVALID_ARG;
+    if (!x || !w || !y || (grad && !z)) return MOE_ERR_INVALID_ARG;
+    for (const void *p : {x, w, residual, (const void *)z, (const void *)y})
+        if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
+    if (!aligned4(bias) || !aligned4(rows) || !aligned4(offsets)) return MOE_ERR_INVALID_ARG;
+    if (!ws || ws_bytes < moe_matmul_workspace_bytes() || !aligned16(ws)) return MOE_ERR_WORKSPACE;
+    MatmulArgs a = {};
+    a.x = (const __nv_bfloat16 *)x;
+    a.w = (const __nv_bfloat16 *)w;
+    a.bias = bias;
+    a.rows = rows;
+    a.offsets = offsets;
+    a.residual = residual;
+    a.z = z;
+    a.y = y;
+    a.status = (unsigned *)ws;
+    a.X = X;
+    a.M = M;
+    a.G = G;
+    a.N = N;
+    a.K = K;
+    a.act = act;
+    a.transposed = transposed != 0;
+    a.ybf16 = ydtype == MOE_DT_BF16;
+    return cuda_status(launch_matmul(a, stream));
 }
 
 moe_status moe_debug_hold_fp8_matmul(int hold, long long cycles) {

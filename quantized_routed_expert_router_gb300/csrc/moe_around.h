@@ -1,5 +1,6 @@
 // moe_around.h - internal launcher declarations of the calls around the
-// experts (moe_norm.cu, moe_router_stats.cu, moe_fp8.cu, moe_fp8_rows.cu).
+// experts (moe_norm.cu, moe_router_stats.cu, moe_topk.cu, moe_rows.cu, moe_fp8.cu,
+// moe_fp8_rows.cu, moe_matmul.cu).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -22,6 +23,21 @@ size_t balance_ws_bytes();
 cudaError_t launch_balance(const void *logits, int dtype, const int32_t *counts, const uint8_t *valid, int T, int E,
                            int k, int gating, float alpha, const float *grad_loss, float *loss, void *dlogits,
                            void *ws, cudaStream_t s);
+
+cudaError_t launch_topk(const void *logits, int dtype, const uint8_t *valid, int T, int E, int k, int gating,
+                        int renormalize, int32_t *ids, float *weights, cudaStream_t s);
+cudaError_t launch_topk_grad(const void *logits, int dtype, const int32_t *ids, const float *dweights, int T, int E,
+                             int k, int gating, int renormalize, const void *addend, void *dlogits, cudaStream_t s);
+
+cudaError_t launch_dispatch_rows(const void *x, int dtype, const int32_t *pos, int T, int k, int n, int M, void *xs,
+                                 cudaStream_t s);
+cudaError_t launch_combine_rows(const void *o, int dtype, const int32_t *pos, const float *weights, int T, int k,
+                                int n, int M, const void *addend, void *y, int ydtype, cudaStream_t s);
+cudaError_t launch_combine_grad(const void *dy, int ydtype, const int32_t *pos, const float *weights, int T, int k,
+                                int n, int M, const void *o, int dtype, void *d_o, float *dweights, cudaStream_t s);
+
+struct MatmulArgs;   // moe_matmul.cuh
+cudaError_t launch_matmul(const MatmulArgs &a, cudaStream_t s);
 
 // moe_fp8_matmul: tiles through TMA and tcgen05 (moe_fp8.cu), or few rows (moe_fp8_rows.cu)
 struct Fp8Args {
