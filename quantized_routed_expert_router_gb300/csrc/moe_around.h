@@ -37,7 +37,7 @@ cudaError_t launch_combine_grad(const void *dy, int ydtype, const int32_t *pos, 
                                 int n, int M, const void *o, int dtype, void *d_o, float *dweights, cudaStream_t s);
 
 struct MatmulArgs;   // moe_matmul.cuh
-cudaError_t launch_matmul(const MatmulArgs &a, cudaStream_t s);
+cudaError_t launch_matmul(MatmulArgs a, cudaStream_t s);
 
 // moe_fp8_matmul: tiles through TMA and tcgen05 (moe_fp8.cu), or few rows (moe_fp8_rows.cu)
 struct Fp8Args {

@@ -29,6 +29,7 @@
 #include "moe_around.h"
 #include "moe_common.cuh"
 #include "moe_launch.h"
+#include "moe_tc.cuh"
 
 namespace moe {
 namespace {
@@ -40,9 +41,6 @@ constexpr int HC = 64;              // columns of an accumulating warp
 constexpr int GATHER_THREADS = 64;  // warps 2 and 3
 constexpr int MAX_SPLIT = 8;        // blocks that share a tile's depth
 constexpr int RED_PITCH = BM + 4;   // fp32 partial tiles, column by column; 16-byte pieces free of bank conflicts
-// bound on every device-side wait, in units of 2^16 SM clock cycles (8e8 cycles: under a second), unless the test
-// hook shortens it; waits for copies and products in flight on the way out keep it
-constexpr uint32_t FP8_WAIT = 12207;
 
 // What bounds the tiles is how the sums come back: a TMEM load beside running
 // products takes about 250 cycles however wide it is, so a warp has all of its
@@ -61,19 +59,6 @@ struct Shape {
     // a split tile's part and the sums of a block's share lie over the stages
     static_assert(4 * (BN * RED_PITCH + BM * (BN / 2 + 4)) <= STAGES * STAGE, "");
 };
-// position in the ring of stages
-template <int N>
-struct Ring {
-    int i = 0;
-    uint32_t phase = 0;
-    __device__ __forceinline__ void next() {
-        if (++i == N) {
-            i = 0;
-            phase ^= 1;
-        }
-    }
-};
-
 struct Ctl {
     uint64_t full[6], done[6];   // a stage is loaded; its products are done (the stage is free, the sums are there)
     uint64_t dempty[4], drain;   // a TMEM buffer is read
@@ -85,78 +70,10 @@ struct Ctl {
 
 // ------------------------------------------------------------ PTX helpers
 
-__device__ __forceinline__ uint32_t sa(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void bar_init(uint64_t *b, uint32_t n) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(sa(b)), "r"(n) : "memory");
-}
-__device__ __forceinline__ void bar_expect(uint64_t *b, uint32_t bytes, uint32_t me) {
-    asm volatile(
-        "{\n .reg .pred e;\n setp.ne.u32 e, %2, 0;\n @e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}" ::"r"(
-            sa(b)), "r"(bytes), "r"(me)
-        : "memory");
-}
-__device__ __forceinline__ void bar_arrive(uint64_t *b, uint32_t me) {
-    asm volatile("{\n .reg .pred e;\n setp.ne.u32 e, %1, 0;\n @e mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(sa(b)),
-                 "r"(me)
-                 : "memory");
-}
-// bits 16 .. 47 of the cycle counter
-__device__ __forceinline__ uint32_t clock_hi() { return (uint32_t)((unsigned long long)clock64() >> 16); }
-__device__ __forceinline__ bool bar_test(uint64_t *b, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok) : "r"(sa(b)), "r"(parity) : "memory");
-    return ok != 0;
-}
-// 1 in one lane of a converged warp.  The single-thread instructions (copies,
-// products, commits, arrivals) are predicated on it in straight code that the
-// whole warp runs: a branch around them costs more than they do (a stage of
-// products took 540 cycles to issue behind a test of the lane number, 260 behind
-// a branch on this, 200 predicated).
-__device__ __forceinline__ uint32_t elect() {
-    uint32_t p;
-    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
-    return p;
-}
-// wait for a phase; false once this block has given up (the first wait to run
-// out says so to the others and in the status word).  Inline: a call would take
-// registers that the accumulating warps do not have.
+// wait for a phase; false once this block has given up.  Inline: a call would take registers that the accumulating warps
+// do not have.
 __device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, Ctl *c, const Fp8Args &a) {
-    if (bar_test(b, parity)) return true;
-    const uint32_t t0 = clock_hi();
-    while (!bar_test(b, parity)) {
-        if (*(volatile int *)&c->abort) return false;
-        if (clock_hi() - t0 > a.wait) {
-            *(volatile int *)&c->abort = 1;
-            atomicOr(a.status, MOE_DEV_TIMEOUT);
-            return false;
-        }
-    }
-    return true;
-}
-// wait on the way out of a block: for its own copies and products in flight,
-// until FP8_WAIT after t0 at most
-__device__ __forceinline__ void bar_settle(uint64_t *b, uint32_t parity, uint32_t t0) {
-    while (!bar_test(b, parity))
-        if (clock_hi() - t0 > FP8_WAIT) return;
-}
-__device__ __forceinline__ void tma_tile(void *dst, const CUtensorMap *m, int x, int y, uint64_t *bar, uint32_t me) {
-    asm volatile(
-        "{\n .reg .pred e;\n setp.ne.u32 e, %5, 0;\n"
-        " @e cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n}" ::"r"(
-            sa(dst)), "l"(m), "r"(x), "r"(y), "r"(sa(bar)), "r"(me)
-        : "memory");
-}
-// 16 bytes, or 16 zeros where `bytes` is 0
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-// shared-memory descriptor of a K-major tile with 128-byte rows and the
-// 128-byte swizzle: 8-row groups 1024 bytes apart
-__device__ __forceinline__ uint64_t tile_desc(uint32_t addr) {
-    return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
-           ((uint64_t)2 << 61);
+    return bar_wait(b, parity, &c->abort, a.wait, a.status);
 }
 __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t add, uint32_t me) {
     asm volatile(
@@ -165,26 +82,6 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t ad, uint64_t bd, u
         "r"(me)
         : "memory");
 }
-__device__ __forceinline__ void mma_commit(uint64_t *bar, uint32_t me) {
-    asm volatile(
-        "{\n .reg .pred e;\n setp.ne.u32 e, %1, 0;\n"
-        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(sa(bar)), "r"(me)
-        : "memory");
-}
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t v[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
-          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
-          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-        : "r"(addr));
-}
-// waits for this thread's loads.  What uses their values is volatile too, so that it stays behind the wait.
-__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 // two sums += {lo, hi} * {s, s}, staying behind the wait for lo and hi
 __device__ __forceinline__ void fma2(uint64_t &acc, uint32_t lo, uint32_t hi, uint64_t ss) {
     asm volatile("{\n .reg .b64 d;\n mov.b64 d, {%1, %2};\n fma.rn.f32x2 %0, d, %3, %0;\n}"
@@ -194,28 +91,6 @@ __device__ __forceinline__ void fma2(uint64_t &acc, uint32_t lo, uint32_t hi, ui
 __device__ __forceinline__ float sum_of(const uint64_t *acc, int i) {
     return __uint_as_float((uint32_t)(acc[i / 2] >> (32 * (i & 1))));
 }
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
-}
-__device__ __forceinline__ float4 ld_peer(uint32_t addr, uint32_t rank) {
-    uint32_t at;
-    float4 v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
-    return v;
-}
-
 // -------------------------------------------------------------- the tile
 
 struct Tile {
@@ -641,22 +516,6 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
 
 // ------------------------------------------------------------------ host
 
-typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_fn() {
-    static const EncodeTiled fn = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return (EncodeTiled)p;
-    }();
-    return fn;
-}
-
 // rows x depth bytes, copied in boxes of `box` rows by 128 bytes
 bool encode(CUtensorMap *m, const void *p, size_t rows, size_t depth, int box) {
     const cuuint64_t dims[2] = {depth, rows}, strides[1] = {depth};
@@ -751,7 +610,7 @@ cudaError_t launch_fp8(const void *x8, const float *x_scale, int X, const int32_
     a.K = K;
     a.KB = (K + BK - 1) / BK;
     a.NB = (N + BK - 1) / BK;
-    a.wait = g_wait > 0 && (g_wait >> 16) < FP8_WAIT ? (uint32_t)(g_wait >> 16) : FP8_WAIT;
+    a.wait = g_wait > 0 && (g_wait >> 16) < kWaitLimit ? (uint32_t)(g_wait >> 16) : kWaitLimit;
     a.hold_copies = g_hold == 1;
     a.hold_products = g_hold == 2;
     if (fp8_few_rows(a)) return launch_fp8_rows(a, ydtype, s);
