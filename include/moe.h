@@ -684,6 +684,12 @@ moe_status moe_debug_set_exchange_wait(long long cycles);
  */
 moe_status moe_debug_hold_fp8_matmul(int hold, long long cycles);
 
+/*
+ * Test hook: the same for moe_matmul launches made after this call (of any number
+ * of places: all of them wait).
+ */
+moe_status moe_debug_hold_matmul(int hold, long long cycles);
+
 const char *moe_status_str(moe_status s);
 
 #ifdef __cplusplus

@@ -28,7 +28,8 @@ EXPORTS = ["moe_act_block", "moe_q8_row_bytes", "moe_packed_bytes", "moe_pack_we
            "moe_add_rmsnorm", "moe_expert_order", "moe_expert_order_workspace_bytes", "moe_balance_loss",
            "moe_balance_loss_workspace_bytes", "moe_fp8_matmul", "moe_fp8_matmul_workspace_bytes",
            "moe_debug_hold_fp8_matmul", "moe_topk", "moe_topk_grad", "moe_dispatch_rows", "moe_combine_rows",
-           "moe_combine_grad", "moe_matmul", "moe_matmul_workspace_bytes"]
+           "moe_combine_grad", "moe_matmul", "moe_matmul_workspace_bytes",
+           "moe_debug_hold_matmul"]
 LAYER_OVERLAP_PREVIOUS = 0x1
 DEV_TIMEOUT, DEV_BAD_ROW = 0x4, 0x8
 DT_F32, DT_BF16 = 0, 1
@@ -132,6 +133,8 @@ def lib():
         L.moe_debug_set_exchange_wait.argtypes = [ctypes.c_longlong]
         L.moe_debug_hold_fp8_matmul.restype = i
         L.moe_debug_hold_fp8_matmul.argtypes = [i, ctypes.c_longlong]
+        L.moe_debug_hold_matmul.restype = i
+        L.moe_debug_hold_matmul.argtypes = [i, ctypes.c_longlong]
         L.moe_status_str.restype = ctypes.c_char_p
         L.moe_status_str.argtypes = [i]
         _lib_handle = L
@@ -424,6 +427,11 @@ def moe_debug_set_exchange_wait(cycles: int):
 def moe_debug_hold_fp8_matmul(hold: int, cycles: int = 0):
     """Test hook: 1 or 2 makes the waits of moe_fp8_matmul's tiles run out after `cycles` (0: default); 0 is off."""
     _check(lib().moe_debug_hold_fp8_matmul(int(hold), int(cycles)), "moe_debug_hold_fp8_matmul")
+
+
+def moe_debug_hold_matmul(hold: int, cycles: int = 0):
+    """Test hook: 1 or 2 makes the waits of moe_matmul run out after `cycles` (0: default); 0 is off."""
+    _check(lib().moe_debug_hold_matmul(int(hold), int(cycles)), "moe_debug_hold_matmul")
 
 
 def moe_read_device_status(ws, clear: bool = True, stream=None) -> int:

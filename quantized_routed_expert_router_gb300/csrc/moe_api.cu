@@ -394,6 +394,12 @@ moe_status moe_debug_hold_fp8_matmul(int hold, long long cycles) {
     return MOE_OK;
 }
 
+moe_status moe_debug_hold_matmul(int hold, long long cycles) {
+    if (hold < 0 || hold > 2 || cycles < 0) return MOE_ERR_INVALID_ARG;
+    hold_matmul(hold, cycles);
+    return MOE_OK;
+}
+
 moe_status moe_read_device_status(void *ws, int clear, uint32_t *flags, cudaStream_t stream) {
     if (!ws || !flags) return MOE_ERR_INVALID_ARG;
     uint32_t v = 0;

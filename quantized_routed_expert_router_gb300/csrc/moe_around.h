@@ -38,6 +38,7 @@ cudaError_t launch_combine_grad(const void *dy, int ydtype, const int32_t *pos, 
 
 struct MatmulArgs;   // moe_matmul.cuh
 cudaError_t launch_matmul(MatmulArgs a, cudaStream_t s);
+void hold_matmul(int hold, long long cycles);   // moe_debug_hold_matmul
 
 // moe_fp8_matmul: tiles through TMA and tcgen05 (moe_fp8.cu), or few rows (moe_fp8_rows.cu)
 struct Fp8Args {

@@ -1,28 +1,35 @@
 // moe_matmul.cu - products of bf16 rows with bf16 matrices, dense or grouped by
 // expert, with bias, activation and residual in the epilogue (moe_matmul).
 //
-// A tile is 128 columns of a matrix by up to BT places of one group.  The columns
-// are the rows of the tensor cores' first operand, the places the columns of the
+// A tile is 128 columns of a matrix a block by up to BT places of one group.  The
+// columns are the rows of the tensor cores' first operand, the places the columns of the
 // second: TMEM then gives a lane a column and a register a place, so that
 //   - the number of places of a product follows the tile's (16, 32, .. BT);
 //   - a lane has its bias in a register, and what a warp reads or writes of a
 //     place is 32 columns side by side, wherever rows of y start: nothing is
 //     turned in shared memory and no row of another group is touched.
-// With the gated activation a tile takes 64 columns of y: gate and up rows in
+// With the gated activation a block's 128 columns are 64 of y: gate and up rows in
 // turns of 16, by one copy whose map has the two as a dimension, so that lanes l
 // and l + 16 of a warp hold the gate and the up value of a column.
 //
 // The warps of a block have roles:
 //   warp 0    : TMA copies of matrix tiles, and of rows that lie in order (64
 //               values deep, 128-byte swizzle), into a ring of stages
-//   warp 1    : one thread issues the products; the sums of a tile stay in one of
-//               the TMEM buffers for the whole depth
+//   warp 1    : one thread issues the products into one of the TMEM buffers
 //   warps 2-3 : rows that are gathered, by 16-byte asynchronous copies that
 //               signal the stage when they land
 //   warps 4-11: the epilogue, while the products of the next tile run
-// Blocks are persistent, one an SM.  Where there are too few tiles for the SMs a
-// cluster of blocks splits the depth of a tile and adds its parts through
-// distributed shared memory in rank order.
+// Blocks are persistent, one an SM.
+//   Pairs: two blocks share a tile of 256 columns by 256 places.  Each holds its 128
+// columns and half of the places; the first one issues products that read both
+// halves (cta_group::2).  The other's warp 1 passes on that its stage is loaded.
+//   Split depth: where there are too few tiles for the SMs, a cluster of blocks
+// splits the depth of a tile and adds its parts through distributed shared memory
+// in rank order.
+//
+// Sums.  The tensor cores cut off what they add below the 24 bits of a running sum, always towards
+// zero: over K values that is about K 2^-34 of the sum, 1.7e-6 at K = 2048.  Beside a rounding to bf16 it does
+// not count.  For fp32 results (TY = float) a running sum is 512 values of depth long and these are added in fp32.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -41,20 +48,24 @@ constexpr int THREADS = 32 * (EPI_FIRST + EPI_WARPS);
 constexpr int GATHER_THREADS = 64;  // warps 2 and 3
 constexpr int MAX_SPLIT = 8;        // blocks that share a tile's depth
 constexpr int MAX_STAGES = 10;
+constexpr int RUN = 8;              // stages of a running sum of fp32 results
 
-template <int BT>
+template <int BT, bool PAIR>
 struct Shape {
-    static constexpr int STAGES = BT == 256 ? 4 : BT == 128 ? 6 : 10;
-    static constexpr int W_BYTES = BN * 2 * BK, X_BYTES = BT * 2 * BK, STAGE = W_BYTES + X_BYTES;
+    static constexpr int PLACES = PAIR ? BT / 2 : BT;   // of a block's stage
+    static constexpr int STAGES = BT == 32 ? 10 : 6;
+    static constexpr int W_BYTES = BN * 2 * BK, X_BYTES = PLACES * 2 * BK, STAGE = W_BYTES + X_BYTES;
     static constexpr int SMEM = STAGES * STAGE + 1024;   // + alignment of the swizzle pattern
     static constexpr int NBUF = BT == 256 ? 2 : 4;       // TMEM buffers
     static constexpr int COLS = NBUF * BT;
     static constexpr int BOX = BT < 64 ? BT : 64;        // places of a copy
-    static_assert(STAGES <= MAX_STAGES && COLS <= 512 && 4 * BT * BN <= STAGES * STAGE, "");
+    static constexpr int PIECES = BT < 64 ? 1 : BT / 64;   // 32 places each, of an epilogue warp
+    static_assert(STAGES <= MAX_STAGES && COLS <= 512 && (PAIR || 4 * BT * BN <= STAGES * STAGE), "");
 };
 
 struct Ctl {
     uint64_t full[MAX_STAGES], done[MAX_STAGES];   // a stage is loaded; its products are done
+    uint64_t other[MAX_STAGES];                    // the pair's other block has loaded its part of a stage
     uint64_t sums[4], read[4], drain;              // a tile's sums are there; they are read
     uint32_t tmem;
     int abort;
@@ -62,11 +73,46 @@ struct Ctl {
     int tstart[MOE_MAX_EXPERTS + 1];   // first tile of places of each group
 };
 
+template <bool PAIR>
 __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t add, uint32_t me) {
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n .reg .pred e, p;\n setp.ne.u32 e, %5, 0;\n setp.ne.u32 p, %4, 0;\n"
+            " @e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(ad), "l"(bd), "r"(idesc),
+            "r"(add), "r"(me)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred e, p;\n setp.ne.u32 e, %5, 0;\n setp.ne.u32 p, %4, 0;\n"
+            " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(ad), "l"(bd), "r"(idesc),
+            "r"(add), "r"(me)
+            : "memory");
+}
+// the barrier is told when the products so far are done; of a pair, that of either block
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint64_t *bar, uint32_t me) {
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n .reg .pred e;\n setp.ne.u32 e, %1, 0;\n"
+            " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n}" ::"r"(
+                sa(bar)), "r"(me), "h"((uint16_t)3)
+            : "memory");
+    else
+        mma_commit(bar, me);
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t v[16]) {
     asm volatile(
-        "{\n .reg .pred e, p;\n setp.ne.u32 e, %5, 0;\n setp.ne.u32 p, %4, 0;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"(add),
-        "r"(me)
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const float v[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};" ::"r"(addr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
+        "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
         : "memory");
 }
 __device__ __forceinline__ void tma_3d(void *dst, const CUtensorMap *m, int x, int y, int z, uint64_t *bar, uint32_t me) {
@@ -92,11 +138,11 @@ __device__ __forceinline__ uint64_t across_desc(uint32_t addr) {
 }
 
 struct Tile {
-    int g, first, rows, n0;   // group, first place, places (1..BT), first column of y
+    int g, first, rows, n0;   // group, first place, places (1..BT), this block's first column of y
 };
 // tiles of a group: its tiles of places fastest, so that blocks at work at the same time share a matrix tile in L2
-template <int BT>
-__device__ __forceinline__ Tile tile_at(const Ctl *c, const MatmulArgs &a, int t) {
+template <int BT, bool PAIR>
+__device__ __forceinline__ Tile tile_at(const Ctl *c, const MatmulArgs &a, int t, int rank) {
     const int q = t / a.ntn;
     int lo = 0, hi = a.G;     // tstart[lo] <= q < tstart[hi]
     while (hi - lo > 1) {
@@ -107,7 +153,7 @@ __device__ __forceinline__ Tile tile_at(const Ctl *c, const MatmulArgs &a, int t
     const int mt = c->tstart[lo + 1] - c->tstart[lo], local = t - c->tstart[lo] * a.ntn;
     Tile r;
     r.g = lo;
-    r.n0 = local / mt * (a.act == MOE_ACT_SWIGLU ? BN / 2 : BN);
+    r.n0 = (PAIR ? 2 * (local / mt) + rank : local / mt) * (a.act == MOE_ACT_SWIGLU ? BN / 2 : BN);
     r.first = c->goff[lo] + local % mt * BT;
     r.rows = min(BT, c->goff[lo + 1] - r.first);
     return r;
@@ -141,33 +187,45 @@ __device__ __forceinline__ void clear_bad(const MatmulArgs &a, float (&v)[C], in
     }
 }
 
-template <int BT, bool SPLIT>
+// places of a tile that one of a pair's blocks loads (a product takes them in 32s)
+__device__ __forceinline__ int half_of(int rows) { return ((rows + 31) >> 5) << 4; }
+
+template <int BT, bool PAIR, bool SPLIT, typename TY>
 __global__ void __launch_bounds__(THREADS, 1)
     matmul_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw, const MatmulArgs a) {
-    using S = Shape<BT>;
+    using S = Shape<BT, PAIR>;
     constexpr int STAGES = S::STAGES, NBUF = S::NBUF;
+    constexpr bool RUNS = sizeof(TY) == 4;
     extern __shared__ uint8_t raw[];
     __shared__ Ctl c;
     uint8_t *stages = raw + ((1024 - (sa(raw) & 1023)) & 1023);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rank = PAIR || SPLIT ? (int)cluster_rank() : 0, parts = SPLIT ? (int)cluster_size() : 1;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
-            bar_init(&c.full[i], a.rows ? 1 + GATHER_THREADS : 1);   // TMA's copies, and the gathered rows
-            bar_init(&c.done[i], 1);
+            bar_init(&c.full[i], (a.rows ? 1 + GATHER_THREADS : 1) + a.hold_copies);   // TMA's copies, the gathered rows
+            bar_init(&c.done[i], 1 + a.hold_products);
+            bar_init(&c.other[i], 1);
         }
         for (int i = 0; i < NBUF; ++i) {
-            bar_init(&c.sums[i], 1);
-            bar_init(&c.read[i], EPI_WARPS);
+            bar_init(&c.sums[i], 1 + a.hold_products);
+            bar_init(&c.read[i], PAIR ? 2 * EPI_WARPS : EPI_WARPS);
         }
         bar_init(&c.drain, 1);
         c.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sa(&c.tmem)),
-                     "n"(S::COLS) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        if constexpr (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sa(&c.tmem)),
+                         "n"(S::COLS) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sa(&c.tmem)),
+                         "n"(S::COLS) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        }
     }
     if (!a.offsets) {
         if (threadIdx.x == 0) {
@@ -202,13 +260,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync();   // the other block's barriers are there
     fence_after();
     const uint32_t tmem = c.tmem;
     // Rising offsets have fewer than 2^30 tiles (the launch checks it).  Falling ones let groups overlap and can have
     // many more: no more than 2^30 of them, so that tile numbers stay in 32 bits.
     const int total = (int)min((long long)c.tstart[a.G] * a.ntn, 0x3FFFFFFFll);
-    const int rank = SPLIT ? (int)cluster_rank() : 0, parts = SPLIT ? (int)cluster_size() : 1;
-    const int t0 = SPLIT ? (int)blockIdx.x / parts : (int)blockIdx.x, dt = SPLIT ? total : (int)gridDim.x;
+    const int t0 = SPLIT ? (int)blockIdx.x / parts : PAIR ? (int)blockIdx.x / 2 : (int)blockIdx.x;
+    const int dt = SPLIT ? total : PAIR ? (int)gridDim.x / 2 : (int)gridDim.x;
     const int kb0 = SPLIT ? rank * a.KB / parts : 0, kb1 = SPLIT ? (rank + 1) * a.KB / parts : a.KB;
 
     if (warp < EPI_FIRST) {
@@ -219,10 +278,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             int it = 0;
             bool ok = true;
             for (int t = t0; t < total && ok; t += dt) {
-                const Tile tl = tile_at<BT>(&c, a, t);
+                const Tile tl = tile_at<BT, PAIR>(&c, a, t, rank);
                 const int n0 = __shfl_sync(0xFFFFFFFFu, tl.n0, 0), g = __shfl_sync(0xFFFFFFFFu, tl.g, 0);
-                const int first = __shfl_sync(0xFFFFFFFFu, tl.first, 0);
-                const int boxes = a.rows ? 0 : (__shfl_sync(0xFFFFFFFFu, tl.rows, 0) + S::BOX - 1) / S::BOX;
+                const int rows = __shfl_sync(0xFFFFFFFFu, tl.rows, 0), h = PAIR ? half_of(rows) : 0;
+                const int first = __shfl_sync(0xFFFFFFFFu, tl.first, 0) + rank * h;
+                const int mine = PAIR ? (rank ? max(rows - h, 0) : min(rows, h)) : rows;
+                const int boxes = a.rows ? 0 : (mine + S::BOX - 1) / S::BOX;
                 const uint32_t bytes = S::W_BYTES + boxes * S::BOX * 2 * BK;
                 for (int kb = kb0; kb < kb1; ++kb, ++it, r.next()) {
                     ok = bar_wait(&c.done[r.i], r.phase ^ 1, &c.abort, a.wait, a.status);
@@ -248,40 +309,62 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int i = it > STAGES ? it - STAGES : 0; i < it; ++i)
                 bar_settle(ok ? &c.done[i % STAGES] : &c.full[i % STAGES], (i / STAGES) & 1, t_out);
             __syncwarp();
-        } else if (warp == 1) {
+        } else if (warp == 1 && rank && PAIR) {
+            // this block's part of a stage is loaded: the first block may take it
             const uint32_t me = elect();
-            // 16 values of depth: 32 bytes of a row, or 16 rows across
-            const uint64_t step = a.transposed ? 16 * 128 >> 4 : 32 >> 4;
-            const uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a.transposed << 15) | ((uint32_t)(BN >> 4) << 24);
             Ring<STAGES> r;
-            Ring<NBUF> d;
             bool ok = true;
-            for (int t = t0; t < total && ok; t += dt, d.next()) {
-                const int rows = __shfl_sync(0xFFFFFFFFu, tile_at<BT>(&c, a, t).rows, 0);
-                const uint32_t idesc = idesc0 | ((uint32_t)((rows + 15) >> 4) << 18);
-                ok = bar_wait(&c.read[d.i], d.phase ^ 1, &c.abort, a.wait, a.status);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) break;
-                fence_after();
+            for (int t = t0; t < total && ok; t += dt)
                 for (int kb = kb0; kb < kb1; ++kb, r.next()) {
                     ok = bar_wait(&c.full[r.i], r.phase, &c.abort, a.wait, a.status);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
-                    // gathered rows were written through the generic proxy, and the wait made them visible here; the
-                    // products read through the async proxy
                     if (a.rows) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    fence_after();
-                    const uint32_t sw = sa(stages) + r.i * S::STAGE;
-                    const uint64_t ad = a.transposed ? across_desc(sw) : tile_desc(sw), bd = tile_desc(sw + S::W_BYTES);
-#pragma unroll
-                    for (int k = 0; k < BK / 16; ++k)
-                        mma_bf16(tmem + d.i * BT, ad + k * step, bd + 2 * k, idesc, k | (kb - kb0), me);
-                    mma_commit(&c.done[r.i], me);
+                    bar_arrive_at(&c.other[r.i], 0, me);
                 }
-                if (ok) mma_commit(&c.sums[d.i], me);
+            __syncwarp();
+        } else if (warp == 1) {
+            const uint32_t me = elect();
+            // 16 values of depth: 32 bytes of a row, or 16 rows across
+            const uint64_t step = a.transposed ? 16 * 128 >> 4 : 32 >> 4;
+            const uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a.transposed << 15) |
+                                    ((uint32_t)((PAIR ? 2 * BN : BN) >> 4) << 24);
+            Ring<STAGES> r;
+            Ring<NBUF> d;
+            bool ok = true;
+            for (int t = t0; t < total && ok; t += dt) {
+                const int rows = __shfl_sync(0xFFFFFFFFu, (tile_at<BT, PAIR>(&c, a, t, rank).rows), 0);
+                const uint32_t idesc = idesc0 | ((uint32_t)(PAIR ? half_of(rows) >> 3 : (rows + 15) >> 4) << 18);
+                for (int kb = kb0; kb < kb1 && ok;) {
+                    const int first = kb, end = RUNS ? min(kb + RUN, kb1) : kb1;
+                    ok = bar_wait(&c.read[d.i], d.phase ^ 1, &c.abort, a.wait, a.status);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    fence_after();
+                    for (; kb < end; ++kb, r.next()) {
+                        ok = bar_wait(&c.full[r.i], r.phase, &c.abort, a.wait, a.status) &&
+                             (!PAIR || bar_wait(&c.other[r.i], r.phase, &c.abort, a.wait, a.status));
+                        ok = __all_sync(0xFFFFFFFFu, ok);
+                        if (!ok) break;
+                        // gathered rows were written through the generic proxy, and the wait made them visible here; the
+                        // products read through the async proxy
+                        if (a.rows) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        fence_after();
+                        const uint32_t sw = sa(stages) + r.i * S::STAGE;
+                        const uint64_t ad = a.transposed ? across_desc(sw) : tile_desc(sw), bd = tile_desc(sw + S::W_BYTES);
+#pragma unroll
+                        for (int k = 0; k < BK / 16; ++k)
+                            mma_bf16<PAIR>(tmem + d.i * BT, ad + k * step, bd + 2 * k, idesc, k | (kb - first), me);
+                        commit<PAIR>(&c.done[r.i], me);
+                    }
+                    if (ok) {
+                        commit<PAIR>(&c.sums[d.i], me);
+                        d.next();
+                    }
+                }
             }
             if (!ok) {   // products in flight end before TMEM is freed
-                mma_commit(&c.drain, me);
+                commit<PAIR>(&c.drain, me);
                 bar_settle(&c.drain, 0, clock_hi());
             }
             __syncwarp();
@@ -293,14 +376,16 @@ __global__ void __launch_bounds__(THREADS, 1)
             Ring<STAGES> r;
             bool ok = true;
             for (int t = t0; t < total && ok; t += dt) {
-                const Tile tl = tile_at<BT>(&c, a, t);
-                uint32_t row[BT / 8];   // in units of 16 bytes: X K <= 2^36, K / 8 of them a row
+                const Tile tl = tile_at<BT, PAIR>(&c, a, t, rank);
+                const int h = PAIR ? half_of(tl.rows) : 0, first = tl.first + rank * h;
+                const int mine = PAIR ? (rank ? max(tl.rows - h, 0) : min(tl.rows, h)) : tl.rows;
+                uint32_t row[S::PLACES / 8];   // in units of 16 bytes (X K <= 2^36)
 #pragma unroll
-                for (int i = 0; i < BT / 8; ++i) {
-                    const int at = r0 + 8 * i < tl.rows ? a.rows[tl.first + r0 + 8 * i] : 0;
-                    row[i] = (uint32_t)((unsigned)at < (unsigned)a.X ? at : 0);
+                for (int i = 0; i < S::PLACES / 8; ++i) {
+                    const int at = r0 + 8 * i < mine ? a.rows[first + r0 + 8 * i] : 0;
+                    row[i] = (uint32_t)((unsigned)at < (unsigned)a.X ? at : 0) * (uint32_t)(a.K >> 3);
                 }
-                const int nr = (tl.rows - r0 + 7) >> 3;   // of this thread
+                const int nr = (mine - r0 + 7) >> 3;   // of this thread
                 for (int kb = kb0; kb < kb1; ++kb, r.next()) {
                     ok = bar_wait(&c.done[r.i], r.phase ^ 1, &c.abort, a.wait, a.status);
                     ok = __all_sync(0xFFFFFFFFu, ok);
@@ -308,9 +393,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const bool in = kb * BK + 8 * pc < a.K;
                     const uint8_t *src = x + (in ? 2 * (kb * BK + 8 * pc) : 0);
                     const uint32_t bytes = in ? 16 : 0, dst = to + r.i * S::STAGE;
+                    if (nr == S::PLACES / 8) {
 #pragma unroll
-                    for (int i = 0; i < BT / 8; ++i)
-                        if (i < nr) copy16(dst + i * 8 * 2 * BK, src + (size_t)row[i] * (2 * (size_t)a.K), bytes);
+                        for (int i = 0; i < S::PLACES / 8; ++i) copy16(dst + i * 8 * 2 * BK, src + 16 * (uint64_t)row[i], bytes);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < S::PLACES / 8; ++i)
+                            if (i < nr) copy16(dst + i * 8 * 2 * BK, src + 16 * (uint64_t)row[i], bytes);
+                    }
                     // this thread's arrival, once its copies have landed; nobody waits here for them
                     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sa(&c.full[r.i])) : "memory");
                 }
@@ -322,13 +412,53 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t at0 = tmem + ((uint32_t)(32 * quad) << 16);
         Ring<NBUF> d;
         bool ok = true;
-        for (int t = t0; t < total; t += dt, d.next()) {
-            const Tile tl = tile_at<BT>(&c, a, t);
+        // the sums of a buffer are read
+        const auto give_back = [&] {
+            fence_before();
+            if (PAIR) bar_arrive_at(&c.read[d.i], 0, lane == 0);
+            else bar_arrive(&c.read[d.i], lane == 0);
+            d.next();
+        };
+        for (int t = t0; t < total; t += dt) {
+            const Tile tl = tile_at<BT, PAIR>(&c, a, t, rank);
             const Column col = column_of(a, tl, quad, lane);
-            ok = bar_wait(&c.sums[d.i], d.phase, &c.abort, a.wait, a.status);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
-            fence_after();
+            if (RUNS && kb1 - kb0 > RUN) {
+                // every running sum but the last into registers; the last one's buffer gets the whole
+                float acc[S::PIECES][32] = {};
+                for (int kb = kb0; kb < kb1; kb += RUN) {
+                    ok = bar_wait(&c.sums[d.i], d.phase, &c.abort, a.wait, a.status);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    fence_after();
+#pragma unroll
+                    for (int p = 0; p < S::PIECES; ++p)
+#pragma unroll
+                        for (int q = 0; q < 32; q += 16) {
+                            const int j = 32 * half + 64 * p + q;
+                            if (j >= tl.rows) continue;
+                            uint32_t u[16];
+                            tmem_ld16(at0 + d.i * BT + j, u);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) acc[p][q + i] += __uint_as_float(u[i]);
+                        }
+                    if (kb + RUN < kb1) give_back();
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int p = 0; p < S::PIECES; ++p)
+#pragma unroll
+                    for (int q = 0; q < 32; q += 16) {
+                        const int j = 32 * half + 64 * p + q;
+                        if (j < tl.rows) tmem_st16(at0 + d.i * BT + j, acc[p] + q);
+                    }
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            } else {
+                ok = bar_wait(&c.sums[d.i], d.phase, &c.abort, a.wait, a.status);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                fence_after();
+            }
 #pragma unroll 1
             for (int j = 32 * half; j < tl.rows; j += 64) {
                 uint32_t u[32];
@@ -340,7 +470,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) red[i * BN] = __uint_as_float(u[i]);
                 } else {
-                    // (16 at a time, in one piece of code for both: its 14 forms for 32 take minutes to compile)
+                    // (16 at a time, in one piece of code for both: its forms for 32 take minutes to compile)
 #pragma unroll 1
                     for (int h = 0; h < 32 && j + h < tl.rows; h += 16) {
                         float v[16];
@@ -348,13 +478,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                         for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(h ? u[16 + i] : u[i]);
                         const int cnt = min(16, tl.rows - j - h), place = tl.first + j + h;
                         if (a.rows) clear_bad(a, v, place, cnt, lane);
-                        if (a.ybf16) emit_t<__nv_bfloat16>(a, v, cnt, place, col.n, col.in, col.bias, lane);
-                        else emit_t<float>(a, v, cnt, place, col.n, col.in, col.bias, lane);
+                        emit_t<TY>(a, v, cnt, place, col.n, col.in, col.bias, lane);
                     }
                 }
             }
-            fence_before();
-            bar_arrive(&c.read[d.i], lane == 0);
+            give_back();
         }
     }
     if (SPLIT) {
@@ -363,7 +491,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (warp >= EPI_FIRST && t0 < total && !*(volatile int *)&c.abort) {
             // each block takes every parts-th 4 places, and adds them over the cluster in rank order
             const int quad = warp & 3, half = (warp - EPI_FIRST) >> 2;
-            const Tile tl = tile_at<BT>(&c, a, t0);
+            const Tile tl = tile_at<BT, PAIR>(&c, a, t0, rank);
             const Column col = column_of(a, tl, quad, lane);
             const uint32_t red = sa(stages) + 4 * (32 * quad + lane);
 #pragma unroll 1
@@ -383,17 +511,18 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 const int cnt = min(4, tl.rows - j);
                 if (a.rows) clear_bad(a, v, tl.first + j, cnt, lane);
-                if (a.ybf16) emit_t<__nv_bfloat16>(a, v, cnt, tl.first + j, col.n, col.in, col.bias, lane);
-                else emit_t<float>(a, v, cnt, tl.first + j, col.n, col.in, col.bias, lane);
+                emit_t<TY>(a, v, cnt, tl.first + j, col.n, col.in, col.bias, lane);
             }
         }
         cluster_sync();   // parts are read before their block ends
     }
     fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync();   // the first block's products are done, and the other's arrivals there
     if (warp == 1) {
         fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::COLS));
+        if constexpr (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::COLS));
+        else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::COLS));
     }
 }
 
@@ -424,25 +553,26 @@ bool encode_w(CUtensorMap *m, const MatmulArgs &a) {
     return encode(m, 3, a.w, size, stride, box);
 }
 
-template <int BT, bool SPLIT>
-cudaError_t launch_t(const MatmulArgs &a, int grid, int split, cudaStream_t s) {
+template <int BT, bool PAIR, bool SPLIT, typename TY>
+cudaError_t launch_t(const MatmulArgs &a, int grid, int cluster, cudaStream_t s) {
+    using S = Shape<BT, PAIR>;
     CUtensorMap mx, mw;
     const cuuint64_t size[2] = {(cuuint64_t)a.K, (cuuint64_t)a.X}, stride[1] = {2 * (cuuint64_t)a.K};
-    const cuuint32_t box[2] = {BK, (cuuint32_t)Shape<BT>::BOX};
+    const cuuint32_t box[2] = {BK, (cuuint32_t)S::BOX};
     if (!encode_fn()) return cudaErrorSymbolNotFound;
     if (!encode(&mx, 2, a.x, size, stride, box) || !encode_w(&mw, a)) return cudaErrorInvalidValue;
-    auto *k = matmul_kernel<BT, SPLIT>;
-    cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<BT>::SMEM);
+    auto *k = matmul_kernel<BT, PAIR, SPLIT, TY>;
+    cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = Shape<BT>::SMEM;
+    cfg.dynamicSmemBytes = S::SMEM;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
-    if (SPLIT) {
+    if (PAIR || SPLIT) {
         at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = (unsigned)split;
+        at[0].val.clusterDim.x = (unsigned)cluster;
         at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
         cfg.attrs = at;
         cfg.numAttrs = 1;
@@ -450,25 +580,48 @@ cudaError_t launch_t(const MatmulArgs &a, int grid, int split, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, k, mx, mw, a);
 }
 
-}  // namespace
-
-cudaError_t launch_matmul(MatmulArgs a, cudaStream_t s) {
-    a.KB = (a.K + BK - 1) / BK;
-    a.ntn = a.act == MOE_ACT_SWIGLU ? (a.N + 63) / 64 : (a.N + 127) / 128;
-    a.wait = kWaitLimit;
+template <typename TY>
+cudaError_t launch_matmul_t(MatmulArgs a, cudaStream_t s) {
+    const int wide = a.act == MOE_ACT_SWIGLU ? 2 * a.N : a.N;
     // most tiles there can be: a group's last one may be short
     const long long sms = num_sms(), groups = a.offsets ? (a.G < a.M ? a.G : a.M) : 1;
-    const auto tiles = [&](int bt) { return (a.offsets ? a.M / bt + groups : (a.M + bt - 1) / bt) * a.ntn; };
-    if (tiles(32) > 0x3FFFFFFF) return cudaErrorNotSupported;
+    const auto tiles = [&](int bt, int bn) {
+        return (a.offsets ? a.M / bt + groups : (a.M + bt - 1) / bt) * ((wide + bn - 1) / bn);
+    };
+    if (tiles(32, BN) > 0x3FFFFFFF) return cudaErrorNotSupported;
     const long long rows = a.M / groups;   // of a group on average
-    const int bt = rows <= 32 ? 32 : rows > 128 && tiles(256) >= sms ? 256 : 128;
-    const long long n = tiles(bt);
+    const bool pair = rows > 64 && 2 * tiles(256, 2 * BN) >= sms;
+    if (pair) {
+        a.ntn = (wide + 2 * BN - 1) / (2 * BN);
+        const long long n = tiles(256, 2 * BN), most = sms / 2;
+        return launch_t<256, true, false, TY>(a, 2 * (int)(n < most ? n : most), 2, s);
+    }
+    a.ntn = (wide + BN - 1) / BN;
+    const int bt = rows <= 32 ? 32 : 128;
+    const long long n = tiles(bt, BN);
     int split = 1;
     while (split < MAX_SPLIT && n * split * 2 <= sms && a.KB >= split * 8) split *= 2;
     const int grid = (int)(split > 1 ? n * split : n < sms ? n : sms);
-    if (split > 1) return bt == 32 ? launch_t<32, true>(a, grid, split, s) : launch_t<128, true>(a, grid, split, s);
-    if (bt == 32) return launch_t<32, false>(a, grid, 1, s);
-    return bt == 128 ? launch_t<128, false>(a, grid, 1, s) : launch_t<256, false>(a, grid, 1, s);
+    if (split > 1)
+        return bt == 32 ? launch_t<32, false, true, TY>(a, grid, split, s) : launch_t<128, false, true, TY>(a, grid, split, s);
+    return bt == 32 ? launch_t<32, false, false, TY>(a, grid, 1, s) : launch_t<128, false, false, TY>(a, grid, 1, s);
+}
+
+}  // namespace
+
+static long long g_wait = 0;   // 0: the kernel's own bound
+static int g_hold = 0;
+void hold_matmul(int hold, long long cycles) {
+    g_hold = hold;
+    g_wait = cycles;
+}
+
+cudaError_t launch_matmul(MatmulArgs a, cudaStream_t s) {
+    a.KB = (a.K + BK - 1) / BK;
+    a.wait = g_wait > 0 && (g_wait >> 16) < kWaitLimit ? (uint32_t)(g_wait >> 16) : kWaitLimit;
+    a.hold_copies = g_hold == 1;
+    a.hold_products = g_hold == 2;
+    return a.ybf16 ? launch_matmul_t<__nv_bfloat16>(a, s) : launch_matmul_t<float>(a, s);
 }
 
 }  // namespace moe

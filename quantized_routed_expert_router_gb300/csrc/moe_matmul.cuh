@@ -20,7 +20,9 @@ struct MatmulArgs {
     int act, transposed, ybf16;
     int KB;          // blocks of depth
     int ntn;         // column tiles
-    uint32_t wait;   // bound on waits in units of 2^16 cycles
+    // test hook: bound on waits in units of 2^16 cycles; arrivals that never come at a stage's copies, at its products
+    uint32_t wait;
+    int hold_copies, hold_products;
 };
 
 // 1 / (1 + exp(-v)) by the machine's exp and reciprocal: off by (5 + 1.3 |v|) 2^-24 of itself
@@ -45,108 +47,113 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float
 __device__ __forceinline__ void put(float *p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
+// C places of a column, FULL: all of them are there, otherwise the first cnt; rows are `step` values apart
+template <bool FULL, typename TY, int C>
+__device__ __forceinline__ void fetch(const TY *p, size_t step, int cnt, float (&v)[C]) {
+#pragma unroll
+    for (int j = 0; j < C; ++j, p += step) v[j] = FULL || j < cnt ? to_f(*p) : 0.f;
+}
+template <bool FULL, typename TY, int C>
+__device__ __forceinline__ void spread(TY *p, size_t step, int cnt, const float (&v)[C]) {
+#pragma unroll
+    for (int j = 0; j < C; ++j, p += step)
+        if (FULL || j < cnt) put(p, v[j]);
+}
+
 // Products of C places with one column of the tile (lane by lane) to y and z.
-//   v   : the products; of `cnt` places, the first of which is `place`
-//   n   : this lane's column of y; in: it is there
-//   b   : its bias
-// MOE_ACT_SWIGLU: lanes 0 to 15 hold gate columns, lanes 16 to 31 the up columns that belong to them.  Two places at
-// a time, either lane of a pair takes one of them: it gives away its product of the other and gets what it lacks.
-template <int ACT, typename TY, int C>
-__device__ __forceinline__ void emit(const MatmulArgs &a, float (&v)[C], int cnt, int place, int n, bool in, float b,
-                                     int lane) {
+//   v : the products; of `cnt` places, the first of which is `place`
+//   n : this lane's column of y, which is there
+//   b : its bias
+// What a place takes here counts beside the products (a tile of 128 x 256 has 16384 cycles of them at K = 2048): bounds and
+// what is absent are tested once for all places, not at each (30 instructions a value, then 17000 cycles a tile).
+template <int ACT, bool FULL, typename TY, int C>
+__device__ __forceinline__ void emit(const MatmulArgs &a, float (&v)[C], int cnt, int place, int n, float b, int lane) {
     const size_t N = (size_t)a.N;
     TY *y = static_cast<TY *>(a.y), *z = static_cast<TY *>(a.z);
+    const TY *r = static_cast<const TY *>(a.residual);
     if constexpr (ACT == MOE_ACT_SWIGLU) {
+        // Lanes 0 to 15 hold gate columns, lanes 16 to 31 the up columns that belong to them.  Two places at a time, either
+        // lane of a pair takes one of them: it gives away its product of the other and gets what it lacks.
         const int half = lane >> 4;
 #pragma unroll
         for (int j = 0; j < C; ++j) v[j] += b;
-        if (z) {
-            TY *to = z + (size_t)place * 2 * N + half * N + n;
+        if (z) spread<FULL>(z + (size_t)place * 2 * N + half * N + n, 2 * N, cnt, v);
+        float h[C / 2], add[C / 2];
+        const int mine = (cnt + 1 - half) >> 1;   // places that this lane takes
+        if (r) {
+            fetch<FULL>(r + (size_t)(place + half) * N + n, 2 * N, mine, add);
+        } else {
 #pragma unroll
-            for (int j = 0; j < C; ++j)
-                if (in && j < cnt) put(to + (size_t)j * 2 * N, v[j]);
+            for (int j = 0; j < C / 2; ++j) add[j] = 0.f;
         }
-        const TY *r = a.residual ? static_cast<const TY *>(a.residual) + (size_t)place * N + n : nullptr;
-        TY *to = y + (size_t)place * N + n;
 #pragma unroll
-        for (int j0 = 0; j0 < C; j0 += 16) {
-            constexpr int P = C < 16 ? C : 16;
-            float add[P / 2];
-#pragma unroll
-            for (int j = 0; j < P; j += 2)
-                add[j / 2] = r && in && j0 + j + half < cnt ? to_f(r[(size_t)(j0 + j + half) * N]) : 0.f;
-#pragma unroll
-            for (int j = 0; j < P; j += 2) {
-                const float mine = half ? v[j0 + j + 1] : v[j0 + j], other = half ? v[j0 + j] : v[j0 + j + 1];
-                const float got = __shfl_xor_sync(0xFFFFFFFFu, other, 16);
-                const float gate = half ? got : mine, up = half ? mine : got;
-                if (in && j0 + j + half < cnt) put(to + (size_t)(j0 + j + half) * N, silu(gate) * up + add[j / 2]);
-            }
+        for (int j = 0; j < C / 2; ++j) {
+            const float keep = half ? v[2 * j + 1] : v[2 * j];
+            const float got = __shfl_xor_sync(0xFFFFFFFFu, half ? v[2 * j] : v[2 * j + 1], 16);
+            h[j] = silu(half ? got : keep) * (half ? keep : got) + add[j];
         }
+        spread<FULL>(y + (size_t)(place + half) * N + n, 2 * N, mine, h);
     } else if constexpr (ACT == MOE_ACT_SWIGLU_GRAD) {
-        const TY *from = z + (size_t)place * 2 * N + n;
-        TY *to = y + (size_t)place * 2 * N + n;
-        constexpr int P = C < 8 ? C : 8;
+        const size_t at = (size_t)place * 2 * N + n;
+        float g[C], u[C];
+        fetch<FULL>(z + at, 2 * N, cnt, g);
+        fetch<FULL>(z + at + N, 2 * N, cnt, u);
 #pragma unroll
-        for (int j0 = 0; j0 < C; j0 += P) {
-            float g[P], u[P];
-#pragma unroll
-            for (int j = 0; j < P; ++j) {
-                const bool live = in && j0 + j < cnt;
-                g[j] = live ? to_f(from[(size_t)(j0 + j) * 2 * N]) : 0.f;
-                u[j] = live ? to_f(from[(size_t)(j0 + j) * 2 * N + N]) : 0.f;
-            }
-#pragma unroll
-            for (int j = 0; j < P; ++j) {
-                if (!in || j0 + j >= cnt) continue;
-                const float s = sigmoid(g[j]);
-                put(to + (size_t)(j0 + j) * 2 * N, v[j0 + j] * u[j] * (s * (1.f + g[j] * (1.f - s))));
-                put(to + (size_t)(j0 + j) * 2 * N + N, v[j0 + j] * (g[j] * s));
-            }
+        for (int j = 0; j < C; ++j) {
+            const float s = sigmoid(g[j]);
+            u[j] = v[j] * u[j] * (s * (1.f + g[j] * (1.f - s)));
+            g[j] = v[j] * (g[j] * s);
         }
+        spread<FULL>(y + at, 2 * N, cnt, u);
+        spread<FULL>(y + at + N, 2 * N, cnt, g);
     } else {
-        constexpr bool GRAD = ACT == MOE_ACT_SILU_GRAD || ACT == MOE_ACT_GELU_GRAD;
-        const TY *r = static_cast<const TY *>(GRAD ? a.z : a.residual);
-        if (r) r += (size_t)place * N + n;
-        if (z) z += (size_t)place * N + n;
-        y += (size_t)place * N + n;
-        constexpr int P = C < 16 ? C : 16;
+        const size_t at = (size_t)place * N + n;
+        if constexpr (ACT == MOE_ACT_SILU_GRAD || ACT == MOE_ACT_GELU_GRAD) {
+            float f[C];
+            fetch<FULL>(z + at, N, cnt, f);
 #pragma unroll
-        for (int j0 = 0; j0 < C; j0 += P) {
-            float add[P];
+            for (int j = 0; j < C; ++j) v[j] *= ACT == MOE_ACT_SILU_GRAD ? silu_slope(f[j]) : gelu_slope(f[j]);
+        } else {
+            float add[C];
+            if (r) {
+                fetch<FULL>(r + at, N, cnt, add);
+            } else {
 #pragma unroll
-            for (int j = 0; j < P; ++j) add[j] = r && in && j0 + j < cnt ? to_f(r[(size_t)(j0 + j) * N]) : 0.f;
+                for (int j = 0; j < C; ++j) add[j] = 0.f;
+            }
 #pragma unroll
-            for (int j = 0; j < P; ++j) {
-                if (!in || j0 + j >= cnt) continue;
-                float f = v[j0 + j];
-                if constexpr (GRAD) {
-                    f *= ACT == MOE_ACT_SILU_GRAD ? silu_slope(add[j]) : gelu_slope(add[j]);
-                } else {
-                    f += b;
-                    if (ACT != MOE_ACT_NONE && z) put(z + (size_t)(j0 + j) * N, f);
-                    if (ACT == MOE_ACT_SILU) f = silu(f);
-                    if (ACT == MOE_ACT_GELU) f = gelu(f);
-                    f += add[j];
-                }
-                put(y + (size_t)(j0 + j) * N, f);
+            for (int j = 0; j < C; ++j) v[j] += b;
+            if (ACT != MOE_ACT_NONE && z) spread<FULL>(z + at, N, cnt, v);
+#pragma unroll
+            for (int j = 0; j < C; ++j) {
+                if (ACT == MOE_ACT_SILU) v[j] = silu(v[j]);
+                if (ACT == MOE_ACT_GELU) v[j] = gelu(v[j]);
+                v[j] += add[j];
             }
         }
+        spread<FULL>(y + at, N, cnt, v);
     }
 }
 
+template <bool FULL, typename TY, int C>
+__device__ __forceinline__ void emit_f(const MatmulArgs &a, float (&v)[C], int cnt, int place, int n, float b, int lane) {
+    switch (a.act) {
+        case MOE_ACT_NONE: return emit<MOE_ACT_NONE, FULL, TY, C>(a, v, cnt, place, n, b, lane);
+        case MOE_ACT_SILU: return emit<MOE_ACT_SILU, FULL, TY, C>(a, v, cnt, place, n, b, lane);
+        case MOE_ACT_GELU: return emit<MOE_ACT_GELU, FULL, TY, C>(a, v, cnt, place, n, b, lane);
+        case MOE_ACT_SWIGLU: return emit<MOE_ACT_SWIGLU, FULL, TY, C>(a, v, cnt, place, n, b, lane);
+        case MOE_ACT_SILU_GRAD: return emit<MOE_ACT_SILU_GRAD, FULL, TY, C>(a, v, cnt, place, n, b, lane);
+        case MOE_ACT_GELU_GRAD: return emit<MOE_ACT_GELU_GRAD, FULL, TY, C>(a, v, cnt, place, n, b, lane);
+        default: return emit<MOE_ACT_SWIGLU_GRAD, FULL, TY, C>(a, v, cnt, place, n, b, lane);
+    }
+}
+// (with the gated activation N is a multiple of 16, and the lanes of a warp are there or not together)
 template <typename TY, int C>
 __device__ __forceinline__ void emit_t(const MatmulArgs &a, float (&v)[C], int cnt, int place, int n, bool in, float b,
                                        int lane) {
-    switch (a.act) {
-        case MOE_ACT_NONE: return emit<MOE_ACT_NONE, TY, C>(a, v, cnt, place, n, in, b, lane);
-        case MOE_ACT_SILU: return emit<MOE_ACT_SILU, TY, C>(a, v, cnt, place, n, in, b, lane);
-        case MOE_ACT_GELU: return emit<MOE_ACT_GELU, TY, C>(a, v, cnt, place, n, in, b, lane);
-        case MOE_ACT_SWIGLU: return emit<MOE_ACT_SWIGLU, TY, C>(a, v, cnt, place, n, in, b, lane);
-        case MOE_ACT_SILU_GRAD: return emit<MOE_ACT_SILU_GRAD, TY, C>(a, v, cnt, place, n, in, b, lane);
-        case MOE_ACT_GELU_GRAD: return emit<MOE_ACT_GELU_GRAD, TY, C>(a, v, cnt, place, n, in, b, lane);
-        default: return emit<MOE_ACT_SWIGLU_GRAD, TY, C>(a, v, cnt, place, n, in, b, lane);
-    }
+    if (!in) return;
+    if (cnt == C) emit_f<true, TY, C>(a, v, cnt, place, n, b, lane);
+    else emit_f<false, TY, C>(a, v, cnt, place, n, b, lane);
 }
 
 }  // namespace moe

@@ -53,6 +53,15 @@ __device__ __forceinline__ bool bar_test(uint64_t *b, uint32_t parity) {
         : "=r"(ok) : "r"(sa(b)), "r"(parity) : "memory");
     return ok != 0;
 }
+// Arrives at the barrier at the same place in block `rank` of the cluster.  What it stands for are copies and products,
+// which have barriers and fences of their own; ordered for the cluster (release, acquire) it and the wait for it took 2000
+// cycles a stage.
+__device__ __forceinline__ void bar_arrive_at(uint64_t *b, uint32_t rank, uint32_t me) {
+    asm volatile(
+        "{\n .reg .pred e;\n .reg .b32 at;\n setp.ne.u32 e, %2, 0;\n mapa.shared::cluster.u32 at, %0, %1;\n"
+        " @e mbarrier.arrive.shared::cluster.b64 _, [at];\n}" ::"r"(sa(b)), "r"(rank), "r"(me)
+        : "memory");
+}
 // 1 in one lane of a converged warp.  The single-thread instructions (copies,
 // products, commits, arrivals) are predicated on it in straight code that the
 // whole warp runs: a branch around them costs more than they do (a stage of
