@@ -4,105 +4,175 @@
 //
 // A warp takes a row, VEC * J values a lane.  A logit becomes a 32-bit key whose
 // unsigned order is the choice's: larger numbers first, -0 equal to 0, NaN above
-// all, 0 for what may not be taken (-inf, past E, chosen already).  Each of the k
-// rounds finds the largest key of the warp; where several lanes hold it, the one
-// with the lowest index wins.  Slot s of the row ends in lane s.
+// all.  The choice works on keys whose 10 lowest bits are replaced by the expert's
+// index (reversed, so that the lower one wins): one maximum over the warp then names
+// the value and who holds it, no two keys are equal, and a lane keeps its four
+// largest in order, so that a round is a maximum and a shift of the lane that had
+// it.  Slot s of the row ends in lane s.  A row where this may not be exact is done
+// again with whole keys (choose_exactly): two of the k + 1 largest that agree in
+// their upper 22 bits (fp32 logits: one row in a hundred; bf16 ones are exact), or
+// four of the chosen in one lane.  65536 rows of 256, 8 chosen: 63.6 us when every
+// round looked through all values of its lane.
 #include <cuda_bf16.h>
 #include <math.h>
 
 #include "moe_around.h"
 #include "moe_launch.h"
+#include "moe_router.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 8;
 constexpr unsigned kAll = 0xFFFFFFFFu;
+// blocks of a launch that share an SM (registers for the rows in hand); of the gradient, with one row more
+constexpr int grad_blocks(int values) { return values <= 4 ? 5 : values <= 8 ? 4 : values <= 16 ? 2 : 1; }
+constexpr int blocks_per_sm(int values) { return values <= 4 ? 6 : values <= 8 ? 5 : values <= 16 ? 3 : 2; }
+
+constexpr uint32_t kNone = 0x007FFFFFu;   // the key of -inf: what is not above it may not be taken
+constexpr uint32_t kIndex = MOE_MAX_EXPERTS - 1;
 
 __device__ __forceinline__ uint32_t key_of(float v) {
-    const uint32_t u = __float_as_uint(v + 0.f);   // -0 becomes 0
-    if (v != v) return kAll;
-    if (u == 0xFF800000u) return 0;
+    const uint32_t u = __float_as_uint(v + 0.f);   // -0 becomes 0, a NaN the positive one
     return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
-__device__ __forceinline__ float value_of(uint32_t key) {   // -inf for 0
-    if (key == 0) return -INFINITY;
-    return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+__device__ __forceinline__ float sigmoid(float l) {
+    const float z = expf(-fabsf(l));
+    return __fdividef(l < 0.f ? z : 1.f, 1.f + z);   // (a NaN stays one)
 }
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(kAll, v, off);
-    return v;
-}
-__device__ __forceinline__ float exp_fast(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
-    return r;
-}
-// sigma(l) exp(-m) for m = min(l's row's largest, 0): what all of a row's sigmas have in common cancels
-// in their ratios, so that rows whose sigmas would vanish keep theirs
-__device__ __forceinline__ float sigmoid_over(float l, float m) {
-    return l >= 0.f ? 1.f / (1.f + expf(-l)) : expf(l - m) / (1.f + expf(l));
-}
-__device__ __forceinline__ float min0(float v) { return v > 0.f ? 0.f : v; }   // NaN stays
+// sigma(l) exp(-m) for the row's largest m < 0: what all of a row's sigmas have in common cancels in their ratios, so that
+// rows whose sigmas would vanish keep theirs
+__device__ __forceinline__ float sigmoid_over(float l, float m) { return expf(l - m) / (1.f + expf(l)); }
 
-template <typename T, int VEC>
-__device__ __forceinline__ void load_vec(const T *p, float v[VEC]) {
-    if constexpr (VEC == 1) {
-        v[0] = (float)p[0];
-    } else if constexpr (sizeof(T) == 4) {
-        const float4 f = *reinterpret_cast<const float4 *>(p);
-        v[0] = f.x;
-        v[1] = f.y;
-        v[2] = f.z;
-        v[3] = f.w;
-    } else {
-        const uint2 u = *reinterpret_cast<const uint2 *>(p);
-        v[0] = __uint_as_float(u.x << 16);
-        v[1] = __uint_as_float(u.x & 0xFFFF0000u);
-        v[2] = __uint_as_float(u.y << 16);
-        v[3] = __uint_as_float(u.y & 0xFFFF0000u);
+// a row of logits; past E, where load does not come, it is -inf
+template <typename T, int VEC, int J>
+struct Row {
+    Raw<T, VEC> v[J];
+    __device__ __forceinline__ Row() {
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int i = 0; i < (int)(sizeof(v[j].w) / 4); ++i) v[j].w[i] = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;
     }
-}
-template <typename T, int VEC>
-__device__ __forceinline__ void store_vec(T *p, const float v[VEC]) {
-    if constexpr (VEC == 1) {
-        p[0] = (T)v[0];
-    } else if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    } else {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
-        *reinterpret_cast<uint2 *>(p) =
-            make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    __device__ __forceinline__ void load(const T *row, int E, int lane) {
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int e = 32 * VEC * j + VEC * lane;
+            if (e < E) v[j].load(row + e);
+        }
     }
-}
-
-// sum of exp(l - m) over a row
-template <int VEC, int J>
-__device__ __forceinline__ float row_sum(const float l[J][VEC], float m) {
-    float s = 0.f;
+    __device__ __forceinline__ float value(int i) const { return v[i / VEC].value(i % VEC); }   // i: of VEC * J
+    // sum of exp(l - m)
+    __device__ __forceinline__ float sum(float m) const {
+        float s = 0.f;
 #pragma unroll
-    for (int j = 0; j < J; ++j)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) s += exp_fast(l[j][i] - m);
-    return warp_sum(s);
-}
+        for (int i = 0; i < VEC * J; ++i) s += exp_fast(value(i) - m);
+        return warp_sum(s);
+    }
+};
 
-// lane < k holds a chosen logit (-inf: none); m: the largest of the row, all: sum of exp(l - m) over the row where
-// the weights are shares of it.  The slot's weight; slope: 1 - sigma(l), or 1 for softmax
-__device__ __forceinline__ float weight_of(float l, float m, float all, bool sigmoid, bool renorm, float &slope) {
+// Lane < k holds a chosen logit (-inf: none); m: the largest of the row, all: sum of exp(l - m) over the row where
+// the weights are shares of it.  The slot's weight; slope: 1 - sigma(l), or 1 for softmax.
+__device__ __forceinline__ float weight_of(float l, float m, float all, bool sigmoidal, bool renorm, float &slope) {
     const bool some = l != -INFINITY;
     float g;
     slope = 1.f;
-    if (sigmoid) {
-        g = some ? sigmoid_over(l, renorm ? min0(m) : 0.f) : 0.f;
-        slope = some ? sigmoid_over(-l, 0.f) : 0.f;
+    if (sigmoidal) {
+        g = renorm && m < 0.f ? sigmoid_over(l, m) : sigmoid(l);
+        slope = sigmoid(-l);
     } else {
-        g = some ? expf(l - m) : 0.f;
+        g = expf(l - m);
     }
+    if (!some) g = 0.f;
     if (renorm) all = warp_sum(g);
-    else if (sigmoid) return g;
-    return some ? g / all : 0.f;
+    else if (sigmoidal) return g;
+    return some ? __fdividef(g, all) : 0.f;
+}
+
+// a >= b afterwards
+__device__ __forceinline__ void order2(uint32_t &a, uint32_t &b) {
+    const uint32_t m = max(a, b);
+    b = min(a, b);
+    a = m;
+}
+
+// the k largest of a row by whole keys, the expert of slot s in lane s (-1: none): each round finds the largest key of the
+// warp; where several lanes hold it, the one with the lowest index wins
+template <typename T, int VEC, int J>
+__device__ __noinline__ int choose_exactly(const T *logits, int E, int k, int lane) {
+    Row<T, VEC, J> row;
+    row.load(logits, E, lane);
+    uint32_t key[VEC * J];
+#pragma unroll
+    for (int i = 0; i < VEC * J; ++i) key[i] = key_of(row.value(i));
+    int id = -1;
+    for (int s = 0; s < k; ++s) {
+        uint32_t best = 0;
+        int at = 0;   // of this lane's largest: the lowest index
+#pragma unroll
+        for (int i = 0; i < VEC * J; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                at = 32 * VEC * (i / VEC) + VEC * lane + i % VEC;
+            }
+        const uint32_t top = __reduce_max_sync(kAll, best);
+        if (top <= kNone) break;
+        const int e = (int)__reduce_min_sync(kAll, best == top ? (unsigned)at : kAll);
+        if (lane == s) id = e;
+#pragma unroll
+        for (int i = 0; i < VEC * J; ++i)
+            if (32 * VEC * (i / VEC) + VEC * lane + i % VEC == e) key[i] = 0;
+    }
+    return id;
+}
+
+template <typename T, int VEC, int J>
+__device__ __forceinline__ int choose(const T *logits, const Row<T, VEC, J> &row, int E, int k, int lane) {
+    uint32_t a[4] = {0, 0, 0, 0};   // the lane's largest, in order
+#pragma unroll
+    for (int j = 0; j < VEC * J; j += 4) {
+        uint32_t b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int at = j + i, e = 32 * VEC * (at / VEC) + VEC * lane + at % VEC;
+            b[i] = at < VEC * J ? (key_of(row.value(at % (VEC * J))) & ~kIndex) | (kIndex & ~(uint32_t)e) : 0;
+        }
+        order2(b[0], b[1]);
+        order2(b[2], b[3]);
+        order2(b[0], b[2]);
+        order2(b[1], b[3]);
+        order2(b[1], b[2]);
+        if (j == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[i] = b[i];
+        } else {   // the four largest of both: rising and falling, then in order
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[i] = max(a[i], b[3 - i]);
+            order2(a[0], a[2]);
+            order2(a[1], a[3]);
+            order2(a[0], a[1]);
+            order2(a[2], a[3]);
+        }
+    }
+    uint32_t mine = 0, top = 0;
+#pragma unroll 3
+    for (int s = 0; s <= k; ++s) {   // one more than are taken: is the last one's rank certain?
+        top = __reduce_max_sync(kAll, a[0]);
+        mine = lane == s ? top : mine;
+        if (a[0] == top) {
+            a[0] = a[1];
+            a[1] = a[2];
+            a[2] = a[3];
+            a[3] = 0;
+        }
+    }
+    bool unsure = VEC * J > 4 && a[0] == 0;   // (the key of an expert is not 0)
+    if (sizeof(T) == 4) {
+        const uint32_t down = __shfl_down_sync(kAll, mine, 1), next = lane == 31 ? top : down;
+        unsure = unsure || (lane < k && next > kNone && (mine ^ next) <= kIndex);
+    }
+    if (__any_sync(kAll, unsure)) return choose_exactly<T, VEC, J>(logits, E, k, lane);
+    return lane < k && mine > kNone ? (int)(kIndex - (mine & kIndex)) : -1;
 }
 
 struct TopkArgs {
@@ -113,66 +183,39 @@ struct TopkArgs {
     int T, E, k, sigmoid, renorm;
 };
 
+// A warp walks over rows, the next one's loads under way while it works on one.
 template <typename T, int VEC, int J>
-__global__ void __launch_bounds__(32 * kWarps) topk_kernel(const TopkArgs a) {
-    const int lane = threadIdx.x & 31, t = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (t >= a.T) return;
-    int id = -1;
-    float w = 0.f;
-    if (!a.valid || a.valid[t]) {
-        const T *row = static_cast<const T *>(a.logits) + (size_t)t * a.E;
-        float l[J][VEC];
-        uint32_t key[J][VEC];
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const int e = 32 * VEC * j + VEC * lane;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) l[j][i] = -INFINITY;
-            if (e < a.E) load_vec<T, VEC>(row + e, l[j]);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) key[j][i] = key_of(l[j][i]);
-        }
-        uint32_t best = 0, chosen = 0;
-        int at = 0;   // of this lane's largest: the lowest index
-        const auto look = [&] {
-            best = 0;
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-#pragma unroll
-                for (int i = 0; i < VEC; ++i)
-                    if (key[j][i] > best) {
-                        best = key[j][i];
-                        at = 32 * VEC * j + VEC * lane + i;
-                    }
-        };
-        look();
-        for (int s = 0; s < a.k; ++s) {
-            const uint32_t top = __reduce_max_sync(kAll, best);
-            if (top == 0) break;
-            const unsigned who = __ballot_sync(kAll, best == top);
-            int e = __shfl_sync(kAll, at, __ffs(who) - 1);
-            if (who & (who - 1)) e = (int)__reduce_min_sync(kAll, best == top ? (unsigned)at : kAll);
-            if (lane == s) {
-                id = e;
-                chosen = top;
-            }
-            if (best == top && at == e) {
-#pragma unroll
-                for (int j = 0; j < J; ++j)
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i)
-                        if (32 * VEC * j + VEC * lane + i == e) key[j][i] = 0;
-                look();
-            }
-        }
-        const float mine = value_of(chosen), m = __shfl_sync(kAll, mine, 0);
-        const float all = a.sigmoid || a.renorm ? 0.f : row_sum<VEC, J>(l, m);
-        float slope;
-        w = weight_of(mine, m, all, a.sigmoid, a.renorm, slope);
+__global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(VEC * J)) topk_kernel(const TopkArgs a) {
+    const int lane = threadIdx.x & 31, step = gridDim.x * kWarps;
+    const T *logits = static_cast<const T *>(a.logits);
+    Row<T, VEC, J> next;
+    bool next_live = false;
+    int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (t < a.T) {
+        next_live = !a.valid || a.valid[t];
+        next.load(logits + (size_t)t * a.E, a.E, lane);
     }
-    if (lane < a.k) {
-        a.ids[(size_t)t * a.k + lane] = id;
-        if (a.weights) a.weights[(size_t)t * a.k + lane] = w;
+    for (; t < a.T; t += step) {
+        const Row<T, VEC, J> row = next;
+        const bool live = next_live;
+        if (t + step < a.T) {
+            next_live = !a.valid || a.valid[t + step];
+            next.load(logits + (size_t)(t + step) * a.E, a.E, lane);
+        }
+        int id = -1;
+        float w = 0.f;
+        if (live) {
+            const T *at = logits + (size_t)t * a.E;
+            id = choose<T, VEC, J>(at, row, a.E, a.k, lane);
+            const float mine = id >= 0 ? (float)at[id] : -INFINITY, m = __shfl_sync(kAll, mine, 0);
+            const float all = a.sigmoid || a.renorm ? 0.f : row.sum(m);
+            float slope;
+            w = weight_of(mine, m, all, a.sigmoid, a.renorm, slope);
+        }
+        if (lane < a.k) {
+            a.ids[(size_t)t * a.k + lane] = id;
+            if (a.weights) a.weights[(size_t)t * a.k + lane] = w;
+        }
     }
 }
 
@@ -184,79 +227,99 @@ struct TopkGradArgs {
     int T, E, k, sigmoid, renorm;
 };
 
-// ROW: the gradient reaches the whole row (softmax over all E); otherwise the chosen experts
+// ROW: the gradient reaches the whole row (softmax over all E); otherwise the chosen experts.  The next row's slots and
+// logits are under way as in topk_kernel (rows are read before any of them is written: dlogits may be logits, and a
+// row belongs to one warp).
 template <typename T, int VEC, int J, bool ROW>
-__global__ void __launch_bounds__(32 * kWarps) topk_grad_kernel(const TopkGradArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, grad_blocks(VEC * J)) topk_grad_kernel(const TopkGradArgs a) {
     extern __shared__ float buf[];   // a row a warp
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = blockIdx.x * kWarps + warp;
-    if (t >= a.T) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, step = gridDim.x * kWarps;
     float *at = buf + warp * 32 * VEC * J;
-    const T *row = static_cast<const T *>(a.logits) + (size_t)t * a.E;
-    int id = lane < a.k ? a.ids[(size_t)t * a.k + lane] : -1;
-    if ((unsigned)id >= (unsigned)a.E) id = -1;
-    const float mine = id >= 0 ? (float)row[id] : -INFINITY;
-    const float d = id >= 0 ? a.dweights[(size_t)t * a.k + lane] : 0.f;
-    uint32_t top = key_of(mine);
-    float l[J][VEC], all = 0.f;
-    if constexpr (ROW) {
+    const T *logits = static_cast<const T *>(a.logits), *addend = static_cast<const T *>(a.addend);
+    Row<T, VEC, J> next, next_add;
+    int next_id = -1;
+    float next_d = 0.f;
+    const auto fetch = [&](int t) {
+        if (lane < a.k) {
+            next_id = a.ids[(size_t)t * a.k + lane];
+            next_d = a.dweights[(size_t)t * a.k + lane];
+        }
+        if (ROW) next.load(logits + (size_t)t * a.E, a.E, lane);
+        if (addend) next_add.load(addend + (size_t)t * a.E, a.E, lane);
+    };
+    int t = blockIdx.x * kWarps + warp;
+    if (t < a.T) fetch(t);
+    for (; t < a.T; t += step) {
+        const Row<T, VEC, J> row = next, add = next_add;
+        const int id = (unsigned)next_id < (unsigned)a.E ? next_id : -1;
+        const float d = id >= 0 ? next_d : 0.f;
+        const float mine = id >= 0 ? (float)logits[(size_t)t * a.E + id] : -INFINITY;
+        if (t + step < a.T) fetch(t + step);
+        float m = mine;
+        if (ROW) {
+#pragma unroll
+            for (int i = 0; i < VEC * J; ++i) m = max_nan(m, row.value(i));
+        }
+        m = warp_max(m);
+        const float all = ROW ? row.sum(m) : 0.f;
+        float slope;
+        const float w = weight_of(mine, m, all, a.sigmoid, a.renorm, slope);
+        const bool ratio = a.renorm || !a.sigmoid;
+        const float dot = ratio ? warp_sum(id >= 0 ? w * d : 0.f) : 0.f;
+        // the row's gradient at the chosen experts; where an id comes twice (one of its slots finds the other's mark),
+        // slot by slot in their order
+        const float g = ROW ? w * d : slope * w * (d - dot);
+        __syncwarp();
+        if (id >= 0) at[id] = __int_as_float(lane);
+        __syncwarp();
+        const bool twice = __any_sync(kAll, id >= 0 && __float_as_int(at[id]) != lane);
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) at[32 * VEC * j + VEC * lane + i] = 0.f;
+        __syncwarp();
+        if (!twice) {
+            if (id >= 0) at[id] = g;
+        } else {
+            for (int s = 0; s < a.k; ++s) {
+                if (lane == s && id >= 0) at[id] += g;
+                __syncwarp();
+            }
+        }
+        __syncwarp();
+        const float scale = ROW ? dot / all : 0.f;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             const int e = 32 * VEC * j + VEC * lane;
+            if (e >= a.E) continue;
+            float v[VEC];
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) l[j][i] = -INFINITY;
-            if (e < a.E) load_vec<T, VEC>(row + e, l[j]);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) top = max(top, key_of(l[j][i]));
-        }
-    }
-    const float m = value_of(__reduce_max_sync(kAll, top));
-    if constexpr (ROW) all = row_sum<VEC, J>(l, m);
-    float slope;
-    const float w = weight_of(mine, m, all, a.sigmoid, a.renorm, slope);
-    const bool ratio = a.renorm || !a.sigmoid;
-    const float dot = ratio ? warp_sum(id >= 0 ? w * d : 0.f) : 0.f;
-    // the row's gradient at the chosen experts, slot by slot: an id that comes twice is added up in order
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) at[32 * VEC * j + VEC * lane + i] = 0.f;
-    __syncwarp();
-    const float g = ROW ? w * d : slope * w * (d - dot);
-    for (int s = 0; s < a.k; ++s) {
-        if (lane == s && id >= 0) at[id] += g;
-        __syncwarp();
-    }
-    const float scale = ROW ? dot / all : 0.f;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-        const int e = 32 * VEC * j + VEC * lane;
-        if (e >= a.E) continue;
-        float v[VEC];
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = 0.f;
-        if (a.addend) load_vec<T, VEC>(static_cast<const T *>(a.addend) + (size_t)t * a.E + e, v);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            float g = at[e + i];
-            if constexpr (ROW) {
+            for (int i = 0; i < VEC; ++i) {
+                v[i] = at[e + i];
                 // a row without slots has no gradient, whatever its logits are
-                if (dot != 0.f && l[j][i] != -INFINITY) g -= exp_fast(l[j][i] - m) * scale;
+                if (ROW && dot != 0.f && row.value(VEC * j + i) != -INFINITY)
+                    v[i] -= exp_fast(row.value(VEC * j + i) - m) * scale;
+                if (addend) v[i] += add.v[j].value(i);
             }
-            v[i] += g;
+            store_vec<T, VEC>(static_cast<T *>(a.dlogits) + (size_t)t * a.E + e, v);
         }
-        store_vec<T, VEC>(static_cast<T *>(a.dlogits) + (size_t)t * a.E + e, v);
     }
 }
 
+unsigned blocks(int rows, int per_sm) {
+    const long long need = ((long long)rows + kWarps - 1) / kWarps, most = (long long)num_sms() * per_sm;
+    return (unsigned)(need < most ? need : most);
+}
 template <typename T, int VEC, int J>
 cudaError_t topk_t(const TopkArgs &a, cudaStream_t s) {
-    topk_kernel<T, VEC, J><<<(unsigned)((a.T + kWarps - 1) / kWarps), 32 * kWarps, 0, s>>>(a);
+    topk_kernel<T, VEC, J><<<blocks(a.T, blocks_per_sm(VEC * J)), 32 * kWarps, 0, s>>>(a);
     return cudaGetLastError();
 }
 template <typename T, int VEC, int J>
 cudaError_t topk_t(const TopkGradArgs &a, cudaStream_t s) {
-    constexpr int smem = kWarps * 32 * VEC * J * (int)sizeof(float);   // 16 KB at most
-    const unsigned grid = (unsigned)((a.T + kWarps - 1) / kWarps);
+    constexpr int smem = kWarps * 32 * VEC * J * (int)sizeof(float);   // 32 KB at most
+    const unsigned grid = blocks(a.T, grad_blocks(VEC * J));
     if (!a.sigmoid && !a.renorm) topk_grad_kernel<T, VEC, J, true><<<grid, 32 * kWarps, smem, s>>>(a);
     else topk_grad_kernel<T, VEC, J, false><<<grid, 32 * kWarps, smem, s>>>(a);
     return cudaGetLastError();
