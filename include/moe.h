@@ -685,8 +685,8 @@ moe_status moe_debug_set_exchange_wait(long long cycles);
 moe_status moe_debug_hold_fp8_matmul(int hold, long long cycles);
 
 /*
- * Test hook: the same for moe_matmul launches made after this call (of any number
- * of places: all of them wait).
+ * Test hook: the same for moe_matmul launches made after this call (those of more
+ * than 16 places or with transposed; others wait for nothing).
  */
 moe_status moe_debug_hold_matmul(int hold, long long cycles);
 

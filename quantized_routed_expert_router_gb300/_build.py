@@ -25,7 +25,7 @@ CALLS_SO = os.path.join(PKG, "_calls.so")
 SOURCES = ["moe_api.cu", "moe_kernels.cu", "moe_ffn.cu", "moe_noalloc.cu", "moe_fused_api.cu",
            "moe_fused_q4k.cu", "moe_fused_q2k.cu", "moe_fused_q80.cu", "moe_fused_mx4.cu", "moe_fused_q6k.cu",
            "moe_fused_q3k.cu", "moe_norm.cu", "moe_router_stats.cu", "moe_topk.cu", "moe_rows.cu", "moe_fp8.cu",
-           "moe_fp8_rows.cu", "moe_matmul.cu"]
+           "moe_fp8_rows.cu", "moe_matmul.cu", "moe_matmul_rows.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,6 +1,6 @@
 // moe_around.h - internal launcher declarations of the calls around the
 // experts (moe_norm.cu, moe_router_stats.cu, moe_topk.cu, moe_rows.cu, moe_fp8.cu,
-// moe_fp8_rows.cu, moe_matmul.cu).
+// moe_fp8_rows.cu, moe_matmul.cu, moe_matmul_rows.cu).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -36,8 +36,11 @@ cudaError_t launch_combine_rows(const void *o, int dtype, const int32_t *pos, co
 cudaError_t launch_combine_grad(const void *dy, int ydtype, const int32_t *pos, const float *weights, int T, int k,
                                 int n, int M, const void *o, int dtype, void *d_o, float *dweights, cudaStream_t s);
 
+// moe_matmul: tiles through TMA and tcgen05 (moe_matmul.cu), or few rows (moe_matmul_rows.cu)
 struct MatmulArgs;   // moe_matmul.cuh
 cudaError_t launch_matmul(MatmulArgs a, cudaStream_t s);
+bool matmul_few_rows(const MatmulArgs &a);
+cudaError_t launch_matmul_rows(const MatmulArgs &a, cudaStream_t s);
 void hold_matmul(int hold, long long cycles);   // moe_debug_hold_matmul
 
 // moe_fp8_matmul: tiles through TMA and tcgen05 (moe_fp8.cu), or few rows (moe_fp8_rows.cu)

@@ -48,12 +48,14 @@ constexpr int THREADS = 32 * (EPI_FIRST + EPI_WARPS);
 constexpr int GATHER_THREADS = 64;  // warps 2 and 3
 constexpr int MAX_SPLIT = 8;        // blocks that share a tile's depth
 constexpr int MAX_STAGES = 10;
-constexpr int RUN = 8;              // stages of a running sum of fp32 results
+// registers a thread: at the launch, and where the epilogue takes some of the feeding warps'
+constexpr int LAUNCH_REGS = 168, FEED_REGS = 88, EPI_REGS = 208;
+constexpr int RUN = 12;             // stages of a running sum of fp32 results
 
 template <int BT, bool PAIR>
 struct Shape {
     static constexpr int PLACES = PAIR ? BT / 2 : BT;   // of a block's stage
-    static constexpr int STAGES = BT == 32 ? 10 : 6;
+    static constexpr int STAGES = BT == 32 ? 10 : PAIR && BT == 128 ? 9 : 6;
     static constexpr int W_BYTES = BN * 2 * BK, X_BYTES = PLACES * 2 * BK, STAGE = W_BYTES + X_BYTES;
     static constexpr int SMEM = STAGES * STAGE + 1024;   // + alignment of the swizzle pattern
     static constexpr int NBUF = BT == 256 ? 2 : 4;       // TMEM buffers
@@ -100,21 +102,6 @@ __device__ __forceinline__ void commit(uint64_t *bar, uint32_t me) {
     else
         mma_commit(bar, me);
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t v[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
-        "[%16];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-        : "r"(addr));
-}
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const float v[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16};" ::"r"(addr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
-        "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
-        : "memory");
-}
 __device__ __forceinline__ void tma_3d(void *dst, const CUtensorMap *m, int x, int y, int z, uint64_t *bar, uint32_t me) {
     asm volatile(
         "{\n .reg .pred e;\n setp.ne.u32 e, %6, 0;\n"
@@ -140,21 +127,26 @@ __device__ __forceinline__ uint64_t across_desc(uint32_t addr) {
 struct Tile {
     int g, first, rows, n0;   // group, first place, places (1..BT), this block's first column of y
 };
-// tiles of a group: its tiles of places fastest, so that blocks at work at the same time share a matrix tile in L2
+// Tiles of a group: its tiles of places fastest, so that blocks at work at the same time share a matrix tile in L2.  Whole
+// column tiles of all groups come first, then those that are cut off by the matrix's end: they take less time, and fill up
+// the last round (3108 rows over 32 of 2880 x 2880: 384 tiles of pairs, 352 of them whole, on 76 pairs).
 template <int BT, bool PAIR>
 __device__ __forceinline__ Tile tile_at(const Ctl *c, const MatmulArgs &a, int t, int rank) {
-    const int q = t / a.ntn;
+    const int whole = (int)((unsigned)c->tstart[a.G] * (unsigned)a.whole);   // (taken where it is at most t)
+    const bool cut = a.whole != a.ntn && (long long)c->tstart[a.G] * a.whole <= t;
+    const int q = cut ? t - whole : t / a.whole;
     int lo = 0, hi = a.G;     // tstart[lo] <= q < tstart[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (c->tstart[mid] <= q) lo = mid;
         else hi = mid;
     }
-    const int mt = c->tstart[lo + 1] - c->tstart[lo], local = t - c->tstart[lo] * a.ntn;
+    const int mt = c->tstart[lo + 1] - c->tstart[lo], local = cut ? q - c->tstart[lo] : t - c->tstart[lo] * a.whole;
+    const int ct = cut ? a.whole : local / mt;
     Tile r;
     r.g = lo;
-    r.n0 = (PAIR ? 2 * (local / mt) + rank : local / mt) * (a.act == MOE_ACT_SWIGLU ? BN / 2 : BN);
-    r.first = c->goff[lo] + local % mt * BT;
+    r.n0 = (PAIR ? 2 * ct + rank : ct) * (a.act == MOE_ACT_SWIGLU ? BN / 2 : BN);
+    r.first = c->goff[lo] + (cut ? local : local % mt) * BT;
     r.rows = min(BT, c->goff[lo + 1] - r.first);
     return r;
 }
@@ -173,6 +165,22 @@ __device__ __forceinline__ Column column_of(const MatmulArgs &a, const Tile &tl,
     const size_t at = gated ? (size_t)tl.g * 2 * a.N + (lane >> 4) * a.N + c.n : (size_t)tl.g * a.N + c.n;
     c.bias = a.bias && c.in ? a.bias[at] : 0.f;
     return c;
+}
+// what the epilogue reads of this warp's places and columns, into L2 while the products run (2048 deep with an fp32
+// residual: 227 us without, of which 150 are without the residual)
+template <typename TY>
+__device__ __forceinline__ void prefetch_rows(const MatmulArgs &a, const Tile &tl, int quad, int half, int lane) {
+    const bool grad = a.act >= MOE_ACT_SILU_GRAD, both = a.act == MOE_ACT_SWIGLU_GRAD, gated = a.act == MOE_ACT_SWIGLU;
+    const TY *p = static_cast<const TY *>(grad ? a.z : a.residual);
+    const int n = tl.n0 + (gated ? 16 : 32) * quad, have = min(gated ? 16 : 32, a.N - n);
+    if (!p || have <= 0) return;
+    const size_t pitch = both ? 2 * (size_t)a.N : (size_t)a.N;
+    for (int j = 32 * half + lane; j < tl.rows; j += 64)
+        for (int h = 0; h <= (both ? 1 : 0); ++h) {
+            const TY *at = p + (size_t)(tl.first + j) * pitch + (size_t)h * a.N + n;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(at + have - 1));
+        }
 }
 // places first .. first + cnt - 1 whose row index is bad: their products are 0
 template <int C>
@@ -270,7 +278,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int dt = SPLIT ? total : PAIR ? (int)gridDim.x / 2 : (int)gridDim.x;
     const int kb0 = SPLIT ? rank * a.KB / parts : 0, kb1 = SPLIT ? (rank + 1) * a.KB / parts : a.KB;
 
+    // Registers: the running sums of fp32 results take 128, beside 32 on their way.
+    constexpr bool MOVE = RUNS && PAIR;
+    static_assert(FEED_REGS * 32 * EPI_FIRST + EPI_REGS * 32 * EPI_WARPS <= LAUNCH_REGS * THREADS, "");
     if (warp < EPI_FIRST) {
+        if (MOVE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FEED_REGS));
         if (warp == 0) {
             const uint32_t me = elect();
             const bool gated = a.act == MOE_ACT_SWIGLU;
@@ -279,10 +291,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             bool ok = true;
             for (int t = t0; t < total && ok; t += dt) {
                 const Tile tl = tile_at<BT, PAIR>(&c, a, t, rank);
-                const int n0 = __shfl_sync(0xFFFFFFFFu, tl.n0, 0), g = __shfl_sync(0xFFFFFFFFu, tl.g, 0);
-                const int rows = __shfl_sync(0xFFFFFFFFu, tl.rows, 0), h = PAIR ? half_of(rows) : 0;
-                const int first = __shfl_sync(0xFFFFFFFFu, tl.first, 0) + rank * h;
-                const int mine = PAIR ? (rank ? max(rows - h, 0) : min(rows, h)) : rows;
+                const int h = PAIR ? half_of(tl.rows) : 0, first = tl.first + rank * h;
+                const int mine = PAIR ? (rank ? max(tl.rows - h, 0) : min(tl.rows, h)) : tl.rows;
                 const int boxes = a.rows ? 0 : (mine + S::BOX - 1) / S::BOX;
                 const uint32_t bytes = S::W_BYTES + boxes * S::BOX * 2 * BK;
                 for (int kb = kb0; kb < kb1; ++kb, ++it, r.next()) {
@@ -293,12 +303,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                     uint64_t *bar = &c.full[r.i];
                     bar_expect(bar, bytes, me);
                     if (gated) {
-                        tma_5d(sw, &mw, kb * BK, 0, 0, n0 / 16, g, bar, me);
+                        tma_5d(sw, &mw, kb * BK, 0, 0, tl.n0 / 16, tl.g, bar, me);
                     } else if (a.transposed) {
-                        tma_3d(sw, &mw, n0, kb * BK, g, bar, me);
-                        tma_3d(sw + S::W_BYTES / 2, &mw, n0 + BN / 2, kb * BK, g, bar, me);
+                        tma_3d(sw, &mw, tl.n0, kb * BK, tl.g, bar, me);
+                        tma_3d(sw + S::W_BYTES / 2, &mw, tl.n0 + BN / 2, kb * BK, tl.g, bar, me);
                     } else {
-                        tma_3d(sw, &mw, kb * BK, n0, g, bar, me);
+                        tma_3d(sw, &mw, kb * BK, tl.n0, tl.g, bar, me);
                     }
                     for (int i = 0; i < boxes; ++i)
                         tma_tile(sx + i * S::BOX * 2 * BK, &mx, kb * BK, first + i * S::BOX, bar, me);
@@ -408,6 +418,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             asm volatile("cp.async.wait_all;" ::: "memory");
         }
     } else {
+        if (MOVE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
         const int quad = warp & 3, half = (warp - EPI_FIRST) >> 2;   // TMEM lanes, and every other 32 places
         const uint32_t at0 = tmem + ((uint32_t)(32 * quad) << 16);
         Ring<NBUF> d;
@@ -422,67 +433,89 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int t = t0; t < total; t += dt) {
             const Tile tl = tile_at<BT, PAIR>(&c, a, t, rank);
             const Column col = column_of(a, tl, quad, lane);
-            if (RUNS && kb1 - kb0 > RUN) {
-                // every running sum but the last into registers; the last one's buffer gets the whole
+            if (!SPLIT) prefetch_rows<TY>(a, tl, quad, half, lane);
+            // 16 places of this warp to the others of the cluster (over the stages: every copy and product is done), or out
+            const auto pass_on = [&](float(&v)[16], const float(&x)[16], int j) {
+                if (SPLIT) {
+                    float *red = reinterpret_cast<float *>(stages) + j * BN + 32 * quad + lane;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) red[i * BN] = v[i];
+                } else {
+                    const int cnt = min(16, tl.rows - j), place = tl.first + j;
+                    if (a.rows) clear_bad(a, v, place, cnt, lane);
+                    emit_t<MOVE, TY>(a, v, x, cnt, place, col.n, col.in, col.bias, lane);
+                }
+            };
+            if constexpr (RUNS) {
+                // The running sums are added in registers and go out from there, so that the buffers are free for the next
+                // tile's (held in TMEM meanwhile, they kept the products waiting: 206 us with a residual, 2048 deep).
                 float acc[S::PIECES][32] = {};
+                const auto place_of = [&](int q) { return 32 * half + 64 * (q >> 1) + 16 * (q & 1); };
+                // Pairs: the residual of the next 16 places is on its way while 16 go out (and of the first ones while the
+                // products run): waited for 16 by 16 it took 8000 of a tile's 27000 cycles, 2048 deep.
+                float x[16];
+                const auto extra = [&](int j) {
+                    if (!MOVE || a.act == MOE_ACT_SWIGLU || a.act == MOE_ACT_SWIGLU_GRAD || !col.in) return;
+                    if (j + 16 <= tl.rows) fetch_extra<true, TY>(a, tl.first + j, 16, col.n, x);
+                    else fetch_extra<false, TY>(a, tl.first + j, tl.rows - j, col.n, x);
+                };
+                extra(place_of(0));
                 for (int kb = kb0; kb < kb1; kb += RUN) {
                     ok = bar_wait(&c.sums[d.i], d.phase, &c.abort, a.wait, a.status);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                     fence_after();
 #pragma unroll
-                    for (int p = 0; p < S::PIECES; ++p)
+                    for (int p = 0; p < S::PIECES; ++p) {
+                        const int j = 32 * half + 64 * p;
+                        if (j >= tl.rows) continue;
+                        uint32_t u[32];
+                        tmem_ld32(at0 + d.i * BT + j, u);
+                        tmem_ld_wait();
 #pragma unroll
-                        for (int q = 0; q < 32; q += 16) {
-                            const int j = 32 * half + 64 * p + q;
-                            if (j >= tl.rows) continue;
-                            uint32_t u[16];
-                            tmem_ld16(at0 + d.i * BT + j, u);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) acc[p][q + i] += __uint_as_float(u[i]);
-                        }
-                    if (kb + RUN < kb1) give_back();
+                        for (int i = 0; i < 32; ++i) acc[p][i] += __uint_as_float(u[i]);
+                    }
+                    give_back();
                 }
                 if (!ok) break;
+                // (one piece of code for all 16s: unrolled, its forms take minutes to compile)
+#pragma unroll 1
+                for (int q = 0; q < 2 * S::PIECES; ++q) {
+                    const int j = place_of(q);
+                    if (j >= tl.rows) break;
+                    float v[16], now[16];
 #pragma unroll
-                for (int p = 0; p < S::PIECES; ++p)
-#pragma unroll
-                    for (int q = 0; q < 32; q += 16) {
-                        const int j = 32 * half + 64 * p + q;
-                        if (j < tl.rows) tmem_st16(at0 + d.i * BT + j, acc[p] + q);
+                    for (int i = 0; i < 16; ++i) {
+                        v[i] = acc[0][i];
+                        now[i] = x[i];
                     }
-                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                    extra(place_of(q + 1));
+#pragma unroll
+                    for (int k = 1; k < 2 * S::PIECES; ++k)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] = q == k ? acc[k >> 1][16 * (k & 1) + i] : v[i];
+                    pass_on(v, now, j);
+                }
             } else {
                 ok = bar_wait(&c.sums[d.i], d.phase, &c.abort, a.wait, a.status);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 fence_after();
-            }
 #pragma unroll 1
-            for (int j = 32 * half; j < tl.rows; j += 64) {
-                uint32_t u[32];
-                tmem_ld32(at0 + d.i * BT + j, u);
-                tmem_ld_wait();
-                if (SPLIT) {
-                    // this block's part, over the stages (every copy and product is done)
-                    float *red = reinterpret_cast<float *>(stages) + j * BN + 32 * quad + lane;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) red[i * BN] = __uint_as_float(u[i]);
-                } else {
-                    // (16 at a time, in one piece of code for both: its forms for 32 take minutes to compile)
+                for (int j = 32 * half; j < tl.rows; j += 64) {
+                    uint32_t u[32];
+                    tmem_ld32(at0 + d.i * BT + j, u);
+                    tmem_ld_wait();
 #pragma unroll 1
                     for (int h = 0; h < 32 && j + h < tl.rows; h += 16) {
                         float v[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(h ? u[16 + i] : u[i]);
-                        const int cnt = min(16, tl.rows - j - h), place = tl.first + j + h;
-                        if (a.rows) clear_bad(a, v, place, cnt, lane);
-                        emit_t<TY>(a, v, cnt, place, col.n, col.in, col.bias, lane);
+                        pass_on(v, v, j + h);
                     }
                 }
+                give_back();
             }
-            give_back();
         }
     }
     if (SPLIT) {
@@ -511,7 +544,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 const int cnt = min(4, tl.rows - j);
                 if (a.rows) clear_bad(a, v, tl.first + j, cnt, lane);
-                emit_t<TY>(a, v, cnt, tl.first + j, col.n, col.in, col.bias, lane);
+                emit_t<false, TY>(a, v, v, cnt, tl.first + j, col.n, col.in, col.bias, lane);
             }
         }
         cluster_sync();   // parts are read before their block ends
@@ -564,6 +597,11 @@ cudaError_t launch_t(const MatmulArgs &a, int grid, int cluster, cudaStream_t s)
     auto *k = matmul_kernel<BT, PAIR, SPLIT, TY>;
     cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     if (err != cudaSuccess) return err;
+    if (PAIR && sizeof(TY) == 4) {   // the registers that its warps hand on have to be there
+        cudaFuncAttributes at;
+        if ((err = cudaFuncGetAttributes(&at, k)) != cudaSuccess) return err;
+        if (at.numRegs < LAUNCH_REGS) return cudaErrorInvalidConfiguration;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(THREADS);
@@ -591,12 +629,20 @@ cudaError_t launch_matmul_t(MatmulArgs a, cudaStream_t s) {
     if (tiles(32, BN) > 0x3FFFFFFF) return cudaErrorNotSupported;
     const long long rows = a.M / groups;   // of a group on average
     const bool pair = rows > 64 && 2 * tiles(256, 2 * BN) >= sms;
+    if (pair && a.offsets && rows <= 110) {
+        a.ntn = (wide + 2 * BN - 1) / (2 * BN);
+        a.whole = wide / (2 * BN);
+        const long long n = tiles(128, 2 * BN), most = sms / 2;
+        return launch_t<128, true, false, TY>(a, 2 * (int)(n < most ? n : most), 2, s);
+    }
     if (pair) {
         a.ntn = (wide + 2 * BN - 1) / (2 * BN);
+        a.whole = wide / (2 * BN);
         const long long n = tiles(256, 2 * BN), most = sms / 2;
         return launch_t<256, true, false, TY>(a, 2 * (int)(n < most ? n : most), 2, s);
     }
     a.ntn = (wide + BN - 1) / BN;
+    a.whole = wide / BN;
     const int bt = rows <= 32 ? 32 : 128;
     const long long n = tiles(bt, BN);
     int split = 1;
@@ -621,6 +667,7 @@ cudaError_t launch_matmul(MatmulArgs a, cudaStream_t s) {
     a.wait = g_wait > 0 && (g_wait >> 16) < kWaitLimit ? (uint32_t)(g_wait >> 16) : kWaitLimit;
     a.hold_copies = g_hold == 1;
     a.hold_products = g_hold == 2;
+    if (matmul_few_rows(a)) return launch_matmul_rows(a, s);
     return a.ybf16 ? launch_matmul_t<__nv_bfloat16>(a, s) : launch_matmul_t<float>(a, s);
 }
 

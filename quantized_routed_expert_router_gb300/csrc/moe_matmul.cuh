@@ -19,7 +19,7 @@ struct MatmulArgs {
     int X, M, G, N, K;
     int act, transposed, ybf16;
     int KB;          // blocks of depth
-    int ntn;         // column tiles
+    int ntn, whole;  // column tiles, and those that the matrix's end does not cut off
     // test hook: bound on waits in units of 2^16 cycles; arrivals that never come at a stage's copies, at its products
     uint32_t wait;
     int hold_copies, hold_products;
@@ -42,16 +42,53 @@ __device__ __forceinline__ float gelu_slope(float v) {
     return 0.5f * (1.f + erff(v * 0.70710678118654752f)) + v * 0.39894228040143268f * expf(-0.5f * v * v);
 }
 
-__device__ __forceinline__ float to_f(float v) { return v; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ void put(float *p, float v) { *p = v; }
-__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+// (what passes by once leaves L2 first: the rows and matrices that other tiles take again are to stay)
+__device__ __forceinline__ float get(const float *p) { return __ldcs(p); }
+__device__ __forceinline__ float get(const __nv_bfloat16 *p) { return __bfloat162float(__ldcs(p)); }
+__device__ __forceinline__ void put(float *p, float v) { __stcs(p, v); }
+__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { __stcs(p, __float2bfloat16_rn(v)); }
+
+// one value of the product (with the gated activation: a gate and an up value) to z and y
+template <typename TY>
+__device__ __forceinline__ void finish(const MatmulArgs &a, int g, int place, int n, float v, float up) {
+    const size_t N = (size_t)a.N, at = place * N + n, at2 = place * 2 * N + n;
+    TY *y = static_cast<TY *>(a.y), *z = static_cast<TY *>(a.z);
+    if (a.act == MOE_ACT_SWIGLU_GRAD) {
+        const float gate = get(z + at2), u = get(z + at2 + N);
+        put(y + at2, v * u * silu_slope(gate));
+        put(y + at2 + N, v * silu(gate));
+        return;
+    }
+    if (a.act == MOE_ACT_SILU_GRAD || a.act == MOE_ACT_GELU_GRAD) {
+        const float f = get(z + at);
+        put(y + at, v * (a.act == MOE_ACT_SILU_GRAD ? silu_slope(f) : gelu_slope(f)));
+        return;
+    }
+    if (a.act == MOE_ACT_SWIGLU) {
+        if (a.bias) {
+            v += a.bias[g * 2 * N + n];
+            up += a.bias[g * 2 * N + N + n];
+        }
+        if (z) {
+            put(z + at2, v);
+            put(z + at2 + N, up);
+        }
+        v = silu(v) * up;
+    } else {
+        if (a.bias) v += a.bias[g * N + n];
+        if (z) put(z + at, v);
+        if (a.act == MOE_ACT_SILU) v = silu(v);
+        else if (a.act == MOE_ACT_GELU) v = gelu(v);
+    }
+    if (a.residual) v += get(static_cast<const TY *>(a.residual) + at);
+    put(y + at, v);
+}
 
 // C places of a column, FULL: all of them are there, otherwise the first cnt; rows are `step` values apart
 template <bool FULL, typename TY, int C>
 __device__ __forceinline__ void fetch(const TY *p, size_t step, int cnt, float (&v)[C]) {
 #pragma unroll
-    for (int j = 0; j < C; ++j, p += step) v[j] = FULL || j < cnt ? to_f(*p) : 0.f;
+    for (int j = 0; j < C; ++j, p += step) v[j] = FULL || j < cnt ? get(p) : 0.f;
 }
 template <bool FULL, typename TY, int C>
 __device__ __forceinline__ void spread(TY *p, size_t step, int cnt, const float (&v)[C]) {
@@ -60,14 +97,28 @@ __device__ __forceinline__ void spread(TY *p, size_t step, int cnt, const float 
         if (FULL || j < cnt) put(p, v[j]);
 }
 
+// the residual of C places (0 without one), or z where the gradient takes it
+template <bool FULL, typename TY, int C>
+__device__ __forceinline__ void fetch_extra(const MatmulArgs &a, int place, int cnt, int n, float (&x)[C]) {
+    const TY *p = static_cast<const TY *>(a.act >= MOE_ACT_SILU_GRAD ? a.z : a.residual);
+    if (p) {
+        fetch<FULL>(p + (size_t)place * a.N + n, (size_t)a.N, cnt, x);
+    } else {
+#pragma unroll
+        for (int j = 0; j < C; ++j) x[j] = 0.f;
+    }
+}
+
 // Products of C places with one column of the tile (lane by lane) to y and z.
 //   v : the products; of `cnt` places, the first of which is `place`
 //   n : this lane's column of y, which is there
 //   b : its bias
 // What a place takes here counts beside the products (a tile of 128 x 256 has 16384 cycles of them at K = 2048): bounds and
 // what is absent are tested once for all places, not at each (30 instructions a value, then 17000 cycles a tile).
-template <int ACT, bool FULL, typename TY, int C>
-__device__ __forceinline__ void emit(const MatmulArgs &a, float (&v)[C], int cnt, int place, int n, float b, int lane) {
+//   x : where PRE, what fetch_extra has brought for the activations that are not gated
+template <int ACT, bool FULL, bool PRE, typename TY, int C>
+__device__ __forceinline__ void emit(const MatmulArgs &a, float (&v)[C], const float (&x)[C], int cnt, int place, int n,
+                                     float b, int lane) {
     const size_t N = (size_t)a.N;
     TY *y = static_cast<TY *>(a.y), *z = static_cast<TY *>(a.z);
     const TY *r = static_cast<const TY *>(a.residual);
@@ -108,19 +159,17 @@ __device__ __forceinline__ void emit(const MatmulArgs &a, float (&v)[C], int cnt
         spread<FULL>(y + at + N, 2 * N, cnt, g);
     } else {
         const size_t at = (size_t)place * N + n;
-        if constexpr (ACT == MOE_ACT_SILU_GRAD || ACT == MOE_ACT_GELU_GRAD) {
-            float f[C];
-            fetch<FULL>(z + at, N, cnt, f);
+        float add[C];   // the residual, or z
+        if constexpr (PRE) {
 #pragma unroll
-            for (int j = 0; j < C; ++j) v[j] *= ACT == MOE_ACT_SILU_GRAD ? silu_slope(f[j]) : gelu_slope(f[j]);
+            for (int j = 0; j < C; ++j) add[j] = x[j];
         } else {
-            float add[C];
-            if (r) {
-                fetch<FULL>(r + at, N, cnt, add);
-            } else {
+            fetch_extra<FULL, TY>(a, place, cnt, n, add);
+        }
+        if constexpr (ACT == MOE_ACT_SILU_GRAD || ACT == MOE_ACT_GELU_GRAD) {
 #pragma unroll
-                for (int j = 0; j < C; ++j) add[j] = 0.f;
-            }
+            for (int j = 0; j < C; ++j) v[j] *= ACT == MOE_ACT_SILU_GRAD ? silu_slope(add[j]) : gelu_slope(add[j]);
+        } else {
 #pragma unroll
             for (int j = 0; j < C; ++j) v[j] += b;
             if (ACT != MOE_ACT_NONE && z) spread<FULL>(z + at, N, cnt, v);
@@ -135,25 +184,26 @@ __device__ __forceinline__ void emit(const MatmulArgs &a, float (&v)[C], int cnt
     }
 }
 
-template <bool FULL, typename TY, int C>
-__device__ __forceinline__ void emit_f(const MatmulArgs &a, float (&v)[C], int cnt, int place, int n, float b, int lane) {
+template <bool FULL, bool PRE, typename TY, int C>
+__device__ __forceinline__ void emit_f(const MatmulArgs &a, float (&v)[C], const float (&x)[C], int cnt, int place, int n,
+                                       float b, int lane) {
     switch (a.act) {
-        case MOE_ACT_NONE: return emit<MOE_ACT_NONE, FULL, TY, C>(a, v, cnt, place, n, b, lane);
-        case MOE_ACT_SILU: return emit<MOE_ACT_SILU, FULL, TY, C>(a, v, cnt, place, n, b, lane);
-        case MOE_ACT_GELU: return emit<MOE_ACT_GELU, FULL, TY, C>(a, v, cnt, place, n, b, lane);
-        case MOE_ACT_SWIGLU: return emit<MOE_ACT_SWIGLU, FULL, TY, C>(a, v, cnt, place, n, b, lane);
-        case MOE_ACT_SILU_GRAD: return emit<MOE_ACT_SILU_GRAD, FULL, TY, C>(a, v, cnt, place, n, b, lane);
-        case MOE_ACT_GELU_GRAD: return emit<MOE_ACT_GELU_GRAD, FULL, TY, C>(a, v, cnt, place, n, b, lane);
-        default: return emit<MOE_ACT_SWIGLU_GRAD, FULL, TY, C>(a, v, cnt, place, n, b, lane);
+        case MOE_ACT_NONE: return emit<MOE_ACT_NONE, FULL, PRE, TY, C>(a, v, x, cnt, place, n, b, lane);
+        case MOE_ACT_SILU: return emit<MOE_ACT_SILU, FULL, PRE, TY, C>(a, v, x, cnt, place, n, b, lane);
+        case MOE_ACT_GELU: return emit<MOE_ACT_GELU, FULL, PRE, TY, C>(a, v, x, cnt, place, n, b, lane);
+        case MOE_ACT_SWIGLU: return emit<MOE_ACT_SWIGLU, FULL, PRE, TY, C>(a, v, x, cnt, place, n, b, lane);
+        case MOE_ACT_SILU_GRAD: return emit<MOE_ACT_SILU_GRAD, FULL, PRE, TY, C>(a, v, x, cnt, place, n, b, lane);
+        case MOE_ACT_GELU_GRAD: return emit<MOE_ACT_GELU_GRAD, FULL, PRE, TY, C>(a, v, x, cnt, place, n, b, lane);
+        default: return emit<MOE_ACT_SWIGLU_GRAD, FULL, PRE, TY, C>(a, v, x, cnt, place, n, b, lane);
     }
 }
 // (with the gated activation N is a multiple of 16, and the lanes of a warp are there or not together)
-template <typename TY, int C>
-__device__ __forceinline__ void emit_t(const MatmulArgs &a, float (&v)[C], int cnt, int place, int n, bool in, float b,
-                                       int lane) {
+template <bool PRE, typename TY, int C>
+__device__ __forceinline__ void emit_t(const MatmulArgs &a, float (&v)[C], const float (&x)[C], int cnt, int place, int n,
+                                       bool in, float b, int lane) {
     if (!in) return;
-    if (cnt == C) emit_f<true, TY, C>(a, v, cnt, place, n, b, lane);
-    else emit_f<false, TY, C>(a, v, cnt, place, n, b, lane);
+    if (cnt == C) emit_f<true, PRE, TY, C>(a, v, x, cnt, place, n, b, lane);
+    else emit_f<false, PRE, TY, C>(a, v, x, cnt, place, n, b, lane);
 }
 
 }  // namespace moe

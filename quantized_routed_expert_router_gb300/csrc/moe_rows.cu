@@ -17,6 +17,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kSlots = 8;   // slots whose rows are on their way at once
+constexpr int kGradThreads = 256;
 
 // V values of a row as they lie in memory, and as numbers
 template <typename T, int V>
@@ -119,36 +120,35 @@ struct GradArgs {
     const float *weights;
     float *dweights;
     int T, k, n, M;
-    int groups;   // blocks a token's slots take, `slots` of them each
-    int slots;
+    int groups;   // blocks a token's slots take
 };
 
-// d_o[pos[t][s]] = w[t][s] dy[t], dweights[t][s] = <o[pos[t][s]], dy[t]>: a block takes whole rows, so that it has
-// the dots to itself
-template <typename TO, typename TY, int V>
-__global__ void __launch_bounds__(kThreads) combine_grad_kernel(const GradArgs a) {
-    __shared__ float part[kThreads / 32][kSlots];
-    const int t = blockIdx.x / a.groups, s0 = (blockIdx.x % a.groups) * a.slots;
-    const int have = min(a.slots, a.k - s0), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float w[kSlots], dot[kSlots] = {};
-    int at[kSlots];
+// d_o[pos[t][s]] = w[t][s] dy[t], dweights[t][s] = <o[pos[t][s]], dy[t]>: a block takes whole rows of S slots, so that it
+// has the dots to itself
+template <typename TO, typename TY, int V, int S>
+__global__ void __launch_bounds__(kGradThreads) combine_grad_kernel(const GradArgs a) {
+    __shared__ float part[kGradThreads / 32][S];
+    const int t = blockIdx.x / a.groups, s0 = (blockIdx.x % a.groups) * S;
+    const int have = min(S, a.k - s0), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float w[S], dot[S] = {};
+    int at[S];
 #pragma unroll
-    for (int s = 0; s < kSlots; ++s) {
+    for (int s = 0; s < S; ++s) {
         at[s] = s < have ? a.pos[(size_t)t * a.k + s0 + s] : -1;
         if ((unsigned)at[s] >= (unsigned)a.M) at[s] = -1;
         w[s] = at[s] >= 0 && a.weights ? a.weights[(size_t)t * a.k + s0 + s] : 1.f;
     }
-    for (int j = threadIdx.x * V; j < a.n; j += kThreads * V) {
+    for (int j = threadIdx.x * V; j < a.n; j += blockDim.x * V) {
         AlignedPiece<TY, V> dy;
-        AlignedPiece<TO, V> o[kSlots];
+        AlignedPiece<TO, V> o[S];
         dy.load(static_cast<const TY *>(a.dy) + (size_t)t * a.n + j);
         if (a.dweights) {
 #pragma unroll
-            for (int s = 0; s < kSlots; ++s)
+            for (int s = 0; s < S; ++s)
                 if (at[s] >= 0) o[s].load(static_cast<const TO *>(a.o) + (size_t)at[s] * a.n + j);
         }
 #pragma unroll
-        for (int s = 0; s < kSlots; ++s) {
+        for (int s = 0; s < S; ++s) {
             if (at[s] < 0) continue;
             if (a.dweights) {
 #pragma unroll
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads) combine_grad_kernel(const GradArgs a
     }
     if (!a.dweights) return;
 #pragma unroll
-    for (int s = 0; s < kSlots; ++s) {
+    for (int s = 0; s < S; ++s) {
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) dot[s] += __shfl_xor_sync(0xFFFFFFFFu, dot[s], off);
         if (lane == 0) part[warp][s] = dot[s];
@@ -172,8 +172,7 @@ __global__ void __launch_bounds__(kThreads) combine_grad_kernel(const GradArgs a
     __syncthreads();
     if (threadIdx.x < have) {
         float sum = part[0][threadIdx.x];
-#pragma unroll
-        for (int i = 1; i < kThreads / 32; ++i) sum += part[i][threadIdx.x];
+        for (int i = 1; i < (int)blockDim.x / 32; ++i) sum += part[i][threadIdx.x];
         a.dweights[(size_t)t * a.k + s0 + threadIdx.x] = sum;
     }
 }
@@ -201,16 +200,24 @@ cudaError_t combine_t(RowArgs a, cudaStream_t s) {
     else combine_kernel<TO, TY, 1><<<grid, kThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
-template <typename TO, typename TY>
-cudaError_t combine_grad_t(GradArgs a, cudaStream_t s) {
+template <typename TO, typename TY, int S>
+cudaError_t combine_grad_s(GradArgs a, cudaStream_t s) {
     const int v = values(a.n);
-    a.slots = kSlots;
-    a.groups = (a.k + a.slots - 1) / a.slots;
+    a.groups = (a.k + S - 1) / S;
     const unsigned grid = (unsigned)(a.T * a.groups);
-    if (v == 8) combine_grad_kernel<TO, TY, 8><<<grid, kThreads, 0, s>>>(a);
-    else if (v == 2) combine_grad_kernel<TO, TY, 2><<<grid, kThreads, 0, s>>>(a);
-    else combine_grad_kernel<TO, TY, 1><<<grid, kThreads, 0, s>>>(a);
+    // the fewest rounds of a block's threads over a row, and of those the same number each
+    const int pieces = (a.n + v - 1) / v, rounds = (pieces + kGradThreads - 1) / kGradThreads;
+    const int threads = ((pieces + rounds - 1) / rounds + 31) / 32 * 32;
+    if (v == 8) combine_grad_kernel<TO, TY, 8, S><<<grid, threads, 0, s>>>(a);
+    else if (v == 2) combine_grad_kernel<TO, TY, 2, S><<<grid, threads, 0, s>>>(a);
+    else combine_grad_kernel<TO, TY, 1, S><<<grid, threads, 0, s>>>(a);
     return cudaGetLastError();
+}
+template <typename TO, typename TY>
+cudaError_t combine_grad_t(const GradArgs &a, cudaStream_t s) {
+    // few rows: a block a slot, and the token's row is read by each
+    if ((long long)a.T * a.k <= 4 * num_sms()) return combine_grad_s<TO, TY, 1>(a, s);
+    return a.k <= 4 ? combine_grad_s<TO, TY, 4>(a, s) : combine_grad_s<TO, TY, 8>(a, s);
 }
 
 }  // namespace
@@ -238,7 +245,7 @@ cudaError_t launch_combine_rows(const void *o, int dtype, const int32_t *pos, co
 
 cudaError_t launch_combine_grad(const void *dy, int ydtype, const int32_t *pos, const float *weights, int T, int k,
                                 int n, int M, const void *o, int dtype, void *d_o, float *dweights, cudaStream_t s) {
-    const GradArgs a = {dy, o, d_o, pos, weights, dweights, T, k, n, M, 0, 0};
+    const GradArgs a = {dy, o, d_o, pos, weights, dweights, T, k, n, M, 0};
     if (dtype == MOE_DT_BF16)
         return ydtype == MOE_DT_BF16 ? combine_grad_t<__nv_bfloat16, __nv_bfloat16>(a, s)
                                      : combine_grad_t<__nv_bfloat16, float>(a, s);

@@ -71,9 +71,10 @@ struct Row {
     }
 };
 
-// Lane < k holds a chosen logit (-inf: none); m: the largest of the row, all: sum of exp(l - m) over the row where
+// A row's slots lie in `width` lanes side by side, each with a chosen logit (-inf: none); m: the row's largest, all: sum of exp(l - m) over the row where
 // the weights are shares of it.  The slot's weight; slope: 1 - sigma(l), or 1 for softmax.
-__device__ __forceinline__ float weight_of(float l, float m, float all, bool sigmoidal, bool renorm, float &slope) {
+__device__ __forceinline__ float weight_of(float l, float m, float all, bool sigmoidal, bool renorm, int width,
+                                           float &slope) {
     const bool some = l != -INFINITY;
     float g;
     slope = 1.f;
@@ -84,8 +85,14 @@ __device__ __forceinline__ float weight_of(float l, float m, float all, bool sig
         g = expf(l - m);
     }
     if (!some) g = 0.f;
-    if (renorm) all = warp_sum(g);
-    else if (sigmoidal) return g;
+    if (renorm) {
+        all = g;
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1)
+            if (off < width) all += __shfl_xor_sync(kAll, all, off);
+    } else if (sigmoidal) {
+        return g;
+    }
     return some ? __fdividef(g, all) : 0.f;
 }
 
@@ -126,8 +133,10 @@ __device__ __noinline__ int choose_exactly(const T *logits, int E, int k, int la
     return id;
 }
 
+// The k + 1 largest of a row by keys that carry the index, in order, to slot[0 .. k]; true where a lane ran out of its four.
+// (One more than are taken: is the last one's rank certain?)
 template <typename T, int VEC, int J>
-__device__ __forceinline__ int choose(const T *logits, const Row<T, VEC, J> &row, int E, int k, int lane) {
+__device__ __forceinline__ bool choose(const Row<T, VEC, J> &row, int k, int lane, uint32_t *lists, uint32_t *slot) {
     uint32_t a[4] = {0, 0, 0, 0};   // the lane's largest, in order
 #pragma unroll
     for (int j = 0; j < VEC * J; j += 4) {
@@ -154,25 +163,21 @@ __device__ __forceinline__ int choose(const T *logits, const Row<T, VEC, J> &row
             order2(a[2], a[3]);
         }
     }
-    uint32_t mine = 0, top = 0;
+    // The lists lie in shared memory, a lane its column, with a 0 behind them.  Whose value is the largest writes it to the
+    // round's slot and takes up its next one: two instructions of the pipe that bounds this instead of eight in registers.
+#pragma unroll
+    for (int i = 1; i < 4; ++i) lists[32 * (i - 1) + lane] = a[i];
+    uint32_t head = a[0], *at = lists + lane;
 #pragma unroll 3
-    for (int s = 0; s <= k; ++s) {   // one more than are taken: is the last one's rank certain?
-        top = __reduce_max_sync(kAll, a[0]);
-        mine = lane == s ? top : mine;
-        if (a[0] == top) {
-            a[0] = a[1];
-            a[1] = a[2];
-            a[2] = a[3];
-            a[3] = 0;
+    for (int s = 0; s <= k; ++s) {
+        const uint32_t top = __reduce_max_sync(kAll, head);
+        if (head == top) {
+            slot[s] = top;
+            head = *at;
+            at += 32;
         }
     }
-    bool unsure = VEC * J > 4 && a[0] == 0;   // (the key of an expert is not 0)
-    if (sizeof(T) == 4) {
-        const uint32_t down = __shfl_down_sync(kAll, mine, 1), next = lane == 31 ? top : down;
-        unsure = unsure || (lane < k && next > kNone && (mine ^ next) <= kIndex);
-    }
-    if (__any_sync(kAll, unsure)) return choose_exactly<T, VEC, J>(logits, E, k, lane);
-    return lane < k && mine > kNone ? (int)(kIndex - (mine & kIndex)) : -1;
+    return VEC * J > 4 && head == 0;   // (the key of an expert is not 0)
 }
 
 struct TopkArgs {
@@ -181,41 +186,80 @@ struct TopkArgs {
     int32_t *ids;
     float *weights;
     int T, E, k, sigmoid, renorm;
+    int width, batch;   // lanes of a row's slots (a power of two), rows of a batch
 };
 
-// A warp walks over rows, the next one's loads under way while it works on one.
-template <typename T, int VEC, int J>
+// A warp takes a batch of rows: it makes their choices one after the other, the next row's loads under way while it works on
+// one, and the weights of all of them at once, a lane a slot (a row by itself took 353 instructions at E = 256, of which
+// two thirds do not depend on E).  ALL: the weights are shares of the whole row.
+template <typename T, int VEC, int J, bool ALL>
 __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(VEC * J)) topk_kernel(const TopkArgs a) {
-    const int lane = threadIdx.x & 31, step = gridDim.x * kWarps;
+    __shared__ uint32_t s_lists[kWarps][4 * 32], s_slots[kWarps][64];
+    const int lane = threadIdx.x & 31, step = gridDim.x * kWarps * a.batch;
+    const int r = lane / a.width, s = lane & (a.width - 1);   // of the batch's weights
+    uint32_t *lists = s_lists[threadIdx.x >> 5], *slots = s_slots[threadIdx.x >> 5];
+    lists[96 + lane] = 0;
     const T *logits = static_cast<const T *>(a.logits);
     Row<T, VEC, J> next;
     bool next_live = false;
-    int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (t < a.T) {
+    const auto fetch = [&](int t) {
+        if (t >= a.T) return;
         next_live = !a.valid || a.valid[t];
         next.load(logits + (size_t)t * a.E, a.E, lane);
-    }
-    for (; t < a.T; t += step) {
-        const Row<T, VEC, J> row = next;
-        const bool live = next_live;
-        if (t + step < a.T) {
-            next_live = !a.valid || a.valid[t + step];
-            next.load(logits + (size_t)(t + step) * a.E, a.E, lane);
+    };
+    int base = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * a.batch;
+    fetch(base);
+    for (; base < a.T; base += step) {
+        const int n = min(a.batch, a.T - base);
+        unsigned unsure = 0;   // rows of the batch
+        float all = 0.f;
+        for (int i = 0; i < n; ++i) {
+            const Row<T, VEC, J> row = next;
+            const bool live = next_live;
+            fetch(i + 1 < n ? base + i + 1 : base + step);
+            uint32_t *slot = slots + i * (a.width + 1);
+            if (live) {
+                if (choose<T, VEC, J>(row, a.k, lane, lists, slot)) unsure |= 1u << i;
+                if (ALL) {
+                    float m = row.value(0);
+#pragma unroll
+                    for (int j = 1; j < VEC * J; ++j) m = max_nan(m, row.value(j));
+                    const float sum = row.sum(warp_max(m));
+                    if (r == i) all = sum;
+                }
+            } else if (lane <= a.k) {
+                slot[lane] = 0;
+            }
         }
-        int id = -1;
-        float w = 0.f;
-        if (live) {
-            const T *at = logits + (size_t)t * a.E;
-            id = choose<T, VEC, J>(at, row, a.E, a.k, lane);
-            const float mine = id >= 0 ? (float)at[id] : -INFINITY, m = __shfl_sync(kAll, mine, 0);
-            const float all = a.sigmoid || a.renorm ? 0.f : row.sum(m);
-            float slope;
-            w = weight_of(mine, m, all, a.sigmoid, a.renorm, slope);
+        __syncwarp();
+        const bool mine = r < n && s < a.k;
+        const int at = min(r, n - 1) * (a.width + 1) + min(s, a.k - 1);
+        uint32_t key = slots[at];
+        if (sizeof(T) == 4) {
+            const uint32_t below = slots[at + 1];
+            if (mine && below > kNone && (key ^ below) <= kIndex) unsure |= 1u << r;
         }
-        if (lane < a.k) {
-            a.ids[(size_t)t * a.k + lane] = id;
-            if (a.weights) a.weights[(size_t)t * a.k + lane] = w;
+        if (__any_sync(kAll, unsure)) {
+            unsure = __reduce_or_sync(kAll, unsure);
+            for (int i = 0; i < n; ++i) {
+                if (!(unsure >> i & 1)) continue;
+                const int e = choose_exactly<T, VEC, J>(logits + (size_t)(base + i) * a.E, a.E, a.k, lane);
+                if (lane < a.k) slots[i * (a.width + 1) + lane] = e >= 0 ? ~kIndex | (kIndex - e) : 0;
+            }
+            __syncwarp();
+            key = slots[at];
         }
+        const int id = mine && key > kNone ? (int)(kIndex - (key & kIndex)) : -1;
+        const float l = id >= 0 ? (float)logits[(size_t)(base + r) * a.E + id] : -INFINITY;
+        const float m = __shfl_sync(kAll, l, lane - s);
+        float slope;
+        const float w = weight_of(l, m, all, a.sigmoid, a.renorm, a.width, slope);
+        if (mine) {
+            const size_t to = (size_t)(base + r) * a.k + s;
+            a.ids[to] = id;
+            if (a.weights) a.weights[to] = w;
+        }
+        __syncwarp();
     }
 }
 
@@ -263,7 +307,7 @@ __global__ void __launch_bounds__(32 * kWarps, grad_blocks(VEC * J)) topk_grad_k
         m = warp_max(m);
         const float all = ROW ? row.sum(m) : 0.f;
         float slope;
-        const float w = weight_of(mine, m, all, a.sigmoid, a.renorm, slope);
+        const float w = weight_of(mine, m, all, a.sigmoid, a.renorm, 32, slope);
         const bool ratio = a.renorm || !a.sigmoid;
         const float dot = ratio ? warp_sum(id >= 0 ? w * d : 0.f) : 0.f;
         // the row's gradient at the chosen experts; where an id comes twice (one of its slots finds the other's mark),
@@ -312,8 +356,16 @@ unsigned blocks(int rows, int per_sm) {
     return (unsigned)(need < most ? need : most);
 }
 template <typename T, int VEC, int J>
-cudaError_t topk_t(const TopkArgs &a, cudaStream_t s) {
-    topk_kernel<T, VEC, J><<<blocks(a.T, blocks_per_sm(VEC * J)), 32 * kWarps, 0, s>>>(a);
+cudaError_t topk_t(TopkArgs a, cudaStream_t s) {
+    const int per_sm = blocks_per_sm(VEC * J);
+    a.width = 1;
+    while (a.width < a.k) a.width *= 2;
+    // batches where every warp has one: few rows take the time of one
+    a.batch = 32 / a.width;
+    while (a.batch > 1 && (long long)num_sms() * per_sm * kWarps * a.batch > a.T) a.batch /= 2;
+    const unsigned grid = blocks((a.T + a.batch - 1) / a.batch, per_sm);
+    if (!a.sigmoid && !a.renorm) topk_kernel<T, VEC, J, true><<<grid, 32 * kWarps, 0, s>>>(a);
+    else topk_kernel<T, VEC, J, false><<<grid, 32 * kWarps, 0, s>>>(a);
     return cudaGetLastError();
 }
 template <typename T, int VEC, int J>
@@ -343,7 +395,7 @@ cudaError_t by_width(const A &a, cudaStream_t s) {
 
 cudaError_t launch_topk(const void *logits, int dtype, const uint8_t *valid, int T, int E, int k, int gating,
                         int renormalize, int32_t *ids, float *weights, cudaStream_t s) {
-    const TopkArgs a = {logits, valid, ids, weights, T, E, k, gating == MOE_GATE_SIGMOID, renormalize != 0};
+    const TopkArgs a = {logits, valid, ids, weights, T, E, k, gating == MOE_GATE_SIGMOID, renormalize != 0, 0, 0};
     return dtype == MOE_DT_BF16 ? by_width<__nv_bfloat16>(a, s) : by_width<float>(a, s);
 }
 

@@ -13,8 +13,8 @@ moe = pytest.importorskip("quantized_routed_expert_router_gb300")
 
 DEV = "cuda"
 
-# few places and many, whole depth and in parts, one block a tile and two, more depth than the ring and less
-SIZES = [(3, 272, 4096), (40, 7168, 200), (100, 400, 4096), (100, 4000, 1024), (2500, 1040, 400), (4000, 2048, 1024)]
+# few places (transposed: by tiles) and many, whole depth and in parts, one block a tile and two, more depth than the ring and less
+SIZES = [(17, 272, 4096), (40, 7168, 200), (100, 400, 4096), (100, 4000, 1024), (2500, 1040, 400), (4000, 2048, 1024)]
 
 
 @pytest.mark.gpu
@@ -50,6 +50,25 @@ def test_waits_run_out_then_recovery(M, N, K, gathered, dtype, hold):
             check(y[a:b], *product(x[rows[a:b].long()], w[e]))
     else:
         check(y, *product(x, w))
+
+
+@pytest.mark.gpu
+def test_few_rows_wait_for_nothing_unless_transposed():
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x, w = rand(16, 1024, g=g), rand(136, 1024, g=g, scale=1024 ** -0.5)
+    y, st = torch.full((16, 136), 7.0, device=DEV), workspace()
+    try:
+        moe.moe_debug_hold_matmul(1, 1 << 17)
+        moe.moe_matmul(x, w, y, st)
+        torch.cuda.synchronize()
+        check(y, *product(x, w))
+        assert moe.moe_read_device_status(st) == 0
+        y.fill_(7.0)
+        moe.moe_matmul(x, w.t().contiguous(), y, st, transposed=True)
+        torch.cuda.synchronize()
+    finally:
+        moe.moe_debug_hold_matmul(0)
+    assert moe.moe_read_device_status(st) == moe.DEV_TIMEOUT and bool((y == 7.0).all())
 
 
 def test_the_hook_refuses_what_it_does_not_know():
