@@ -60,7 +60,7 @@ struct Shape {
     static constexpr int SMEM = STAGES * STAGE + 1024;   // + alignment of the swizzle pattern
     static constexpr int NBUF = BT == 256 ? 2 : 4;       // TMEM buffers
     static constexpr int COLS = NBUF * BT;
-    static constexpr int BOX = BT < 64 ? BT : 64;        // places of a copy
+    static constexpr int BOX = PLACES, LESS = PLACES == 128 ? 64 : PLACES;   // places of a copy, of one for few places
     static constexpr int PIECES = BT < 64 ? 1 : BT / 64;   // 32 places each, of an epilogue warp
     static_assert(STAGES <= MAX_STAGES && COLS <= 512 && (PAIR || 4 * BT * BN <= STAGES * STAGE), "");
 };
@@ -107,6 +107,14 @@ __device__ __forceinline__ void tma_3d(void *dst, const CUtensorMap *m, int x, i
         "{\n .reg .pred e;\n setp.ne.u32 e, %6, 0;\n"
         " @e cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
         "[%5];\n}" ::"r"(sa(dst)), "l"(m), "r"(x), "r"(y), "r"(z), "r"(sa(bar)), "r"(me)
+        : "memory");
+}
+__device__ __forceinline__ void tma_4d(void *dst, const CUtensorMap *m, int x, int y, int z, int u, uint64_t *bar,
+                                       uint32_t me) {
+    asm volatile(
+        "{\n .reg .pred e;\n setp.ne.u32 e, %7, 0;\n"
+        " @e cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];\n}" ::"r"(sa(dst)), "l"(m), "r"(x), "r"(y), "r"(z), "r"(u), "r"(sa(bar)), "r"(me)
         : "memory");
 }
 __device__ __forceinline__ void tma_5d(void *dst, const CUtensorMap *m, int x, int y, int z, int u, int v, uint64_t *bar,
@@ -200,7 +208,8 @@ __device__ __forceinline__ int half_of(int rows) { return ((rows + 31) >> 5) << 
 
 template <int BT, bool PAIR, bool SPLIT, typename TY>
 __global__ void __launch_bounds__(THREADS, 1)
-    matmul_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw, const MatmulArgs a) {
+    matmul_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mx_less,
+                  const __grid_constant__ CUtensorMap mw, const MatmulArgs a) {
     using S = Shape<BT, PAIR>;
     constexpr int STAGES = S::STAGES, NBUF = S::NBUF;
     constexpr bool RUNS = sizeof(TY) == 4;
@@ -285,16 +294,19 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (MOVE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FEED_REGS));
         if (warp == 0) {
             const uint32_t me = elect();
-            const bool gated = a.act == MOE_ACT_SWIGLU;
             Ring<STAGES> r;
             int it = 0;
             bool ok = true;
             for (int t = t0; t < total && ok; t += dt) {
                 const Tile tl = tile_at<BT, PAIR>(&c, a, t, rank);
-                const int h = PAIR ? half_of(tl.rows) : 0, first = tl.first + rank * h;
-                const int mine = PAIR ? (rank ? max(tl.rows - h, 0) : min(tl.rows, h)) : tl.rows;
-                const int boxes = a.rows ? 0 : (mine + S::BOX - 1) / S::BOX;
-                const uint32_t bytes = S::W_BYTES + boxes * S::BOX * 2 * BK;
+                const int n0 = __shfl_sync(0xFFFFFFFFu, tl.n0, 0), g = __shfl_sync(0xFFFFFFFFu, tl.g, 0);
+                const int rows = __shfl_sync(0xFFFFFFFFu, tl.rows, 0), h = PAIR ? half_of(rows) : 0;
+                const int first = __shfl_sync(0xFFFFFFFFu, tl.first, 0) + rank * h;
+                const int mine = PAIR ? (rank ? max(rows - h, 0) : min(rows, h)) : rows;
+                // (one copy each of matrix and rows: with two of 64 rows a stage 8192 x 2048 by 7168 x 2048 took 4% more)
+                const CUtensorMap *rows_map = mine > S::LESS ? &mx : &mx_less;
+                const int box = a.rows || mine <= 0 ? 0 : mine > S::LESS ? S::BOX : S::LESS;
+                const uint32_t bytes = S::W_BYTES + box * 2 * BK;
                 for (int kb = kb0; kb < kb1; ++kb, ++it, r.next()) {
                     ok = bar_wait(&c.done[r.i], r.phase ^ 1, &c.abort, a.wait, a.status);
                     ok = __all_sync(0xFFFFFFFFu, ok);
@@ -302,16 +314,18 @@ __global__ void __launch_bounds__(THREADS, 1)
                     uint8_t *sw = stages + r.i * S::STAGE, *sx = sw + S::W_BYTES;
                     uint64_t *bar = &c.full[r.i];
                     bar_expect(bar, bytes, me);
-                    if (gated) {
-                        tma_5d(sw, &mw, kb * BK, 0, 0, tl.n0 / 16, tl.g, bar, me);
+                    // (by the dimensions that the map has)
+                    if (a.wdims == 5) {
+                        tma_5d(sw, &mw, kb * BK, 0, 0, n0 / 16, g, bar, me);
+                    } else if (a.wdims == 4) {
+                        tma_4d(sw, &mw, 0, kb * BK, n0 / 64, g, bar, me);
                     } else if (a.transposed) {
-                        tma_3d(sw, &mw, tl.n0, kb * BK, tl.g, bar, me);
-                        tma_3d(sw + S::W_BYTES / 2, &mw, tl.n0 + BN / 2, kb * BK, tl.g, bar, me);
+                        tma_3d(sw, &mw, n0, kb * BK, g, bar, me);
+                        tma_3d(sw + S::W_BYTES / 2, &mw, n0 + BN / 2, kb * BK, g, bar, me);
                     } else {
-                        tma_3d(sw, &mw, kb * BK, tl.n0, tl.g, bar, me);
+                        tma_3d(sw, &mw, kb * BK, n0, g, bar, me);
                     }
-                    for (int i = 0; i < boxes; ++i)
-                        tma_tile(sx + i * S::BOX * 2 * BK, &mx, kb * BK, first + i * S::BOX, bar, me);
+                    if (box) tma_tile(sx, rows_map, kb * BK, first, bar, me);
                 }
             }
             // copies in flight land, and their products end, before the block ends
@@ -571,17 +585,22 @@ bool encode(CUtensorMap *m, int dims, const void *p, const cuuint64_t *size, con
 
 bool encode_w(CUtensorMap *m, const MatmulArgs &a) {
     const cuuint64_t K = (cuuint64_t)a.K, N = (cuuint64_t)a.N, G = (cuuint64_t)a.G;
-    if (a.act == MOE_ACT_SWIGLU) {   // depth, 16 rows, gate or up, which 16, group
+    if (a.wdims == 5) {   // depth, 16 rows, gate or up, which 16, group
         const cuuint64_t size[5] = {K, 16, 2, N / 16, G}, stride[4] = {2 * K, 2 * N * K, 32 * K, 4 * N * K};
         const cuuint32_t box[5] = {BK, 16, 2, BN / 32, 1};
         return encode(m, 5, a.w, size, stride, box);
     }
-    if (a.transposed) {
+    if (a.wdims == 4) {   // 64 columns, depth, which 64, group
+        const cuuint64_t size[4] = {64, K, N / 64, G}, stride[3] = {2 * N, 128, 2 * N * K};
+        const cuuint32_t box[4] = {64, BK, BN / 64, 1};
+        return encode(m, 4, a.w, size, stride, box);
+    }
+    if (a.transposed) {   // columns, depth, group
         const cuuint64_t size[3] = {N, K, G}, stride[2] = {2 * N, 2 * N * K};
         const cuuint32_t box[3] = {64, BK, 1};
         return encode(m, 3, a.w, size, stride, box);
     }
-    const cuuint64_t size[3] = {K, N, G}, stride[2] = {2 * K, 2 * N * K};
+    const cuuint64_t size[3] = {K, N, G}, stride[2] = {2 * K, 2 * N * K};   // depth, rows, group
     const cuuint32_t box[3] = {BK, BN, 1};
     return encode(m, 3, a.w, size, stride, box);
 }
@@ -589,11 +608,12 @@ bool encode_w(CUtensorMap *m, const MatmulArgs &a) {
 template <int BT, bool PAIR, bool SPLIT, typename TY>
 cudaError_t launch_t(const MatmulArgs &a, int grid, int cluster, cudaStream_t s) {
     using S = Shape<BT, PAIR>;
-    CUtensorMap mx, mw;
+    CUtensorMap mx, mx_less, mw;
     const cuuint64_t size[2] = {(cuuint64_t)a.K, (cuuint64_t)a.X}, stride[1] = {2 * (cuuint64_t)a.K};
-    const cuuint32_t box[2] = {BK, (cuuint32_t)S::BOX};
+    const cuuint32_t box[2] = {BK, (cuuint32_t)S::BOX}, less[2] = {BK, (cuuint32_t)S::LESS};
     if (!encode_fn()) return cudaErrorSymbolNotFound;
-    if (!encode(&mx, 2, a.x, size, stride, box) || !encode_w(&mw, a)) return cudaErrorInvalidValue;
+    if (!encode(&mx, 2, a.x, size, stride, box) || !encode(&mx_less, 2, a.x, size, stride, less) || !encode_w(&mw, a))
+        return cudaErrorInvalidValue;
     auto *k = matmul_kernel<BT, PAIR, SPLIT, TY>;
     cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     if (err != cudaSuccess) return err;
@@ -615,7 +635,7 @@ cudaError_t launch_t(const MatmulArgs &a, int grid, int cluster, cudaStream_t s)
         cfg.attrs = at;
         cfg.numAttrs = 1;
     }
-    return cudaLaunchKernelEx(&cfg, k, mx, mw, a);
+    return cudaLaunchKernelEx(&cfg, k, mx, mx_less, mw, a);
 }
 
 template <typename TY>
@@ -667,6 +687,7 @@ cudaError_t launch_matmul(MatmulArgs a, cudaStream_t s) {
     a.wait = g_wait > 0 && (g_wait >> 16) < kWaitLimit ? (uint32_t)(g_wait >> 16) : kWaitLimit;
     a.hold_copies = g_hold == 1;
     a.hold_products = g_hold == 2;
+    a.wdims = a.act == MOE_ACT_SWIGLU ? 5 : a.transposed && a.N % 64 == 0 ? 4 : 3;
     if (matmul_few_rows(a)) return launch_matmul_rows(a, s);
     return a.ybf16 ? launch_matmul_t<__nv_bfloat16>(a, s) : launch_matmul_t<float>(a, s);
 }

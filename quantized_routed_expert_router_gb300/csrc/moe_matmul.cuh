@@ -18,6 +18,7 @@ struct MatmulArgs {
     unsigned *status;
     int X, M, G, N, K;
     int act, transposed, ybf16;
+    int wdims;       // dimensions of w's tensor map: 5 gate and up rows in turns, 4 transposed in 64s of columns, 3
     int KB;          // blocks of depth
     int ntn, whole;  // column tiles, and those that the matrix's end does not cut off
     // test hook: bound on waits in units of 2^16 cycles; arrivals that never come at a stage's copies, at its products
