@@ -167,16 +167,14 @@ __device__ __forceinline__ bool choose(const Row<T, VEC, J> &row, int k, int lan
     // round's slot and takes up its next one: two instructions of the pipe that bounds this instead of eight in registers.
 #pragma unroll
     for (int i = 1; i < 4; ++i) lists[32 * (i - 1) + lane] = a[i];
-    uint32_t head = a[0], *at = lists + lane;
+    uint32_t head = a[0], at = (uint32_t)__cvta_generic_to_shared(lists + lane);
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(slot);
 #pragma unroll 3
-    for (int s = 0; s <= k; ++s) {
-        const uint32_t top = __reduce_max_sync(kAll, head);
-        if (head == top) {
-            slot[s] = top;
-            head = *at;
-            at += 32;
-        }
-    }
+    for (int s = 0; s <= k; ++s)   // (predicated: a branch around three instructions costs as much as they do)
+        asm volatile(
+            "{\n .reg .pred p;\n setp.eq.u32 p, %0, %2;\n @p st.shared.u32 [%3], %2;\n @p ld.shared.u32 %0, [%1];\n"
+            " @p add.u32 %1, %1, 128;\n}"
+            : "+r"(head), "+r"(at) : "r"(__reduce_max_sync(kAll, head)), "r"(to + 4 * s) : "memory");
     return VEC * J > 4 && head == 0;   // (the key of an expert is not 0)
 }
 
@@ -195,28 +193,30 @@ struct TopkArgs {
 template <typename T, int VEC, int J, bool ALL>
 __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(VEC * J)) topk_kernel(const TopkArgs a) {
     __shared__ uint32_t s_lists[kWarps][4 * 32], s_slots[kWarps][64];
-    const int lane = threadIdx.x & 31, step = gridDim.x * kWarps * a.batch;
+    const int lane = threadIdx.x & 31, warp = blockIdx.x * kWarps + (threadIdx.x >> 5), warps = gridDim.x * kWarps;
     const int r = lane / a.width, s = lane & (a.width - 1);   // of the batch's weights
     uint32_t *lists = s_lists[threadIdx.x >> 5], *slots = s_slots[threadIdx.x >> 5];
     lists[96 + lane] = 0;
     const T *logits = static_cast<const T *>(a.logits);
+    // this warp's rows: as many as any other's, but for one
+    const int end = (int)((long long)a.T * (warp + 1) / warps);
+    int base = (int)((long long)a.T * warp / warps);
     Row<T, VEC, J> next;
     bool next_live = false;
     const auto fetch = [&](int t) {
-        if (t >= a.T) return;
+        if (t >= end) return;
         next_live = !a.valid || a.valid[t];
         next.load(logits + (size_t)t * a.E, a.E, lane);
     };
-    int base = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * a.batch;
     fetch(base);
-    for (; base < a.T; base += step) {
-        const int n = min(a.batch, a.T - base);
+    for (; base < end; base += a.batch) {
+        const int n = min(a.batch, end - base);
         unsigned unsure = 0;   // rows of the batch
         float all = 0.f;
         for (int i = 0; i < n; ++i) {
             const Row<T, VEC, J> row = next;
             const bool live = next_live;
-            fetch(i + 1 < n ? base + i + 1 : base + step);
+            fetch(base + i + 1);
             uint32_t *slot = slots + i * (a.width + 1);
             if (live) {
                 if (choose<T, VEC, J>(row, a.k, lane, lists, slot)) unsure |= 1u << i;
@@ -280,25 +280,42 @@ __global__ void __launch_bounds__(32 * kWarps, grad_blocks(VEC * J)) topk_grad_k
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, step = gridDim.x * kWarps;
     float *at = buf + warp * 32 * VEC * J;
     const T *logits = static_cast<const T *>(a.logits), *addend = static_cast<const T *>(a.addend);
+    // On its way: the slots two rows ahead, and one row ahead what is read (the chosen logits need the slots).
     Row<T, VEC, J> next, next_add;
-    int next_id = -1;
-    float next_d = 0.f;
-    const auto fetch = [&](int t) {
-        if (lane < a.k) {
-            next_id = a.ids[(size_t)t * a.k + lane];
-            next_d = a.dweights[(size_t)t * a.k + lane];
-        }
+    int ids[2] = {-1, -1};
+    float ds[2] = {}, next_mine = -INFINITY;
+    const auto fetch_slots = [&](int t, int i) {
+        if (t >= a.T || lane >= a.k) return;
+        ids[i] = a.ids[(size_t)t * a.k + lane];
+        ds[i] = a.dweights[(size_t)t * a.k + lane];
+    };
+    const auto fetch = [&](int t, int i) {
+        if (t >= a.T) return;
         if (ROW) next.load(logits + (size_t)t * a.E, a.E, lane);
+        else next_mine = (unsigned)ids[i] < (unsigned)a.E ? (float)logits[(size_t)t * a.E + ids[i]] : -INFINITY;
         if (addend) next_add.load(addend + (size_t)t * a.E, a.E, lane);
     };
     int t = blockIdx.x * kWarps + warp;
-    if (t < a.T) fetch(t);
+    fetch_slots(t, 0);
+    fetch_slots(t + step, 1);
+    fetch(t, 0);
     for (; t < a.T; t += step) {
         const Row<T, VEC, J> row = next, add = next_add;
-        const int id = (unsigned)next_id < (unsigned)a.E ? next_id : -1;
-        const float d = id >= 0 ? next_d : 0.f;
-        const float mine = id >= 0 ? (float)logits[(size_t)t * a.E + id] : -INFINITY;
-        if (t + step < a.T) fetch(t + step);
+        const int id = (unsigned)ids[0] < (unsigned)a.E ? ids[0] : -1;
+        const float d = id >= 0 ? ds[0] : 0.f;
+        float mine = next_mine;
+        if (ROW) {   // from the row, through shared memory
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) at[32 * VEC * j + VEC * lane + i] = row.value(VEC * j + i);
+            __syncwarp();
+            mine = id >= 0 ? at[id] : -INFINITY;
+        }
+        fetch(t + step, 1);
+        ids[0] = ids[1];
+        ds[0] = ds[1];
+        fetch_slots(t + 2 * step, 1);
         float m = mine;
         if (ROW) {
 #pragma unroll
