@@ -356,7 +356,7 @@ moe_status moe_matmul(const void *x, int X, const int32_t *rows, int M, const in
     if (N < 1 || N > (1 << 20) || (long long)G * N > (1ll << 30)) return MOE_ERR_INVALID_ARG;
     if (K < 8 || K > (1 << 20) || K % 8 || (transposed && N % 8)) return MOE_ERR_UNSUPPORTED;
     if (act == MOE_ACT_SWIGLU && (transposed || N % 16)) return MOE_ERR_UNSUPPORTED;
-    if ((long long)X * K > (1ll << 36)) return MOE_ERR_INVALID_ARG;
+    if ((long long)X * K > (1ll << 35)) return MOE_ERR_INVALID_ARG;
     if (!offsets && G != 1) return MOE_ERR_INVALID_ARG;
     const bool grad = act >= MOE_ACT_SILU_GRAD;
     if (grad ? bias || residual : act == MOE_ACT_NONE && z != nullptr) return MOE_ERR_INVALID_ARG;

@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const Tile tl = tile_at<BT, PAIR>(&c, a, t, rank);
                 const int h = PAIR ? half_of(tl.rows) : 0, first = tl.first + rank * h;
                 const int mine = PAIR ? (rank ? max(tl.rows - h, 0) : min(tl.rows, h)) : tl.rows;
-                uint32_t row[S::PLACES / 8];   // in units of 16 bytes (X K <= 2^36)
+                uint32_t row[S::PLACES / 8];   // in units of 16 bytes (X K <= 2^35 values)
 #pragma unroll
                 for (int i = 0; i < S::PLACES / 8; ++i) {
                     const int at = r0 + 8 * i < mine ? a.rows[first + r0 + 8 * i] : 0;
@@ -618,9 +618,11 @@ cudaError_t launch_t(const MatmulArgs &a, int grid, int cluster, cudaStream_t s)
     cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     if (err != cudaSuccess) return err;
     if (PAIR && sizeof(TY) == 4) {   // the registers that its warps hand on have to be there
-        cudaFuncAttributes at;
-        if ((err = cudaFuncGetAttributes(&at, k)) != cudaSuccess) return err;
-        if (at.numRegs < LAUNCH_REGS) return cudaErrorInvalidConfiguration;
+        static const bool there = [k] {
+            cudaFuncAttributes at;
+            return cudaFuncGetAttributes(&at, k) == cudaSuccess && at.numRegs >= LAUNCH_REGS;
+        }();
+        if (!there) return cudaErrorInvalidConfiguration;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
@@ -638,6 +640,46 @@ cudaError_t launch_t(const MatmulArgs &a, int grid, int cluster, cudaStream_t s)
     return cudaLaunchKernelEx(&cfg, k, mx, mx_less, mw, a);
 }
 
+// clusters of SIZE blocks that fit the GPU at once (its SMs come in groups, and a cluster lies within one); 0: not known
+template <int BT, typename TY, int SIZE>
+int clusters_at_once() {
+    static const int n = [] {
+        auto *k = matmul_kernel<BT, false, true, TY>;
+        int n = 0;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(SIZE);
+        cfg.blockDim = dim3(THREADS);
+        cfg.dynamicSmemBytes = Shape<BT, false>::SMEM;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = SIZE;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<BT, false>::SMEM) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess) {
+            cudaGetLastError();   // this call goes on without
+            return 0;
+        }
+        return n;
+    }();
+    return n;
+}
+
+template <int BT, typename TY>
+cudaError_t launch_single(const MatmulArgs &a, long long n, cudaStream_t s) {
+    // Depth in parts while every part still has an SM of its own and 4 blocks of depth, and all clusters run at once (16 of
+    // 8 blocks did not: 64 x 7168 by 2048 x 7168 18.8 us in 8 parts, 14.5 in 4; 64 x 8192 by 512 x 8192 11.5 in 8, 14.6 in 4,
+    // 22.7 in 2; 64 x 4096 by 1000 x 4096 10.4, 12.5 and 14.7).
+    const auto room = [&](int parts, int clusters) { return a.KB >= 4 * parts && n * parts <= num_sms() && n <= clusters; };
+    int split = 1;
+    if (room(2, clusters_at_once<BT, TY, 2>())) split = 2;
+    if (split == 2 && room(4, clusters_at_once<BT, TY, 4>())) split = 4;
+    if (split == 4 && room(MAX_SPLIT, clusters_at_once<BT, TY, MAX_SPLIT>())) split = MAX_SPLIT;
+    if (split > 1) return launch_t<BT, false, true, TY>(a, (int)n * split, split, s);
+    return launch_t<BT, false, false, TY>(a, (int)(n < num_sms() ? n : num_sms()), 1, s);
+}
+
 template <typename TY>
 cudaError_t launch_matmul_t(MatmulArgs a, cudaStream_t s) {
     const int wide = a.act == MOE_ACT_SWIGLU ? 2 * a.N : a.N;
@@ -648,29 +690,19 @@ cudaError_t launch_matmul_t(MatmulArgs a, cudaStream_t s) {
     };
     if (tiles(32, BN) > 0x3FFFFFFF) return cudaErrorNotSupported;
     const long long rows = a.M / groups;   // of a group on average
-    const bool pair = rows > 64 && 2 * tiles(256, 2 * BN) >= sms;
-    if (pair && a.offsets && rows <= 110) {
+    // Pairs where that leaves one of them for every other SM.  Few places a group: shorter stages, and more of them on their
+    // way (3108 rows over 32 of 2880 x 2880, 97 a group: 104.9 us, by 256 places 108.7).
+    if (rows > 64 && 2 * tiles(256, 2 * BN) >= sms) {
+        const bool less = a.offsets && rows <= 110;
         a.ntn = (wide + 2 * BN - 1) / (2 * BN);
         a.whole = wide / (2 * BN);
-        const long long n = tiles(128, 2 * BN), most = sms / 2;
-        return launch_t<128, true, false, TY>(a, 2 * (int)(n < most ? n : most), 2, s);
-    }
-    if (pair) {
-        a.ntn = (wide + 2 * BN - 1) / (2 * BN);
-        a.whole = wide / (2 * BN);
-        const long long n = tiles(256, 2 * BN), most = sms / 2;
-        return launch_t<256, true, false, TY>(a, 2 * (int)(n < most ? n : most), 2, s);
+        const long long n = tiles(less ? 128 : 256, 2 * BN), most = sms / 2;
+        const int grid = 2 * (int)(n < most ? n : most);
+        return less ? launch_t<128, true, false, TY>(a, grid, 2, s) : launch_t<256, true, false, TY>(a, grid, 2, s);
     }
     a.ntn = (wide + BN - 1) / BN;
     a.whole = wide / BN;
-    const int bt = rows <= 32 ? 32 : 128;
-    const long long n = tiles(bt, BN);
-    int split = 1;
-    while (split < MAX_SPLIT && n * split * 2 <= sms && a.KB >= split * 8) split *= 2;
-    const int grid = (int)(split > 1 ? n * split : n < sms ? n : sms);
-    if (split > 1)
-        return bt == 32 ? launch_t<32, false, true, TY>(a, grid, split, s) : launch_t<128, false, true, TY>(a, grid, split, s);
-    return bt == 32 ? launch_t<32, false, false, TY>(a, grid, 1, s) : launch_t<128, false, false, TY>(a, grid, 1, s);
+    return rows <= 32 ? launch_single<32, TY>(a, tiles(32, BN), s) : launch_single<128, TY>(a, tiles(128, BN), s);
 }
 
 }  // namespace

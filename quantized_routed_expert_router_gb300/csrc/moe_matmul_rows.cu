@@ -43,7 +43,7 @@ __device__ __forceinline__ uint4 ld_weight(const __nv_bfloat16 *p) {
 }
 
 template <int NT, int WARPS, int DEPTH, typename TY>
-__global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? NT == 1 ? 4 : 3 : 1) matmul_rows_kernel(const MatmulArgs a) {
+__global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? NT == 1 ? 4 : NT == 2 ? 3 : 2 : 1) matmul_rows_kernel(const MatmulArgs a) {
     constexpr int CHUNK = 8 * NT;   // places of a block
     __shared__ float red[WARPS][RB][CHUNK + 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g8 = lane >> 2, t4 = lane & 3;
@@ -151,13 +151,22 @@ cudaError_t launch_t(const MatmulArgs &a, dim3 grid, cudaStream_t s) {
 
 }  // namespace
 
-bool matmul_few_rows(const MatmulArgs &a) { return a.M <= 16 && !a.transposed; }
+// Up to 16 places (us here, and by tiles): one by 7168 x 2048 6.4, 10.5, by 2048 x 7168 8.4, 18.6; 16 by them 8.4, 10.8 and
+// 8.4, 18.6; 8 over 8 of 256 experts of 2 x 512 x 2048 10.4, 12.5; 16 over 14 of 32 of 2 x 2880 x 2880 55.5, 55.2; 16 over
+// 16 of 128 of 1536 x 2048 20.5, 20.8.  Up to 32 of a single matrix that has too few tiles for the SMs: 32 by 2048 x 7168
+// 12.4, 14.5, but by 7168 x 2048 14.5, 12.5.
+bool matmul_few_rows(const MatmulArgs &a) {
+    if (a.transposed) return false;
+    const int wide = a.act == MOE_ACT_SWIGLU ? 2 * a.N : a.N;
+    return a.M <= 16 || (a.M <= 32 && !a.offsets && wide <= 16 * num_sms());
+}
 
 cudaError_t launch_matmul_rows(const MatmulArgs &a, cudaStream_t s) {
-    const bool two = !a.offsets && a.M > 8;   // a second set of 8 columns beside the first
+    const bool two = !a.offsets && a.M > 8, four = !a.offsets && a.M > 16;   // more sets of 8 columns beside the first
     const int cols = a.act == MOE_ACT_SWIGLU ? RB / 2 : RB;
     const dim3 grid((unsigned)((a.N + cols - 1) / cols), (unsigned)(a.offsets ? a.M : 1));
     const bool wide = a.K >= 2048 && (long long)grid.x * grid.y <= num_sms();
+    if (four) return wide ? launch_t<4, 16, 2>(a, grid, s) : launch_t<4, 8, 2>(a, grid, s);
     if (two) return wide ? launch_t<2, 16, 2>(a, grid, s) : launch_t<2, 8, 2>(a, grid, s);
     return wide ? launch_t<1, 16, 4>(a, grid, s) : launch_t<1, 8, 4>(a, grid, s);
 }

@@ -44,8 +44,23 @@ __device__ __forceinline__ float sigmoid(float l) {
 // rows whose sigmas would vanish keep theirs
 __device__ __forceinline__ float sigmoid_over(float l, float m) { return expf(l - m) / (1.f + expf(l)); }
 
-// a row of logits; past E, where load does not come, it is -inf
-template <typename T, int VEC, int J>
+// sums and maxima over L lanes side by side (a NaN is the largest)
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+    for (int off = L / 2; off >= 1; off >>= 1) v += __shfl_xor_sync(kAll, v, off);
+    return v;
+}
+template <int L>
+__device__ __forceinline__ float lanes_max(float v) {
+    if constexpr (L == 32) return warp_max(v);
+#pragma unroll
+    for (int off = L / 2; off >= 1; off >>= 1) v = max_nan(v, __shfl_xor_sync(kAll, v, off));
+    return v;
+}
+
+// a row of logits in L lanes; past E, where load does not come, it is -inf
+template <typename T, int VEC, int J, int L = 32>
 struct Row {
     Raw<T, VEC> v[J];
     __device__ __forceinline__ Row() {
@@ -57,7 +72,7 @@ struct Row {
     __device__ __forceinline__ void load(const T *row, int E, int lane) {
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const int e = 32 * VEC * j + VEC * lane;
+            const int e = L * VEC * j + VEC * lane;
             if (e < E) v[j].load(row + e);
         }
     }
@@ -67,7 +82,7 @@ struct Row {
         float s = 0.f;
 #pragma unroll
         for (int i = 0; i < VEC * J; ++i) s += exp_fast(value(i) - m);
-        return warp_sum(s);
+        return lanes_sum<L>(s);
     }
 };
 
@@ -271,17 +286,19 @@ struct TopkGradArgs {
     int T, E, k, sigmoid, renorm;
 };
 
-// ROW: the gradient reaches the whole row (softmax over all E); otherwise the chosen experts.  The next row's slots and
-// logits are under way as in topk_kernel (rows are read before any of them is written: dlogits may be logits, and a
-// row belongs to one warp).
-template <typename T, int VEC, int J, bool ROW>
+// ROW: the gradient reaches the whole row (softmax over all E); otherwise the chosen experts.  A row takes L lanes: two rows
+// share a warp where they fit (65536 rows of 128 in bf16: 18.5 us with a warp a row, most of it the instructions that do not
+// depend on E).  The next row's slots and logits are under way as in topk_kernel (a row is read before it is written, by the
+// warp that it belongs to: dlogits may be logits).
+template <typename T, int VEC, int J, bool ROW, int L>
 __global__ void __launch_bounds__(32 * kWarps, grad_blocks(VEC * J)) topk_grad_kernel(const TopkGradArgs a) {
-    extern __shared__ float buf[];   // a row a warp
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, step = gridDim.x * kWarps;
-    float *at = buf + warp * 32 * VEC * J;
+    extern __shared__ float buf[];   // a row's values
+    const int lane = threadIdx.x & (L - 1), first = (threadIdx.x & 31) / L;   // in its row; the row of the warp
+    const int warp = threadIdx.x >> 5, step = gridDim.x * kWarps * (32 / L);
+    float *at = buf + threadIdx.x / L * L * VEC * J;
     const T *logits = static_cast<const T *>(a.logits), *addend = static_cast<const T *>(a.addend);
     // On its way: the slots two rows ahead, and one row ahead what is read (the chosen logits need the slots).
-    Row<T, VEC, J> next, next_add;
+    Row<T, VEC, J, L> next, next_add;
     int ids[2] = {-1, -1};
     float ds[2] = {}, next_mine = -INFINITY;
     const auto fetch_slots = [&](int t, int i) {
@@ -295,20 +312,20 @@ __global__ void __launch_bounds__(32 * kWarps, grad_blocks(VEC * J)) topk_grad_k
         else next_mine = (unsigned)ids[i] < (unsigned)a.E ? (float)logits[(size_t)t * a.E + ids[i]] : -INFINITY;
         if (addend) next_add.load(addend + (size_t)t * a.E, a.E, lane);
     };
-    int t = blockIdx.x * kWarps + warp;
+    int t = (blockIdx.x * kWarps + warp) * (32 / L) + first;
     fetch_slots(t, 0);
     fetch_slots(t + step, 1);
     fetch(t, 0);
-    for (; t < a.T; t += step) {
-        const Row<T, VEC, J> row = next, add = next_add;
-        const int id = (unsigned)ids[0] < (unsigned)a.E ? ids[0] : -1;
+    for (; t - first < a.T; t += step) {   // (all lanes of a warp together; rows past T are not written)
+        const Row<T, VEC, J, L> row = next, add = next_add;
+        const int id = (unsigned)ids[0] < (unsigned)a.E && t < a.T ? ids[0] : -1;
         const float d = id >= 0 ? ds[0] : 0.f;
         float mine = next_mine;
         if (ROW) {   // from the row, through shared memory
 #pragma unroll
             for (int j = 0; j < J; ++j)
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) at[32 * VEC * j + VEC * lane + i] = row.value(VEC * j + i);
+                for (int i = 0; i < VEC; ++i) at[L * VEC * j + VEC * lane + i] = row.value(VEC * j + i);
             __syncwarp();
             mine = id >= 0 ? at[id] : -INFINITY;
         }
@@ -321,12 +338,12 @@ __global__ void __launch_bounds__(32 * kWarps, grad_blocks(VEC * J)) topk_grad_k
 #pragma unroll
             for (int i = 0; i < VEC * J; ++i) m = max_nan(m, row.value(i));
         }
-        m = warp_max(m);
+        m = lanes_max<L>(m);
         const float all = ROW ? row.sum(m) : 0.f;
         float slope;
-        const float w = weight_of(mine, m, all, a.sigmoid, a.renorm, 32, slope);
+        const float w = weight_of(mine, m, all, a.sigmoid, a.renorm, L, slope);
         const bool ratio = a.renorm || !a.sigmoid;
-        const float dot = ratio ? warp_sum(id >= 0 ? w * d : 0.f) : 0.f;
+        const float dot = ratio ? lanes_sum<L>(id >= 0 ? w * d : 0.f) : 0.f;
         // the row's gradient at the chosen experts; where an id comes twice (one of its slots finds the other's mark),
         // slot by slot in their order
         const float g = ROW ? w * d : slope * w * (d - dot);
@@ -338,7 +355,7 @@ __global__ void __launch_bounds__(32 * kWarps, grad_blocks(VEC * J)) topk_grad_k
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) at[32 * VEC * j + VEC * lane + i] = 0.f;
+            for (int i = 0; i < VEC; ++i) at[L * VEC * j + VEC * lane + i] = 0.f;
         __syncwarp();
         if (!twice) {
             if (id >= 0) at[id] = g;
@@ -352,8 +369,8 @@ __global__ void __launch_bounds__(32 * kWarps, grad_blocks(VEC * J)) topk_grad_k
         const float scale = ROW ? dot / all : 0.f;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const int e = 32 * VEC * j + VEC * lane;
-            if (e >= a.E) continue;
+            const int e = L * VEC * j + VEC * lane;
+            if (e >= a.E || t >= a.T) continue;
             float v[VEC];
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
@@ -385,18 +402,18 @@ cudaError_t topk_t(TopkArgs a, cudaStream_t s) {
     else topk_kernel<T, VEC, J, false><<<grid, 32 * kWarps, 0, s>>>(a);
     return cudaGetLastError();
 }
-template <typename T, int VEC, int J>
-cudaError_t topk_t(const TopkGradArgs &a, cudaStream_t s) {
+template <typename T, int VEC, int J, int L>
+cudaError_t grad_t(const TopkGradArgs &a, cudaStream_t s) {
     constexpr int smem = kWarps * 32 * VEC * J * (int)sizeof(float);   // 32 KB at most
-    const unsigned grid = blocks(a.T, grad_blocks(VEC * J));
-    if (!a.sigmoid && !a.renorm) topk_grad_kernel<T, VEC, J, true><<<grid, 32 * kWarps, smem, s>>>(a);
-    else topk_grad_kernel<T, VEC, J, false><<<grid, 32 * kWarps, smem, s>>>(a);
+    const unsigned grid = blocks((a.T + 32 / L - 1) / (32 / L), grad_blocks(VEC * J));
+    if (!a.sigmoid && !a.renorm) topk_grad_kernel<T, VEC, J, true, L><<<grid, 32 * kWarps, smem, s>>>(a);
+    else topk_grad_kernel<T, VEC, J, false, L><<<grid, 32 * kWarps, smem, s>>>(a);
     return cudaGetLastError();
 }
 
 // rows of whole 4-value pieces, or value by value
-template <typename T, typename A>
-cudaError_t by_width(const A &a, cudaStream_t s) {
+template <typename T>
+cudaError_t topk_by_width(const TopkArgs &a, cudaStream_t s) {
     if (a.E % 4 == 0) {
         if (a.E <= 128) return topk_t<T, 4, 1>(a, s);
         if (a.E <= 256) return topk_t<T, 4, 2>(a, s);
@@ -407,20 +424,34 @@ cudaError_t by_width(const A &a, cudaStream_t s) {
     if (a.E <= 256) return topk_t<T, 1, 8>(a, s);
     return topk_t<T, 1, 32>(a, s);
 }
+template <typename T>
+cudaError_t grad_by_width(const TopkGradArgs &a, cudaStream_t s) {
+    const bool two = a.k <= 16;   // rows a warp, where 16 lanes hold one
+    if (a.E % 4 == 0) {
+        if (a.E <= 64 && two) return grad_t<T, 4, 1, 16>(a, s);
+        if (a.E <= 128) return two ? grad_t<T, 4, 2, 16>(a, s) : grad_t<T, 4, 1, 32>(a, s);
+        if (a.E <= 256) return grad_t<T, 4, 2, 32>(a, s);
+        if (a.E <= 512) return grad_t<T, 4, 4, 32>(a, s);
+        return grad_t<T, 4, 8, 32>(a, s);
+    }
+    if (a.E <= 64) return two ? grad_t<T, 1, 4, 16>(a, s) : grad_t<T, 1, 2, 32>(a, s);
+    if (a.E <= 256) return grad_t<T, 1, 8, 32>(a, s);
+    return grad_t<T, 1, 32, 32>(a, s);
+}
 
 }  // namespace
 
 cudaError_t launch_topk(const void *logits, int dtype, const uint8_t *valid, int T, int E, int k, int gating,
                         int renormalize, int32_t *ids, float *weights, cudaStream_t s) {
     const TopkArgs a = {logits, valid, ids, weights, T, E, k, gating == MOE_GATE_SIGMOID, renormalize != 0, 0, 0};
-    return dtype == MOE_DT_BF16 ? by_width<__nv_bfloat16>(a, s) : by_width<float>(a, s);
+    return dtype == MOE_DT_BF16 ? topk_by_width<__nv_bfloat16>(a, s) : topk_by_width<float>(a, s);
 }
 
 cudaError_t launch_topk_grad(const void *logits, int dtype, const int32_t *ids, const float *dweights, int T, int E,
                              int k, int gating, int renormalize, const void *addend, void *dlogits, cudaStream_t s) {
     const TopkGradArgs a = {logits, addend, ids, dweights, dlogits, T, E, k, gating == MOE_GATE_SIGMOID,
                             renormalize != 0};
-    return dtype == MOE_DT_BF16 ? by_width<__nv_bfloat16>(a, s) : by_width<float>(a, s);
+    return dtype == MOE_DT_BF16 ? grad_by_width<__nv_bfloat16>(a, s) : grad_by_width<float>(a, s);
 }
 
 }  // namespace moe

@@ -82,7 +82,7 @@ def test_combine_grad_refusals(change, status):
 @pytest.mark.parametrize("change,status", [
     (dict(X=-1), INVALID), (dict(X=MANY), INVALID), (dict(M=-1), INVALID), (dict(M=MANY), INVALID), (dict(G=0), INVALID),
     (dict(G=1025), INVALID), (dict(N=0), INVALID), (dict(N=(1 << 20) + 1), INVALID), (dict(K=0), UNSUP), (dict(K=12), UNSUP),
-    (dict(K=(1 << 20) + 8), UNSUP), (dict(X=1 << 17, K=1 << 20), INVALID), (dict(G=1024, N=(1 << 20) + 0, offs=None), INVALID),
+    (dict(K=(1 << 20) + 8), UNSUP), (dict(X=1 << 17, K=1 << 20), INVALID), (dict(X=(1 << 15) + 1, K=1 << 20), INVALID), (dict(G=1024, N=(1 << 20) + 0, offs=None), INVALID),
     (dict(yd=2), INVALID), (dict(act=-1), INVALID), (dict(act=7), INVALID), (dict(G=2), INVALID), (dict(X=0), INVALID),
     (dict(X=3), INVALID), (dict(x=None), INVALID), (dict(w=None), INVALID), (dict(y=None), INVALID),
     (dict(x=P + 8), INVALID), (dict(w=P + 8), INVALID), (dict(y=P + 8), INVALID), (dict(act=1, z=P + 8), INVALID),
