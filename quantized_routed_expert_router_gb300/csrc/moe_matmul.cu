@@ -62,7 +62,7 @@ struct Shape {
     static constexpr int COLS = NBUF * BT;
     static constexpr int BOX = PLACES, LESS = PLACES == 128 ? 64 : PLACES;   // places of a copy, of one for few places
     static constexpr int PIECES = BT < 64 ? 1 : BT / 64;   // 32 places each, of an epilogue warp
-    static_assert(STAGES <= MAX_STAGES && COLS <= 512 && (PAIR || 4 * BT * BN <= STAGES * STAGE), "");
+    static_assert(STAGES <= MAX_STAGES && COLS <= 512 && 4 * BT * BN <= STAGES * STAGE, "");
 };
 
 struct Ctl {
@@ -90,14 +90,14 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t ad, uint64_t bd, u
             "r"(add), "r"(me)
             : "memory");
 }
-// the barrier is told when the products so far are done; of a pair, that of either block
+// the barrier is told when the products so far are done; of a pair, whose first block is `lead` of the cluster, that of either
 template <bool PAIR>
-__device__ __forceinline__ void commit(uint64_t *bar, uint32_t me) {
+__device__ __forceinline__ void commit(uint64_t *bar, int lead, uint32_t me) {
     if constexpr (PAIR)
         asm volatile(
             "{\n .reg .pred e;\n setp.ne.u32 e, %1, 0;\n"
             " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n}" ::"r"(
-                sa(bar)), "r"(me), "h"((uint16_t)3)
+                sa(bar)), "r"(me), "h"((uint16_t)(3 << lead))
             : "memory");
     else
         mma_commit(bar, me);
@@ -217,7 +217,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     __shared__ Ctl c;
     uint8_t *stages = raw + ((1024 - (sa(raw) & 1023)) & 1023);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int rank = PAIR || SPLIT ? (int)cluster_rank() : 0, parts = SPLIT ? (int)cluster_size() : 1;
+    // of the cluster: this block, the first one of its pair; of the pair: this block; of the depth: this block's part
+    const int in_cluster = PAIR || SPLIT ? (int)cluster_rank() : 0, lead = in_cluster & ~1;
+    const int rank = PAIR ? in_cluster & 1 : 0, part = SPLIT ? in_cluster / (PAIR ? 2 : 1) : 0;
+    const int size = PAIR || SPLIT ? (int)cluster_size() : 1, parts = SPLIT ? size / (PAIR ? 2 : 1) : 1;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
@@ -283,12 +286,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     // Rising offsets have fewer than 2^30 tiles (the launch checks it).  Falling ones let groups overlap and can have
     // many more: no more than 2^30 of them, so that tile numbers stay in 32 bits.
     const int total = (int)min((long long)c.tstart[a.G] * a.ntn, 0x3FFFFFFFll);
-    const int t0 = SPLIT ? (int)blockIdx.x / parts : PAIR ? (int)blockIdx.x / 2 : (int)blockIdx.x;
-    const int dt = SPLIT ? total : PAIR ? (int)gridDim.x / 2 : (int)gridDim.x;
-    const int kb0 = SPLIT ? rank * a.KB / parts : 0, kb1 = SPLIT ? (rank + 1) * a.KB / parts : a.KB;
+    const int t0 = (int)blockIdx.x / size, dt = SPLIT ? total : (int)gridDim.x / size;
+    const int kb0 = SPLIT ? part * a.KB / parts : 0, kb1 = SPLIT ? (part + 1) * a.KB / parts : a.KB;
 
     // Registers: the running sums of fp32 results take 128, beside 32 on their way.
-    constexpr bool MOVE = RUNS && PAIR;
+    constexpr bool MOVE = RUNS && PAIR && !SPLIT;
     static_assert(FEED_REGS * 32 * EPI_FIRST + EPI_REGS * 32 * EPI_WARPS <= LAUNCH_REGS * THREADS, "");
     if (warp < EPI_FIRST) {
         if (MOVE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FEED_REGS));
@@ -344,7 +346,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                     if (a.rows) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    bar_arrive_at(&c.other[r.i], 0, me);
+                    bar_arrive_at(&c.other[r.i], lead, me);
                 }
             __syncwarp();
         } else if (warp == 1) {
@@ -379,16 +381,16 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                         for (int k = 0; k < BK / 16; ++k)
                             mma_bf16<PAIR>(tmem + d.i * BT, ad + k * step, bd + 2 * k, idesc, k | (kb - first), me);
-                        commit<PAIR>(&c.done[r.i], me);
+                        commit<PAIR>(&c.done[r.i], lead, me);
                     }
                     if (ok) {
-                        commit<PAIR>(&c.sums[d.i], me);
+                        commit<PAIR>(&c.sums[d.i], lead, me);
                         d.next();
                     }
                 }
             }
             if (!ok) {   // products in flight end before TMEM is freed
-                commit<PAIR>(&c.drain, me);
+                commit<PAIR>(&c.drain, lead, me);
                 bar_settle(&c.drain, 0, clock_hi());
             }
             __syncwarp();
@@ -440,7 +442,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // the sums of a buffer are read
         const auto give_back = [&] {
             fence_before();
-            if (PAIR) bar_arrive_at(&c.read[d.i], 0, lane == 0);
+            if (PAIR) bar_arrive_at(&c.read[d.i], lead, lane == 0);
             else bar_arrive(&c.read[d.i], lane == 0);
             d.next();
         };
@@ -536,27 +538,31 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         cluster_sync();
         if (warp >= EPI_FIRST && t0 < total && !*(volatile int *)&c.abort) {
-            // each block takes every parts-th 4 places, and adds them over the cluster in rank order
+            // Each block takes every parts-th C places, and adds them over the cluster's parts of its columns in order.  A load
+            // takes a microsecond, so a warp has many on their way; and it takes 32 columns side by side (four places of a column
+            // at a time, a row apart, were slower: 128 x 4096 by 1000 x 4096 14.5 us instead of 10.6).
+            constexpr int C = PAIR ? 16 : BT == 32 ? 4 : 8, PARTS = PAIR ? MAX_SPLIT / 2 : MAX_SPLIT;
             const int quad = warp & 3, half = (warp - EPI_FIRST) >> 2;
             const Tile tl = tile_at<BT, PAIR>(&c, a, t0, rank);
             const Column col = column_of(a, tl, quad, lane);
             const uint32_t red = sa(stages) + 4 * (32 * quad + lane);
 #pragma unroll 1
-            for (int j = 4 * (rank + parts * half); j < tl.rows; j += 8 * parts) {
-                float p[MAX_SPLIT][4], v[4];
+            for (int j = C * (part + parts * half); j < tl.rows; j += 2 * C * parts) {
+                float p[PARTS][C], v[C];
 #pragma unroll
-                for (int i = 0; i < MAX_SPLIT; ++i)
+                for (int i = 0; i < PARTS; ++i)
+                    if (i < parts) {
 #pragma unroll
-                    for (int h = 0; h < 4; ++h)
-                        if (i < parts) p[i][h] = ld_peer1(red + (j + h) * 4 * BN, i);
+                        for (int h = 0; h < C; ++h) p[i][h] = ld_peer1(red + (j + h) * 4 * BN, PAIR ? 2 * i + rank : i);
+                    }
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
+                for (int h = 0; h < C; ++h) {
                     v[h] = p[0][h];
 #pragma unroll
-                    for (int i = 1; i < MAX_SPLIT; ++i)
+                    for (int i = 1; i < PARTS; ++i)
                         if (i < parts) v[h] += p[i][h];
                 }
-                const int cnt = min(4, tl.rows - j);
+                const int cnt = min(C, tl.rows - j);
                 if (a.rows) clear_bad(a, v, tl.first + j, cnt, lane);
                 emit_t<false, TY>(a, v, v, cnt, tl.first + j, col.n, col.in, col.bias, lane);
             }
@@ -617,7 +623,7 @@ cudaError_t launch_t(const MatmulArgs &a, int grid, int cluster, cudaStream_t s)
     auto *k = matmul_kernel<BT, PAIR, SPLIT, TY>;
     cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     if (err != cudaSuccess) return err;
-    if (PAIR && sizeof(TY) == 4) {   // the registers that its warps hand on have to be there
+    if (PAIR && !SPLIT && sizeof(TY) == 4) {   // the registers that its warps hand on have to be there
         static const bool there = [k] {
             cudaFuncAttributes at;
             return cudaFuncGetAttributes(&at, k) == cudaSuccess && at.numRegs >= LAUNCH_REGS;
@@ -641,22 +647,23 @@ cudaError_t launch_t(const MatmulArgs &a, int grid, int cluster, cudaStream_t s)
 }
 
 // clusters of SIZE blocks that fit the GPU at once (its SMs come in groups, and a cluster lies within one); 0: not known
-template <int BT, typename TY, int SIZE>
+template <int BT, bool PAIR, typename TY, int SIZE>
 int clusters_at_once() {
     static const int n = [] {
-        auto *k = matmul_kernel<BT, false, true, TY>;
+        auto *k = matmul_kernel<BT, PAIR, true, TY>;
+        constexpr int smem = Shape<BT, PAIR>::SMEM;
         int n = 0;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(SIZE);
         cfg.blockDim = dim3(THREADS);
-        cfg.dynamicSmemBytes = Shape<BT, false>::SMEM;
+        cfg.dynamicSmemBytes = smem;
         cudaLaunchAttribute at[1];
         at[0].id = cudaLaunchAttributeClusterDimension;
         at[0].val.clusterDim.x = SIZE;
         at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
         cfg.attrs = at;
         cfg.numAttrs = 1;
-        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<BT, false>::SMEM) != cudaSuccess ||
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
             cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess) {
             cudaGetLastError();   // this call goes on without
             return 0;
@@ -665,23 +672,33 @@ int clusters_at_once() {
     }();
     return n;
 }
-
-template <int BT, typename TY>
-cudaError_t launch_single(const MatmulArgs &a, long long n, cudaStream_t s) {
-    // Depth in parts while every part still has an SM of its own and 4 blocks of depth, and all clusters run at once (16 of
-    // 8 blocks did not: 64 x 7168 by 2048 x 7168 18.8 us in 8 parts, 14.5 in 4; 64 x 8192 by 512 x 8192 11.5 in 8, 14.6 in 4,
-    // 22.7 in 2; 64 x 4096 by 1000 x 4096 10.4, 12.5 and 14.7).
-    const auto room = [&](int parts, int clusters) { return a.KB >= 4 * parts && n * parts <= num_sms() && n <= clusters; };
-    int split = 1;
-    if (room(2, clusters_at_once<BT, TY, 2>())) split = 2;
-    if (split == 2 && room(4, clusters_at_once<BT, TY, 4>())) split = 4;
-    if (split == 4 && room(MAX_SPLIT, clusters_at_once<BT, TY, MAX_SPLIT>())) split = MAX_SPLIT;
-    if (split > 1) return launch_t<BT, false, true, TY>(a, (int)n * split, split, s);
-    return launch_t<BT, false, false, TY>(a, (int)(n < num_sms() ? n : num_sms()), 1, s);
+// how many parts of the depth n tiles can have: every part with 4 blocks of depth and an SM (a pair: two) of its own, and all
+// clusters at once (16 of 8 blocks did not fit: 64 x 7168 by 2048 x 7168 18.8 us in 8 parts, 14.5 in 4; 64 x 8192 by
+// 512 x 8192 11.5 in 8, 14.6 in 4, 22.7 in 2; 64 x 4096 by 1000 x 4096 10.4, 12.5 and 14.7)
+template <int BT, bool PAIR, typename TY>
+int parts_of(long long n, int KB) {
+    const auto room = [&](int parts, int clusters) {
+        return KB >= 4 * parts && n * parts * (PAIR ? 2 : 1) <= num_sms() && n <= clusters;
+    };
+    if (!room(2, clusters_at_once<BT, PAIR, TY, PAIR ? 4 : 2>())) return 1;
+    if (!room(4, clusters_at_once<BT, PAIR, TY, PAIR ? 8 : 4>())) return 2;
+    if (PAIR || !room(MAX_SPLIT, clusters_at_once<BT, PAIR, TY, 8>())) return 4;
+    return MAX_SPLIT;
+}
+template <int BT, bool PAIR, typename TY>
+cudaError_t launch_tiles(MatmulArgs a, int wide, long long n, int parts, cudaStream_t s) {
+    constexpr int PER = PAIR ? 2 : 1;
+    a.ntn = (wide + PER * BN - 1) / (PER * BN);
+    a.whole = wide / (PER * BN);
+    if constexpr (!PAIR || BT == 256) {   // (of pairs with fewer places there are many)
+        if (parts > 1) return launch_t<BT, PAIR, true, TY>(a, (int)n * parts * PER, parts * PER, s);
+    }
+    const long long most = num_sms() / PER;
+    return launch_t<BT, PAIR, false, TY>(a, (int)(n < most ? n : most) * PER, PER, s);
 }
 
 template <typename TY>
-cudaError_t launch_matmul_t(MatmulArgs a, cudaStream_t s) {
+cudaError_t launch_matmul_t(const MatmulArgs &a, cudaStream_t s) {
     const int wide = a.act == MOE_ACT_SWIGLU ? 2 * a.N : a.N;
     // most tiles there can be: a group's last one may be short
     const long long sms = num_sms(), groups = a.offsets ? (a.G < a.M ? a.G : a.M) : 1;
@@ -690,19 +707,28 @@ cudaError_t launch_matmul_t(MatmulArgs a, cudaStream_t s) {
     };
     if (tiles(32, BN) > 0x3FFFFFFF) return cudaErrorNotSupported;
     const long long rows = a.M / groups;   // of a group on average
-    // Pairs where that leaves one of them for every other SM.  Few places a group: shorter stages, and more of them on their
-    // way (3108 rows over 32 of 2880 x 2880, 97 a group: 104.9 us, by 256 places 108.7).
-    if (rows > 64 && 2 * tiles(256, 2 * BN) >= sms) {
-        const bool less = a.offsets && rows <= 110;
-        a.ntn = (wide + 2 * BN - 1) / (2 * BN);
-        a.whole = wide / (2 * BN);
-        const long long n = tiles(less ? 128 : 256, 2 * BN), most = sms / 2;
-        const int grid = 2 * (int)(n < most ? n : most);
-        return less ? launch_t<128, true, false, TY>(a, grid, 2, s) : launch_t<256, true, false, TY>(a, grid, 2, s);
+    const long long n32 = tiles(32, BN), n128 = tiles(128, BN), n256 = tiles(256, 2 * BN);
+    if (rows <= 32) return launch_tiles<32, false, TY>(a, wide, n32, parts_of<32, false, TY>(n32, a.KB), s);
+    const int single = parts_of<128, false, TY>(n128, a.KB);
+    if (a.offsets) {
+        // Pairs where that leaves one of them for every other SM.  Few places a group: shorter stages, and more of them on
+        // their way (3108 rows over 32 of 2880 x 2880, 97 a group: 104.9 us, by 256 places 108.7).
+        if (rows <= 64 || 2 * n256 < sms) return launch_tiles<128, false, TY>(a, wide, n128, single, s);
+        return rows <= 110 ? launch_tiles<128, true, TY>(a, wide, tiles(128, 2 * BN), 1, s)
+                           : launch_tiles<256, true, TY>(a, wide, n256, 1, s);
     }
-    a.ntn = (wide + BN - 1) / BN;
-    a.whole = wide / BN;
-    return rows <= 32 ? launch_single<32, TY>(a, tiles(32, BN), s) : launch_single<128, TY>(a, tiles(128, BN), s);
+    // One matrix: what takes fewer cycles.  A stage of either comes in about 560 (32 KB from L2); pairs have a longer start and
+    // end, and an exchange between parts its own.  us, by pairs and by one block a tile: 256 x 2048 by 7168 x 2048 16.8, 14.6;
+    // 512 18.7, 24.3; 2048 38.1, 59.6; 512 x 7168 by 2048 x 7168 26.9, 22.8; 1024 28.8, 35.0; 2048 x 1000 by 1000 x 1000
+    // 16.5, 12.6.
+    const int both = parts_of<256, true, TY>(n256, a.KB);
+    const auto cycles = [&](long long n, int parts, long long slots, int stage, int fixed, int exchange) {
+        return (n + slots - 1) / slots * ((a.KB + parts - 1) / parts) * stage + fixed + (parts > 1 ? exchange : 0);
+    };
+    if (cycles(n256, both, both > 1 ? n256 : sms / 2, 550, 18000, 6000) <
+        cycles(n128, single, single > 1 ? n128 : sms, 575, 9000, 4000))
+        return launch_tiles<256, true, TY>(a, wide, n256, both, s);
+    return launch_tiles<128, false, TY>(a, wide, n128, single, s);
 }
 
 }  // namespace

@@ -130,7 +130,7 @@ def run_dense(M, N, K, act, dtype, transposed=False, bias=False, residual=None, 
 DENSE = [(1, 1, 8), (1, 16, 64), (1, 2048, 4096), (2, 7, 72), (3, 136, 4096), (5, 24, 40), (8, 200, 4112), (15, 2051, 1008),
          (16, 7168, 512), (17, 100, 1040), (31, 129, 136), (33, 130, 64), (40, 136, 8192), (64, 512, 1024), (65, 1000, 72),
          (100, 333, 2048), (127, 257, 272), (128, 128, 128), (129, 384, 640), (200, 1026, 4096), (255, 60, 24),
-         (257, 300, 336), (300, 2880, 2880), (333, 4000, 256), (513, 129, 4000), (1000, 1536, 4096), (2048, 2560, 272),
+         (257, 300, 336), (300, 2880, 2880), (333, 4000, 256), (513, 129, 4000), (600, 1030, 4096), (400, 512, 8192), (1000, 1536, 4096), (2048, 2560, 272),
          (2500, 2051, 400), (4100, 1000, 1168)]
 
 
@@ -141,7 +141,7 @@ def test_dense(M, N, K, dtype):
 
 
 # every activation with everything that may go with it, at one row, few rows, a split depth, whole tiles, ragged ones
-SHAPES = [(1, 48, 264), (4, 512, 2048), (21, 144, 4096), (130, 272, 200), (300, 2880, 288), (1100, 400, 136)]
+SHAPES = [(1, 48, 264), (4, 512, 2048), (21, 144, 4096), (130, 272, 200), (300, 2880, 288), (700, 528, 2056), (1100, 400, 136)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)

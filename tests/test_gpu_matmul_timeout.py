@@ -14,7 +14,7 @@ moe = pytest.importorskip("quantized_routed_expert_router_gb300")
 DEV = "cuda"
 
 # few places (transposed: by tiles) and many, whole depth and in parts, one block a tile and two, more depth than the ring and less
-SIZES = [(33, 272, 4096), (40, 7168, 200), (100, 400, 4096), (100, 4000, 1024), (2500, 1040, 400), (4000, 2048, 1024)]
+SIZES = [(33, 272, 4096), (40, 7168, 200), (100, 400, 4096), (600, 1000, 4096), (100, 4000, 1024), (2500, 1040, 400), (4000, 2048, 1024)]
 
 
 @pytest.mark.gpu
