@@ -28,8 +28,9 @@
 // in rank order.
 //
 // Sums.  The tensor cores cut off what they add below the 24 bits of a running sum, always towards
-// zero: over K values that is about K 2^-34 of the sum, 1.7e-6 at K = 2048.  Beside a rounding to bf16 it does
-// not count.  For fp32 results (TY = float) a running sum is 512 values of depth long and these are added in fp32.
+// zero: over K values that is about K 2^-30 of the sum, 1.7e-6 at K = 2048.  Beside a rounding to bf16 it does
+// not count.  For fp32 results (TY = float) a running sum is at most 640 values of depth long and these are added
+// in fp32: 3e-7 to 6e-7, the more the larger a few channels of the rows are (768 long: 6e-7 to 9e-7).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -50,7 +51,9 @@ constexpr int MAX_SPLIT = 8;        // blocks that share a tile's depth
 constexpr int MAX_STAGES = 10;
 // registers a thread: at the launch, and where the epilogue takes some of the feeding warps'
 constexpr int LAUNCH_REGS = 168, FEED_REGS = 88, EPI_REGS = 208;
-constexpr int RUN = 12;             // stages of a running sum of fp32 results
+// stages of a running sum of fp32 results: of a tile's first two, which the products can fill while the epilogue is busy with
+// the tile before, and of the others
+constexpr int FIRST_RUNS = 10, RUN = 8;
 
 template <int BT, bool PAIR>
 struct Shape {
@@ -288,6 +291,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int total = (int)min((long long)c.tstart[a.G] * a.ntn, 0x3FFFFFFFll);
     const int t0 = (int)blockIdx.x / size, dt = SPLIT ? total : (int)gridDim.x / size;
     const int kb0 = SPLIT ? part * a.KB / parts : 0, kb1 = SPLIT ? (part + 1) * a.KB / parts : a.KB;
+    const auto run_end = [&](int kb) {   // of the running sum that starts with stage kb
+        return !RUNS ? kb1 : min(kb + (kb < kb0 + 2 * FIRST_RUNS ? FIRST_RUNS : RUN), kb1);
+    };
 
     // Registers: the running sums of fp32 results take 128, beside 32 on their way.
     constexpr bool MOVE = RUNS && PAIR && !SPLIT;
@@ -362,7 +368,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int rows = __shfl_sync(0xFFFFFFFFu, (tile_at<BT, PAIR>(&c, a, t, rank).rows), 0);
                 const uint32_t idesc = idesc0 | ((uint32_t)(PAIR ? half_of(rows) >> 3 : (rows + 15) >> 4) << 18);
                 for (int kb = kb0; kb < kb1 && ok;) {
-                    const int first = kb, end = RUNS ? min(kb + RUN, kb1) : kb1;
+                    const int first = kb, end = run_end(kb);
                     ok = bar_wait(&c.read[d.i], d.phase ^ 1, &c.abort, a.wait, a.status);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
@@ -476,7 +482,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     else fetch_extra<false, TY>(a, tl.first + j, tl.rows - j, col.n, x);
                 };
                 extra(place_of(0));
-                for (int kb = kb0; kb < kb1; kb += RUN) {
+                for (int kb = kb0; kb < kb1; kb = run_end(kb)) {
                     ok = bar_wait(&c.sums[d.i], d.phase, &c.abort, a.wait, a.status);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
@@ -505,11 +511,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                         v[i] = acc[0][i];
                         now[i] = x[i];
                     }
-                    extra(place_of(q + 1));
 #pragma unroll
                     for (int k = 1; k < 2 * S::PIECES; ++k)
 #pragma unroll
                         for (int i = 0; i < 16; ++i) v[i] = q == k ? acc[k >> 1][16 * (k & 1) + i] : v[i];
+                    extra(place_of(q + 1));
                     pass_on(v, now, j);
                 }
             } else {
