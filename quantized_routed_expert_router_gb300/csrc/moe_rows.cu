@@ -6,7 +6,10 @@
 // it a thread, whole 16-byte pieces where the width allows.  Tokens are what the
 // blocks are dealt by: a block has a token's k places in hand, so that a token's
 // row is read (or written) once for all of them, nothing is added by atomics, and
-// the k rows of a piece are on their way at once.
+// the k rows of a piece are on their way at once.  DRAM bounds all three.  On the
+// device: combine 8192 x 8 rows of 4096 in bf16 90.8 us (0.98 of the copy rate),
+// dispatch 4096 x 8 of 7168 78.5 (0.97), the gradient 8191 x 4 of 2880 65.7 (0.95;
+// 86.6 with blocks of 128 threads whose last round over a row was mostly empty).
 #include <cuda_bf16.h>
 
 #include "moe_around.h"
