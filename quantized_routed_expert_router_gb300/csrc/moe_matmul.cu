@@ -181,20 +181,19 @@ __device__ __forceinline__ Column column_of(const MatmulArgs &a, const Tile &tl,
     c.bias = a.bias && c.in ? a.bias[at] : 0.f;
     return c;
 }
-// what the epilogue reads of this warp's places and columns, into L2 while the products run (2048 deep with an fp32
-// residual: 227 us without, of which 150 are without the residual)
+// what an fp32 epilogue reads (the residual, or z) for places lo .. hi - 1 of a tile into L2; thread `id` of the epilogue's
 template <typename TY>
-__device__ __forceinline__ void prefetch_rows(const MatmulArgs &a, const Tile &tl, int quad, int half, int lane) {
-    const bool grad = a.act >= MOE_ACT_SILU_GRAD, both = a.act == MOE_ACT_SWIGLU_GRAD, gated = a.act == MOE_ACT_SWIGLU;
-    const TY *p = static_cast<const TY *>(grad ? a.z : a.residual);
-    const int n = tl.n0 + (gated ? 16 : 32) * quad, have = min(gated ? 16 : 32, a.N - n);
-    if (!p || have <= 0) return;
+__device__ __forceinline__ void prefetch_rows(const MatmulArgs &a, const TY *p, const Tile &tl, int lo, int hi, int id) {
+    constexpr int LINE = 128 / (int)sizeof(TY), LINES = BN / LINE;   // of a place
+    const bool both = a.act == MOE_ACT_SWIGLU_GRAD;
+    const int have = min(a.act == MOE_ACT_SWIGLU ? BN / 2 : BN, a.N - tl.n0), i = id % LINES * LINE;
+    if (i >= have) return;
     const size_t pitch = both ? 2 * (size_t)a.N : (size_t)a.N;
-    for (int j = 32 * half + lane; j < tl.rows; j += 64)
+    for (int j = lo + id / LINES; j < hi; j += 32 * EPI_WARPS / LINES)
         for (int h = 0; h <= (both ? 1 : 0); ++h) {
-            const TY *at = p + (size_t)(tl.first + j) * pitch + (size_t)h * a.N + n;
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(at + have - 1));
+            const TY *at = p + (size_t)(tl.first + j) * pitch + (size_t)h * a.N + tl.n0;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(at + i));
+            if (i == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + have - 1));   // (a row can start inside a line)
         }
 }
 // places first .. first + cnt - 1 whose row index is bad: their products are 0
@@ -459,7 +458,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int t = t0; t < total; t += dt) {
             const Tile tl = tile_at<BT, PAIR>(&c, a, t, rank);
             const Column col = column_of(a, tl, quad, lane);
-            if (!SPLIT) prefetch_rows<TY>(a, tl, quad, half, lane);
             // 16 places of this warp to the others of the cluster (over the stages: every copy and product is done), or out
             const auto pass_on = [&](float(&v)[16], const float(&x)[16], int j) {
                 if (SPLIT) {
@@ -486,7 +484,17 @@ __global__ void __launch_bounds__(THREADS, 1)
                     else fetch_extra<false, TY>(a, tl.first + j, tl.rows - j, col.n, x);
                 };
                 extra(place_of(0));
+                // All that the tile's 16s read comes into L2 while its products run, in shares: 8192 x 2048 by 7168 x 2048
+                // with a residual takes 202 us so, 214 with all of it asked for at once, 227 with none.  (bf16 results have
+                // half the bytes and no shares to wait for: 144 us either way, z's SwiGLU slopes 112 without and 114 with.)
+                const TY *extras = SPLIT ? nullptr : static_cast<const TY *>(a.act >= MOE_ACT_SILU_GRAD ? a.z : a.residual);
+                int asked = 0;
                 for (int kb = kb0; kb < kb1; kb = run_end(kb)) {
+                    if (extras) {
+                        const int upto = (int)((long long)tl.rows * (run_end(kb) - kb0) / (kb1 - kb0));
+                        prefetch_rows(a, extras, tl, asked, upto, (int)threadIdx.x - 32 * EPI_FIRST);
+                        asked = upto;
+                    }
                     ok = bar_wait(&c.sums[d.i], d.phase, &c.abort, a.wait, a.status);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
