@@ -12,10 +12,12 @@
 // (choose_exactly): two of the k + 1 largest that agree in their upper 22 bits (fp32
 // logits: about two rows in a hundred; bf16 ones are exact), or four of the chosen in
 // one lane (8 of 256: four rows in a thousand; 32 of 1024: half of them).
-// Issue slots bound it: 65536 rows of 256 in fp32, 8 chosen, take 26.5 us on the
-// device (2.7 TB/s; 298 instructions a row, the integer pipe 63% busy), 63.6 when
-// every round looked through all values of its lane.  The gradient moves more and
-// decides less: 65536 x 128 in bf16 over all E 12.4 us (4.4 TB/s).
+// Issue slots bound it: 65536 rows of 512 in fp32, 8 chosen, take 38 us on the
+// device.  Many rows of up to 256, of which up to eight are chosen, go four to a
+// warp (topk_quad_kernel): 65536 x 256 in fp32 23.6 us (26.2 with a warp a row, 63.6
+// when every round looked through all values of its lane), x 128 15.2 (19.3),
+// x 64 12.2 (18.7).  The gradient moves more and decides less: 65536 x 128 in bf16
+// over all E 12.4 us (4.4 TB/s).
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -31,6 +33,8 @@ constexpr unsigned kAll = 0xFFFFFFFFu;
 // blocks of a launch that share an SM (registers for the rows in hand); of the gradient, with one row more
 constexpr int grad_blocks(int values) { return values <= 4 ? 5 : values <= 8 ? 4 : values <= 16 ? 2 : 1; }
 constexpr int blocks_per_sm(int values) { return values <= 4 ? 6 : values <= 8 ? 5 : values <= 16 ? 3 : 2; }
+
+constexpr int quad_blocks(int pieces) { return pieces <= 2 ? 5 : pieces <= 4 ? 4 : 3; }
 
 constexpr uint32_t kNone = 0x007FFFFFu;   // the key of -inf: what is not above it may not be taken
 constexpr uint32_t kIndex = MOE_MAX_EXPERTS - 1;
@@ -121,6 +125,36 @@ __device__ __forceinline__ void order2(uint32_t &a, uint32_t &b) {
     a = m;
 }
 
+// in falling order
+__device__ __forceinline__ void sort4(uint32_t b[4]) {
+    order2(b[0], b[1]);
+    order2(b[2], b[3]);
+    order2(b[0], b[2]);
+    order2(b[1], b[3]);
+    order2(b[1], b[2]);
+}
+// the four largest of two ordered fours, in order
+__device__ __forceinline__ void merge4(uint32_t a[4], const uint32_t b[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = max(a[i], b[3 - i]);   // rising and falling
+    order2(a[0], a[2]);
+    order2(a[1], a[3]);
+    order2(a[0], a[1]);
+    order2(a[2], a[3]);
+}
+// of eight that rise and fall
+__device__ __forceinline__ void sort_bitonic8(uint32_t c[8]) {
+#pragma unroll
+    for (int step = 4; step >= 1; step >>= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (!(i & step)) order2(c[i], c[i + step]);
+}
+// the key that carries expert e's index
+__device__ __forceinline__ uint32_t key_with(float v, int e) { return (key_of(v) & ~kIndex) | (kIndex & ~(uint32_t)e); }
+// a key as choose makes them, of a choice by whole keys (e < 0: none)
+__device__ __forceinline__ uint32_t key_of_choice(int e) { return e >= 0 ? ~kIndex | (kIndex - e) : 0; }
+
 // the k largest of a row by whole keys, the expert of slot s in lane s (-1: none): each round finds the largest key of the
 // warp; where several lanes hold it, the one with the lowest index wins
 template <typename T, int VEC, int J>
@@ -162,23 +196,14 @@ __device__ __forceinline__ bool choose(const Row<T, VEC, J> &row, int k, int lan
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int at = j + i, e = 32 * VEC * (at / VEC) + VEC * lane + at % VEC;
-            b[i] = at < VEC * J ? (key_of(row.value(at % (VEC * J))) & ~kIndex) | (kIndex & ~(uint32_t)e) : 0;
+            b[i] = at < VEC * J ? key_with(row.value(at % (VEC * J)), e) : 0;
         }
-        order2(b[0], b[1]);
-        order2(b[2], b[3]);
-        order2(b[0], b[2]);
-        order2(b[1], b[3]);
-        order2(b[1], b[2]);
+        sort4(b);
         if (j == 0) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) a[i] = b[i];
-        } else {   // the four largest of both: rising and falling, then in order
-#pragma unroll
-            for (int i = 0; i < 4; ++i) a[i] = max(a[i], b[3 - i]);
-            order2(a[0], a[2]);
-            order2(a[1], a[3]);
-            order2(a[0], a[1]);
-            order2(a[2], a[3]);
+        } else {
+            merge4(a, b);
         }
     }
     // The lists lie in shared memory, a lane its column, with a 0 behind them.  Whose value is the largest writes it to the
@@ -262,7 +287,7 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(VEC * J)) topk_kern
             for (int i = 0; i < n; ++i) {
                 if (!(unsure >> i & 1)) continue;
                 const int e = choose_exactly<T, VEC, J>(logits + (size_t)(base + i) * a.E, a.E, a.k, lane);
-                if (lane < a.k) slots[i * (a.width + 1) + lane] = e >= 0 ? ~kIndex | (kIndex - e) : 0;
+                if (lane < a.k) slots[i * (a.width + 1) + lane] = key_of_choice(e);
             }
             __syncwarp();
             key = slots[at];
@@ -278,6 +303,124 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(VEC * J)) topk_kern
             if (a.weights) a.weights[to] = w;
         }
         __syncwarp();
+    }
+}
+
+// Up to eight of up to 256, many rows: eight lanes hold a row, four rows a warp.  A lane orders its 4 J values down to its
+// four largest, and lanes join theirs in three steps of an exchange and a merge, so that all eight have the row's eight
+// largest in order.  What a step costs is shared by four rows.  `lost` is the largest that the joined lists left out, `dropped`
+// the largest that the lane's own left out (five of the chosen in one lane: one row in a hundred with 8 of 256).
+template <typename T, int J, bool ALL>
+__global__ void __launch_bounds__(32 * kWarps, quad_blocks(J)) topk_quad_kernel(const TopkArgs a) {
+    constexpr int L = 8;
+    const int lane = threadIdx.x & 31, s = lane & (L - 1), r = lane / L;
+    const int warp = blockIdx.x * kWarps + (threadIdx.x >> 5), warps = gridDim.x * kWarps;
+    const T *logits = static_cast<const T *>(a.logits);
+    const int fours = (int)(((long long)a.T + 3) / 4), end = (int)((long long)fours * (warp + 1) / warps);
+    int four = (int)((long long)fours * warp / warps);
+    Row<T, 4, J, L> row;
+    bool next_live = false;
+    if (four < end && 4 * four + r < a.T) {
+        row.load(logits + (size_t)(4 * four + r) * a.E, a.E, s);
+        next_live = !a.valid || a.valid[4 * four + r];
+    }
+    for (; four < end; ++four) {
+        const int t = 4 * four + r;
+        const bool live = next_live, more = four + 1 < end && t + 4 < a.T;
+        float all = 0.f;
+        if (ALL) {
+            float m = row.value(0);
+#pragma unroll
+            for (int i = 1; i < 4 * J; ++i) m = max_nan(m, row.value(i));
+            all = row.sum(lanes_max<L>(m));
+        }
+        next_live = more && (!a.valid || a.valid[t + 4]);
+        const T *next = logits + (size_t)(t + 4) * a.E;
+        uint32_t own[4], c[8], lost = 0, dropped = 0;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int e = 4 * L * j + 4 * s;
+            uint32_t b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[i] = key_with(row.v[j].value(i), 4 * L * j + i + 4 * (L - 1));   // (s comes below)
+            if (more && e < a.E) row.v[j].load(next + e);   // the next row's, where these were
+            sort4(b);
+            if (j == 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) own[i] = b[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; i += 2)
+                    dropped = max(dropped, max(min(own[i], b[3 - i]), min(own[i + 1], b[2 - i])));
+                merge4(own, b);
+            }
+        }
+        const uint32_t at_lane = 4 * (L - 1 - s);
+        dropped |= at_lane;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) own[i] |= at_lane;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = own[i], c[7 - i] = __shfl_xor_sync(kAll, own[i], 1);
+        sort_bitonic8(c);
+#pragma unroll
+        for (int off = 2; off <= 4; off *= 2) {
+            uint32_t o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = __shfl_xor_sync(kAll, c[7 - i], off);
+            if (sizeof(T) == 4) {
+                if (off == 4) lost = max(lost, __shfl_xor_sync(kAll, lost, off));
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) lost = max(lost, max(min(c[i], o[i]), min(c[i + 1], o[i + 1])));
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) c[i] = max(c[i], o[i]);
+            sort_bitonic8(c);
+        }
+        uint32_t key = c[0];   // of slot s
+#pragma unroll
+        for (int i = 1; i < 8; ++i) key = s == i ? c[i] : key;
+        // Not certain: what a lane dropped may belong to the chosen, or the last one's rank hangs on the bits that the index took.
+        const uint32_t last = __shfl_sync(kAll, key, (lane & ~(L - 1)) + a.k - 1);
+        bool unsure = dropped > kNone && (sizeof(T) == 4 ? dropped | kIndex : dropped) >= last, tied = false;
+        if (sizeof(T) == 4) {
+            const uint32_t down = __shfl_down_sync(kAll, key, 1), below = s == L - 1 ? lost : down;
+            const bool close = live && s < a.k && below > kNone && (key ^ below) <= kIndex;
+            unsure |= close && s == a.k - 1;
+            tied = close && s < a.k - 1;   // only their order is not certain
+        }
+        unsigned who = __ballot_sync(kAll, unsure && live);
+        for (; who; who &= ~(0xFFu << (__ffs(who) - 1 & ~(L - 1)))) {
+            const int q = (__ffs(who) - 1) / L;
+            const int e = choose_exactly<T, 4, (J + 3) / 4>(logits + (size_t)(4 * four + q) * a.E, a.E, a.k, lane);
+            const uint32_t other = key_of_choice(__shfl_sync(kAll, e, s));
+            if (r == q) key = other;
+        }
+        const bool mine = s < a.k && t < a.T;
+        int id = mine && live && key > kNone ? (int)(kIndex - (key & kIndex)) : -1;
+        float l = id >= 0 ? (float)logits[(size_t)t * a.E + id] : -INFINITY;
+        if (__any_sync(kAll, tied)) {   // by whole keys (those of a choice by whole keys are in order)
+            const uint32_t whole = id >= 0 ? key_of(l) : 0;
+            int rank = 0, from = 0;
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                const uint32_t o = __shfl_sync(kAll, whole, i, L);
+                const int oid = __shfl_sync(kAll, id, i, L);
+                rank += o > whole || (o == whole && (id >= 0 ? oid < id : i < s));
+            }
+#pragma unroll
+            for (int i = 0; i < L; ++i)
+                if (__shfl_sync(kAll, rank, i, L) == s) from = i;
+            id = __shfl_sync(kAll, id, from, L);
+            l = __shfl_sync(kAll, l, from, L);
+        }
+        const float m = __shfl_sync(kAll, l, lane - s);
+        float slope;
+        const float w = weight_of(l, m, all, a.sigmoid, a.renorm, L, slope);
+        if (mine) {
+            const size_t to = (size_t)t * a.k + s;
+            a.ids[to] = id;
+            if (a.weights) a.weights[to] = w;
+        }
     }
 }
 
@@ -405,6 +548,13 @@ cudaError_t topk_t(TopkArgs a, cudaStream_t s) {
     else topk_kernel<T, VEC, J, false><<<grid, 32 * kWarps, 0, s>>>(a);
     return cudaGetLastError();
 }
+template <typename T, int J>
+cudaError_t quad_t(const TopkArgs &a, cudaStream_t s) {
+    const unsigned grid = blocks((int)(((long long)a.T + 3) / 4), quad_blocks(J));
+    if (!a.sigmoid && !a.renorm) topk_quad_kernel<T, J, true><<<grid, 32 * kWarps, 0, s>>>(a);
+    else topk_quad_kernel<T, J, false><<<grid, 32 * kWarps, 0, s>>>(a);
+    return cudaGetLastError();
+}
 template <typename T, int VEC, int J, int L>
 cudaError_t grad_t(const TopkGradArgs &a, cudaStream_t s) {
     constexpr int smem = kWarps * 32 * VEC * J * (int)sizeof(float);   // 32 KB at most
@@ -418,6 +568,11 @@ cudaError_t grad_t(const TopkGradArgs &a, cudaStream_t s) {
 template <typename T>
 cudaError_t topk_by_width(const TopkArgs &a, cudaStream_t s) {
     if (a.E % 4 == 0) {
+        // (fewer rows have a warp each, with a shorter chain: 256 of 256 take 3.4 us so, 3.9 by fours; 4096 5.4 and 4.3)
+        if (a.k <= 8 && a.E <= 256 && a.T >= 8 * a.E) {
+            if (a.E <= 64) return quad_t<T, 2>(a, s);
+            return a.E <= 128 ? quad_t<T, 4>(a, s) : quad_t<T, 8>(a, s);
+        }
         if (a.E <= 128) return topk_t<T, 4, 1>(a, s);
         if (a.E <= 256) return topk_t<T, 4, 2>(a, s);
         if (a.E <= 512) return topk_t<T, 4, 4>(a, s);

@@ -146,6 +146,71 @@ def test_padded_tokens(dtype):
     assert torch.equal(ids[on].long(), order(clean, 6)[on]) and (ids[~on] == -1).all() and (w[~on] == 0).all()
 
 
+MANY = 40003      # rows enough that several share a warp
+
+
+@pytest.mark.parametrize("E,k", [(8, 8), (12, 1), (60, 4), (64, 8), (100, 7), (128, 8), (132, 8), (256, 8), (256, 3),
+                                 (256, 9), (61, 8), (260, 8)])
+@pytest.mark.parametrize("gating", [moe.SOFTMAX, moe.SIGMOID])
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_rows(E, k, gating, renormalize, dtype):
+    l = logits(MANY, E, torch.Generator(device=DEV).manual_seed(E + k), dtype)
+    ids = torch.full((MANY + 1, k), 7, dtype=torch.int32, device=DEV)
+    w = torch.full((MANY + 1, k), 7.0, device=DEV)
+    moe.moe_topk(l, gating, renormalize, ids[:MANY], w[:MANY])
+    want = order(l, k)
+    assert torch.equal(ids[:MANY].long(), want)
+    ww, rel = weights_of(l, want, gating, renormalize)[:2]
+    assert bool(((w[:MANY].double() - ww).abs() <= rel * ww + TINY).all())
+    assert (ids[MANY] == 7).all() and (w[MANY] == 7).all()
+    alone = torch.empty_like(ids)
+    moe.moe_topk(l, gating, renormalize, alone[:MANY])
+    assert torch.equal(alone[:MANY], ids[:MANY])
+
+
+def awkward(T, E, dtype):
+    """Rows of eleven kinds in turn, so that those of a warp differ; every kind meets every place in a warp."""
+    g = torch.Generator(device=DEV).manual_seed(E)
+    l = torch.randn(T, E, generator=g, device=DEV)
+    inf, kind = float("inf"), torch.arange(T, device=DEV) % 11
+    col = torch.arange(E, device=DEV)
+    l[kind == 1] = 0.0
+    l[kind == 2] = torch.where(col % 3 == 1, 0.0, -0.0)
+    l[kind == 3] = torch.where(col >= 3, -inf, l[kind == 3])                     # fewer than the slots
+    l[kind == 4] = -inf
+    l[kind == 5] = torch.finfo(dtype).min
+    l[kind == 6] = torch.where(col % 19 == 5, float("nan"), l[kind == 6])
+    lane = torch.randint(0, 8, (T, 1), generator=g, device=DEV)
+    crowd = (col // 4 % 8 == lane) | (col // 4 % 32 == lane)                      # the largest side by side
+    l = torch.where((kind == 7)[:, None] & crowd, l + 20, l)
+    l[kind == 8] = (1 + torch.randint(0, 40, (int((kind == 8).sum()), E), generator=g, device=DEV) * 2.0 ** -23)
+    l[kind == 9] = torch.where(col % 50 == 3, inf, l[kind == 9])
+    l[kind == 10] = torch.sort(l[kind == 10], dim=1).values
+    return l.to(dtype)
+
+
+@pytest.mark.parametrize("E,k", [(256, 8), (256, 5), (128, 8), (60, 6), (32, 8)])
+@pytest.mark.parametrize("gating,renormalize", [(moe.SOFTMAX, True), (moe.SIGMOID, True), (moe.SIGMOID, False)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_awkward_rows(E, k, gating, renormalize, dtype):
+    """As the definition has them, and as calls of a few rows do: the same weights to the bit."""
+    l = awkward(MANY, E, dtype)
+    valid = torch.rand(MANY, generator=torch.Generator(device=DEV).manual_seed(4), device=DEV) < 0.8
+    for on in (None, valid):
+        ids = torch.full((MANY, k), 7, dtype=torch.int32, device=DEV)
+        w = torch.full((MANY, k), 7.0, device=DEV)
+        moe.moe_topk(l, gating, renormalize, ids, w, valid=on)
+        want = order(l, k) if on is None else torch.where(on[:, None], order(l, k), -1)
+        assert torch.equal(ids.long(), want)
+        few, few_w = torch.empty_like(ids), torch.empty_like(w)
+        for t in range(0, MANY, 1000):
+            to = min(t + 1000, MANY)   # (1000 rows of any E start on 16 bytes)
+            moe.moe_topk(l[t:to], gating, renormalize, few[t:to], few_w[t:to], valid=None if on is None else on[t:to])
+        assert torch.equal(ids, few) and torch.equal(w.nan_to_num(nan=-1.0), few_w.nan_to_num(nan=-1.0))
+        assert torch.equal(torch.isnan(w), torch.isnan(few_w))
+
+
 def gradient(l, ids, d, gating, renormalize):
     """dlogits in 64 bits by autograd, without the tolerance."""
     l = l.double().requires_grad_(True)
