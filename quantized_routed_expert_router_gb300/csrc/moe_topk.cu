@@ -12,12 +12,13 @@
 // (choose_exactly): two of the k + 1 largest that agree in their upper 22 bits (fp32
 // logits: about two rows in a hundred; bf16 ones are exact), or four of the chosen in
 // one lane (8 of 256: four rows in a thousand; 32 of 1024: half of them).
-// Issue slots bound it: 65536 rows of 512 in fp32, 8 chosen, take 38 us on the
-// device.  Many rows of up to 256, of which up to eight are chosen, go four to a
-// warp (topk_quad_kernel): 65536 x 256 in fp32 23.6 us (26.2 with a warp a row, 63.6
-// when every round looked through all values of its lane), x 128 15.2 (19.3),
-// x 64 12.2 (18.7).  The gradient moves more and decides less: 65536 x 128 in bf16
-// over all E 12.4 us (4.4 TB/s).
+// Issue slots bound it: 65536 rows of 256 in fp32, 8 chosen, take 26.2 us on the
+// device so (298 instructions a row, the integer pipe 63% busy), 63.6 when every round
+// looked through all values of its lane.  Many rows of up to 512, of which up to eight
+// are chosen, go four to a warp (topk_quad_kernel): x 512 28.3 us (38.9 with a warp a
+// row), x 256 19.9 (26.2), x 128 15.2 (19.3), x 64 12.2 (18.7); in bf16 19.6 (34.6),
+// 14.1 (23.7), 13.7 (16.8), 11.2 (16.8).  The gradient moves more and decides less:
+// 65536 x 128 in bf16 over all E 12.4 us (4.4 TB/s).
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -34,7 +35,9 @@ constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr int grad_blocks(int values) { return values <= 4 ? 5 : values <= 8 ? 4 : values <= 16 ? 2 : 1; }
 constexpr int blocks_per_sm(int values) { return values <= 4 ? 6 : values <= 8 ? 5 : values <= 16 ? 3 : 2; }
 
-constexpr int quad_blocks(int pieces) { return pieces <= 2 ? 5 : pieces <= 4 ? 4 : 3; }
+constexpr int quad_blocks(int pieces, int bytes) {
+    return pieces <= 2 ? 5 : pieces <= 4 || (pieces <= 8 && bytes == 2) ? 4 : pieces <= 8 ? 3 : 2;
+}
 
 constexpr uint32_t kNone = 0x007FFFFFu;   // the key of -inf: what is not above it may not be taken
 constexpr uint32_t kIndex = MOE_MAX_EXPERTS - 1;
@@ -86,12 +89,30 @@ struct Row {
     __device__ __forceinline__ float value(int i) const { return v[i / VEC].value(i % VEC); }   // i: of VEC * J
     // sum of exp(l - m)
     __device__ __forceinline__ float sum(float m) const {
+        constexpr int RUN = VEC * J < 32 ? VEC * J : 32;   // (no more additions in turn)
         float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < VEC * J; ++i) s += exp_fast(value(i) - m);
+        for (int i = 0; i < VEC * J; i += RUN) {
+            float part = 0.f;
+#pragma unroll
+            for (int k = 0; k < RUN; ++k) part += exp_fast(value(i + k) - m);
+            s = i ? s + part : part;
+        }
         return lanes_sum<L>(s);
     }
 };
+
+// of four; a NaN is the largest
+__device__ __forceinline__ float largest(const Raw<float, 4> &r) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(r.value(0)), "f"(r.value(1)), "f"(r.value(2)));
+    return max_nan(m, r.value(3));
+}
+__device__ __forceinline__ float largest(const Raw<__nv_bfloat16, 4> &r) {
+    uint32_t m;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(r.w[0]), "r"(r.w[1]));
+    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+}
 
 // A row's slots lie in `width` lanes side by side, each with a chosen logit (-inf: none); m: the row's largest, all: sum of
 // exp(l - m) over the row where the weights are shares of it.  The slot's weight; slope: 1 - sigma(l), or 1 for softmax.
@@ -141,6 +162,29 @@ __device__ __forceinline__ void merge4(uint32_t a[4], const uint32_t b[4]) {
     order2(a[1], a[3]);
     order2(a[0], a[1]);
     order2(a[2], a[3]);
+}
+// two ordered fours, one behind the other, into one order
+__device__ __forceinline__ void join8(uint32_t b[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) order2(b[i], b[i + 4]);
+    order2(b[2], b[4]);
+    order2(b[3], b[5]);
+    order2(b[1], b[2]);
+    order2(b[3], b[4]);
+    order2(b[5], b[6]);
+}
+// c becomes the eight largest (rising and falling) of it and the lane's `off` away, both in order; returns the largest that is not
+__device__ __forceinline__ uint32_t take8(uint32_t c[8], int off, bool count) {
+    uint32_t o[8], lost = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = __shfl_xor_sync(kAll, c[7 - i], off);
+    if (count) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) lost = max(lost, max(min(c[i], o[i]), min(c[i + 1], o[i + 1])));
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = max(c[i], o[i]);
+    return lost;
 }
 // of eight that rise and fall
 __device__ __forceinline__ void sort_bitonic8(uint32_t c[8]) {
@@ -306,12 +350,17 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(VEC * J)) topk_kern
     }
 }
 
-// Up to eight of up to 256, many rows: eight lanes hold a row, four rows a warp.  A lane orders its 4 J values down to its
-// four largest, and lanes join theirs in three steps of an exchange and a merge, so that all eight have the row's eight
-// largest in order.  What a step costs is shared by four rows.  `lost` is the largest that the joined lists left out, `dropped`
-// the largest that the lane's own left out (five of the chosen in one lane: one row in a hundred with 8 of 256).
+// Up to eight of up to 512, many rows: eight lanes hold a row, four rows a warp, so that four rows share what a step costs.
+// Lists of a row's lanes are joined in three steps of an exchange and a merge; then all eight lanes have its eight largest.
+//   - Up to 128 experts a lane orders its values down to its four largest.  What it leaves out may belong to the chosen (five of
+//     eight in one lane: one row in a hundred).
+//   - Above, the pieces of four values are ordered by their largest first: the eight largest values lie in the eight pieces
+//     that are largest so, and each lane reads one of those again and orders its four.  This costs 3 instructions a value
+//     instead of 11 (65536 x 256 in fp32: 23.6 us without it).
+// `dropped`: the largest key that this lane saw left out.  In bf16 keys are exact, and so is the choice of pieces: whatever is
+// left out of them is smaller than eight values, or equal with a higher index.
 template <typename T, int J, bool ALL>
-__global__ void __launch_bounds__(32 * kWarps, quad_blocks(J)) topk_quad_kernel(const TopkArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, quad_blocks(J, sizeof(T))) topk_quad_kernel(const TopkArgs a) {
     constexpr int L = 8;
     const int lane = threadIdx.x & 31, s = lane & (L - 1), r = lane / L;
     const int warp = blockIdx.x * kWarps + (threadIdx.x >> 5), warps = gridDim.x * kWarps;
@@ -336,44 +385,79 @@ __global__ void __launch_bounds__(32 * kWarps, quad_blocks(J)) topk_quad_kernel(
         }
         next_live = more && (!a.valid || a.valid[t + 4]);
         const T *next = logits + (size_t)(t + 4) * a.E;
-        uint32_t own[4], c[8], lost = 0, dropped = 0;
+        uint32_t own[4], c[8], dropped = 0;   // the largest that this lane saw left out
+        if constexpr (J <= 4) {
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const int e = 4 * L * j + 4 * s;
-            uint32_t b[4];
+            for (int j = 0; j < J; ++j) {
+                const int e = 4 * L * j + 4 * s;
+                uint32_t b[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) b[i] = key_with(row.v[j].value(i), 4 * L * j + i + 4 * (L - 1));   // (s comes below)
-            if (more && e < a.E) row.v[j].load(next + e);   // the next row's, where these were
-            sort4(b);
-            if (j == 0) {
+                for (int i = 0; i < 4; ++i)   // (s comes below)
+                    b[i] = key_with(row.v[j].value(i), 4 * L * j + i + 4 * (L - 1));
+                if (more && e < a.E) row.v[j].load(next + e);   // the next row's, where these were
+                sort4(b);
+                if (j == 0) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) own[i] = b[i];
-            } else {
+                    for (int i = 0; i < 4; ++i) own[i] = b[i];
+                } else {
 #pragma unroll
-                for (int i = 0; i < 4; i += 2)
-                    dropped = max(dropped, max(min(own[i], b[3 - i]), min(own[i + 1], b[2 - i])));
-                merge4(own, b);
+                    for (int i = 0; i < 4; i += 2)
+                        dropped = max(dropped, max(min(own[i], b[3 - i]), min(own[i + 1], b[2 - i])));
+                    merge4(own, b);
+                }
             }
-        }
-        const uint32_t at_lane = 4 * (L - 1 - s);
-        dropped |= at_lane;
+            const uint32_t at_lane = 4 * (L - 1 - s);
+            dropped |= at_lane;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) own[i] |= at_lane;
+            for (int i = 0; i < 4; ++i) own[i] |= at_lane;
+        } else {
+#pragma unroll
+            for (int j = 0; j < J; j += 8) {
+                uint32_t b[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int e = 4 * L * (j + i) + 4 * s;
+                    b[i] = key_with(largest(row.v[j + i]), 4 * L * (j + i) + 4 * (L - 1)) | (4 * (L - 1 - s));
+                    if (more && e < a.E) row.v[j + i].load(next + e);
+                }
+                sort4(b);
+                sort4(b + 4);
+                join8(b);
+                if (j == 0) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) c[i] = b[i];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (sizeof(T) == 4) dropped = max(dropped, min(c[i], b[7 - i]));
+                        c[i] = max(c[i], b[7 - i]);
+                    }
+                    sort_bitonic8(c);
+                }
+            }
+#pragma unroll
+            for (int off = 1; off <= 4; off *= 2) {
+                dropped = max(dropped, take8(c, off, sizeof(T) == 4));
+                if (off < 4) sort_bitonic8(c);
+            }
+            // the eight lie the other way round in lanes 4 to 7: each lane of the row takes another one
+            const int mine_at = s < 4 ? s : 7 - s;
+            uint32_t mine = c[0];
+#pragma unroll
+            for (int i = 1; i < 4; ++i) mine = mine_at == i ? c[i] : mine;
+            const int e = (int)(kIndex - (mine & kIndex));
+            Raw<T, 4> v;
+            if (live && mine > kNone) v.load(logits + (size_t)t * a.E + e);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) own[i] = live && mine > kNone ? key_with(v.value(i), e + i) : 0;
+            sort4(own);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) c[i] = own[i], c[7 - i] = __shfl_xor_sync(kAll, own[i], 1);
         sort_bitonic8(c);
 #pragma unroll
         for (int off = 2; off <= 4; off *= 2) {
-            uint32_t o[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = __shfl_xor_sync(kAll, c[7 - i], off);
-            if (sizeof(T) == 4) {
-                if (off == 4) lost = max(lost, __shfl_xor_sync(kAll, lost, off));
-#pragma unroll
-                for (int i = 0; i < 8; i += 2) lost = max(lost, max(min(c[i], o[i]), min(c[i + 1], o[i + 1])));
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) c[i] = max(c[i], o[i]);
+            dropped = max(dropped, take8(c, off, sizeof(T) == 4));
             sort_bitonic8(c);
         }
         uint32_t key = c[0];   // of slot s
@@ -383,8 +467,8 @@ __global__ void __launch_bounds__(32 * kWarps, quad_blocks(J)) topk_quad_kernel(
         const uint32_t last = __shfl_sync(kAll, key, (lane & ~(L - 1)) + a.k - 1);
         bool unsure = dropped > kNone && (sizeof(T) == 4 ? dropped | kIndex : dropped) >= last, tied = false;
         if (sizeof(T) == 4) {
-            const uint32_t down = __shfl_down_sync(kAll, key, 1), below = s == L - 1 ? lost : down;
-            const bool close = live && s < a.k && below > kNone && (key ^ below) <= kIndex;
+            const uint32_t below = __shfl_down_sync(kAll, key, 1);
+            const bool close = live && s < L - 1 && s < a.k && below > kNone && (key ^ below) <= kIndex;
             unsure |= close && s == a.k - 1;
             tied = close && s < a.k - 1;   // only their order is not certain
         }
@@ -550,7 +634,7 @@ cudaError_t topk_t(TopkArgs a, cudaStream_t s) {
 }
 template <typename T, int J>
 cudaError_t quad_t(const TopkArgs &a, cudaStream_t s) {
-    const unsigned grid = blocks((int)(((long long)a.T + 3) / 4), quad_blocks(J));
+    const unsigned grid = blocks((int)(((long long)a.T + 3) / 4), quad_blocks(J, sizeof(T)));
     if (!a.sigmoid && !a.renorm) topk_quad_kernel<T, J, true><<<grid, 32 * kWarps, 0, s>>>(a);
     else topk_quad_kernel<T, J, false><<<grid, 32 * kWarps, 0, s>>>(a);
     return cudaGetLastError();
@@ -568,10 +652,12 @@ cudaError_t grad_t(const TopkGradArgs &a, cudaStream_t s) {
 template <typename T>
 cudaError_t topk_by_width(const TopkArgs &a, cudaStream_t s) {
     if (a.E % 4 == 0) {
-        // (fewer rows have a warp each, with a shorter chain: 256 of 256 take 3.4 us so, 3.9 by fours; 4096 5.4 and 4.3)
-        if (a.k <= 8 && a.E <= 256 && a.T >= 8 * a.E) {
+        // (fewer rows have a warp each, with a shorter chain: 1024 x 512 take 4.3 us so, 4.7 by fours; 2048 x 512 4.9 both
+        // ways, 4096 x 512 7.3 and 4.9, 1024 x 256 3.8 and 3.4)
+        if (a.k <= 8 && a.E <= 512 && a.T >= 4 * a.E) {
             if (a.E <= 64) return quad_t<T, 2>(a, s);
-            return a.E <= 128 ? quad_t<T, 4>(a, s) : quad_t<T, 8>(a, s);
+            if (a.E <= 128) return quad_t<T, 4>(a, s);
+            return a.E <= 256 ? quad_t<T, 8>(a, s) : quad_t<T, 16>(a, s);
         }
         if (a.E <= 128) return topk_t<T, 4, 1>(a, s);
         if (a.E <= 256) return topk_t<T, 4, 2>(a, s);

@@ -150,7 +150,7 @@ MANY = 40003      # rows enough that several share a warp
 
 
 @pytest.mark.parametrize("E,k", [(8, 8), (12, 1), (60, 4), (64, 8), (100, 7), (128, 8), (132, 8), (256, 8), (256, 3),
-                                 (256, 9), (61, 8), (260, 8)])
+                                 (256, 9), (61, 8), (260, 8), (512, 8), (512, 2), (388, 6), (512, 9)])
 @pytest.mark.parametrize("gating", [moe.SOFTMAX, moe.SIGMOID])
 @pytest.mark.parametrize("renormalize", [True, False])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
@@ -190,7 +190,7 @@ def awkward(T, E, dtype):
     return l.to(dtype)
 
 
-@pytest.mark.parametrize("E,k", [(256, 8), (256, 5), (128, 8), (60, 6), (32, 8)])
+@pytest.mark.parametrize("E,k", [(256, 8), (256, 5), (128, 8), (60, 6), (32, 8), (512, 8), (400, 3), (144, 8)])
 @pytest.mark.parametrize("gating,renormalize", [(moe.SOFTMAX, True), (moe.SIGMOID, True), (moe.SIGMOID, False)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_many_awkward_rows(E, k, gating, renormalize, dtype):
