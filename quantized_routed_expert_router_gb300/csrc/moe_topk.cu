@@ -18,7 +18,7 @@
 // are chosen, go four to a warp (topk_quad_kernel): x 512 28.3 us (38.9 with a warp a
 // row), x 256 19.9 (26.2), x 128 15.2 (19.3), x 64 12.2 (18.7); in bf16 19.6 (34.6),
 // 14.1 (23.7), 13.7 (16.8), 11.2 (16.8).  The gradient moves more and decides less:
-// 65536 x 128 in bf16 over all E 12.4 us (4.4 TB/s).
+// 65536 x 128 in bf16 over all E 11.3 us (4.8 TB/s).
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -32,7 +32,9 @@ namespace {
 constexpr int kWarps = 8;
 constexpr unsigned kAll = 0xFFFFFFFFu;
 // blocks of a launch that share an SM (registers for the rows in hand); of the gradient, with one row more
-constexpr int grad_blocks(int values) { return values <= 4 ? 5 : values <= 8 ? 4 : values <= 16 ? 2 : 1; }
+constexpr int grad_blocks(int values, bool row) {
+    return values <= 4 ? 5 : values <= 8 ? 4 : values <= 16 ? (row ? 2 : 3) : 1;
+}
 constexpr int blocks_per_sm(int values) { return values <= 4 ? 6 : values <= 8 ? 5 : values <= 16 ? 3 : 2; }
 
 constexpr int quad_blocks(int pieces, int bytes) {
@@ -63,10 +65,13 @@ __device__ __forceinline__ float lanes_sum(float v) {
 }
 template <int L>
 __device__ __forceinline__ float lanes_max(float v) {
-    if constexpr (L == 32) return warp_max(v);
+    if constexpr (L == 32) {
+        return warp_max(v);
+    } else {
 #pragma unroll
-    for (int off = L / 2; off >= 1; off >>= 1) v = max_nan(v, __shfl_xor_sync(kAll, v, off));
-    return v;
+        for (int off = L / 2; off >= 1; off >>= 1) v = max_nan(v, __shfl_xor_sync(kAll, v, off));
+        return v;
+    }
 }
 
 // a row of logits in L lanes; past E, where load does not come, it is -inf
@@ -516,12 +521,12 @@ struct TopkGradArgs {
     int T, E, k, sigmoid, renorm;
 };
 
-// ROW: the gradient reaches the whole row (softmax over all E); otherwise the chosen experts.  A row takes L lanes: two rows
-// share a warp where they fit (65536 rows of 128 in bf16: 18.5 us with a warp a row, most of it the instructions that do not
-// depend on E).  The next row's slots and logits are under way as in topk_kernel (a row is read before it is written, by the
+// ROW: the gradient reaches the whole row (softmax over all E); otherwise the chosen experts.  A row takes L lanes: two or
+// four rows share a warp where they fit, as most instructions do not depend on E (65536 rows of 128 in bf16, over all E: 18.5 us
+// with a row a warp, 12.4 with two, 11.3 with four; of 64, renormalised, 9.0 with two and 5.6 with four).  The next row's slots and logits are under way as in topk_kernel (a row is read before it is written, by the
 // warp that it belongs to: dlogits may be logits).
 template <typename T, int VEC, int J, bool ROW, int L>
-__global__ void __launch_bounds__(32 * kWarps, grad_blocks(VEC * J)) topk_grad_kernel(const TopkGradArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, grad_blocks(VEC * J, ROW)) topk_grad_kernel(const TopkGradArgs a) {
     extern __shared__ float buf[];   // a row's values
     const int lane = threadIdx.x & (L - 1), first = (threadIdx.x & 31) / L;   // in its row; the row of the warp
     const int warp = threadIdx.x >> 5, step = gridDim.x * kWarps * (32 / L);
@@ -642,8 +647,9 @@ cudaError_t quad_t(const TopkArgs &a, cudaStream_t s) {
 template <typename T, int VEC, int J, int L>
 cudaError_t grad_t(const TopkGradArgs &a, cudaStream_t s) {
     constexpr int smem = kWarps * 32 * VEC * J * (int)sizeof(float);   // 32 KB at most
-    const unsigned grid = blocks((a.T + 32 / L - 1) / (32 / L), grad_blocks(VEC * J));
-    if (!a.sigmoid && !a.renorm) topk_grad_kernel<T, VEC, J, true, L><<<grid, 32 * kWarps, smem, s>>>(a);
+    const bool row = !a.sigmoid && !a.renorm;
+    const unsigned grid = blocks((a.T + 32 / L - 1) / (32 / L), grad_blocks(VEC * J, row));
+    if (row) topk_grad_kernel<T, VEC, J, true, L><<<grid, 32 * kWarps, smem, s>>>(a);
     else topk_grad_kernel<T, VEC, J, false, L><<<grid, 32 * kWarps, smem, s>>>(a);
     return cudaGetLastError();
 }
@@ -670,11 +676,12 @@ cudaError_t topk_by_width(const TopkArgs &a, cudaStream_t s) {
 }
 template <typename T>
 cudaError_t grad_by_width(const TopkGradArgs &a, cudaStream_t s) {
-    const bool two = a.k <= 16;   // rows a warp, where 16 lanes hold one
+    const bool four = a.k <= 8, two = a.k <= 16;   // rows a warp, where 8 or 16 lanes hold one
     if (a.E % 4 == 0) {
-        if (a.E <= 64 && two) return grad_t<T, 4, 1, 16>(a, s);
-        if (a.E <= 128) return two ? grad_t<T, 4, 2, 16>(a, s) : grad_t<T, 4, 1, 32>(a, s);
-        if (a.E <= 256) return grad_t<T, 4, 2, 32>(a, s);
+        if (a.E <= 64 && two) return four ? grad_t<T, 4, 2, 8>(a, s) : grad_t<T, 4, 1, 16>(a, s);
+        if (a.E <= 128 && two) return four ? grad_t<T, 4, 4, 8>(a, s) : grad_t<T, 4, 2, 16>(a, s);
+        if (a.E <= 128) return grad_t<T, 4, 1, 32>(a, s);
+        if (a.E <= 256) return two ? grad_t<T, 4, 4, 16>(a, s) : grad_t<T, 4, 2, 32>(a, s);
         if (a.E <= 512) return grad_t<T, 4, 4, 32>(a, s);
         return grad_t<T, 4, 8, 32>(a, s);
     }

@@ -48,7 +48,8 @@ def logits(T, E, g, dtype, spread=1.5):
 
 
 SIZES = [(1, 1, 1), (1, 8, 8), (3, 7, 2), (16, 128, 8), (5, 33, 5), (4, 64, 1), (9, 65, 4), (17, 100, 32), (7, 130, 9),
-         (33, 256, 8), (21, 260, 8), (6, 512, 6), (5, 513, 7), (11, 1024, 32), (4, 1021, 3), (4099, 60, 4), (2050, 32, 8)]
+         (33, 256, 8), (21, 260, 8), (6, 512, 6), (5, 513, 7), (11, 1024, 32), (4, 1021, 3), (4099, 60, 4), (2050, 32, 8),
+         (37, 48, 12), (37, 128, 16), (37, 256, 16), (37, 256, 20), (4099, 128, 8), (4099, 256, 8), (2051, 64, 6)]
 
 
 @pytest.mark.parametrize("T,E,k", SIZES)
