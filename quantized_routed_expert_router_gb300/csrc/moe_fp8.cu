@@ -82,7 +82,7 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t ad, uint64_t bd, u
         "r"(me)
         : "memory");
 }
-// two sums += {lo, hi} * {s, s}, staying behind the wait for lo and hi
+// two sums += {lo, hi} * {s, s}
 __device__ __forceinline__ void fma2(uint64_t &acc, uint32_t lo, uint32_t hi, uint64_t ss) {
     asm volatile("{\n .reg .b64 d;\n mov.b64 d, {%1, %2};\n fma.rn.f32x2 %0, d, %3, %0;\n}"
                  : "+l"(acc) : "r"(lo), "r"(hi), "l"(ss));
@@ -407,15 +407,16 @@ __global__ void __launch_bounds__(Shape<BN>::THREADS, 1)
                 if (work) {
                     // all 64 columns on their way at once; the buffer goes back before they are added
                     uint32_t u[2][32];
-                    tmem_ld32(at0 + d.i * BN, u[0]);
-                    tmem_ld32(at0 + d.i * BN + 32, u[1]);
+                    tmem_ld32_begin(at0 + d.i * BN, u[0]);
+                    tmem_ld32_begin(at0 + d.i * BN + 32, u[1]);
                     uint64_t ss;
                     asm volatile("mov.b64 %0, {%1, %1};" : "=l"(ss) : "r"(__float_as_uint(nx * nw)));
                     if (kb + 1 < kb1) {
                         nx = xs[kb + 1];
                         nw = ws[kb + 1];
                     }
-                    tmem_ld_wait();
+                    tmem_landed(u[0]);
+                    tmem_landed(u[1]);
                     fence_before();
                     bar_arrive(&c.dempty[d.i], lane == 0);
 #pragma unroll

@@ -505,7 +505,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                         if (j >= tl.rows) continue;
                         uint32_t u[32];
                         tmem_ld32(at0 + d.i * BT + j, u);
-                        tmem_ld_wait();
 #pragma unroll
                         for (int i = 0; i < 32; ++i) acc[p][i] += __uint_as_float(u[i]);
                     }
@@ -539,7 +538,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int j = 32 * half; j < tl.rows; j += 64) {
                     uint32_t u[32];
                     tmem_ld32(at0 + d.i * BT + j, u);
-                    tmem_ld_wait();
 #pragma unroll 1
                     for (int h = 0; h < 32 && j + h < tl.rows; h += 16) {
                         float v[16];
