@@ -53,13 +53,25 @@ __device__ __forceinline__ bool bar_test(uint64_t *b, uint32_t parity) {
         : "=r"(ok) : "r"(sa(b)), "r"(parity) : "memory");
     return ok != 0;
 }
-// Arrives at the barrier at the same place in block `rank` of the cluster.  What it stands for are copies and products,
-// which have barriers and fences of their own; ordered for the cluster (release, acquire) it and the wait for it took 2000
-// cycles a stage.
+// Barriers at which another block of the cluster arrives, or its tensor cores do: the wait acquires, and the arrival releases,
+// at the cluster's scope, by fences that are about shared memory alone.  With mbarrier's own .release.cluster and
+// .acquire.cluster, which are about all memory, a stage's hand-over between two blocks took 2000 cycles (8192^3: 1757 us, so
+// 597); with the release alone on the hand-over of TMEM buffers fp32 results waited for the epilogue's stores (8192 x 2048 by
+// 7168 x 2048: 195 us, so 174).
+__device__ __forceinline__ bool bar_test_cluster(uint64_t *b, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " @p fence.acquire.sync_restrict::shared::cluster.cluster;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok) : "r"(sa(b)), "r"(parity) : "memory");
+    return ok != 0;
+}
+// arrives at the barrier at the same place in block `rank` of the cluster
 __device__ __forceinline__ void bar_arrive_at(uint64_t *b, uint32_t rank, uint32_t me) {
     asm volatile(
         "{\n .reg .pred e;\n .reg .b32 at;\n setp.ne.u32 e, %2, 0;\n mapa.shared::cluster.u32 at, %0, %1;\n"
-        " @e mbarrier.arrive.shared::cluster.b64 _, [at];\n}" ::"r"(sa(b)), "r"(rank), "r"(me)
+        " @e fence.release.sync_restrict::shared::cta.cluster;\n"
+        " @e mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [at];\n}" ::"r"(sa(b)), "r"(rank), "r"(me)
         : "memory");
 }
 // 1 in one lane of a converged warp.  The single-thread instructions (copies,
@@ -74,10 +86,13 @@ __device__ __forceinline__ uint32_t elect() {
 }
 // wait for a phase; false once this block has given up (the first wait to run
 // out says so to the others, in *abort in shared memory, and in the status word).
+// CLUSTER: another block, or its tensor cores, arrive at the barrier.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, int *abort, uint32_t limit, unsigned *status) {
-    if (bar_test(b, parity)) return true;
+    const auto test = [&] { return CLUSTER ? bar_test_cluster(b, parity) : bar_test(b, parity); };
+    if (test()) return true;
     const uint32_t t0 = clock_hi();
-    while (!bar_test(b, parity)) {
+    while (!test()) {
         if (*(volatile int *)abort) return false;
         if (clock_hi() - t0 > limit) {
             *(volatile int *)abort = 1;

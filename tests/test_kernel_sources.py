@@ -51,3 +51,25 @@ def test_loads_that_go_on_are_waited_for_by_their_registers(name):
     landed = re.findall(r"tmem_landed\(([\w\[\]]+)\);", text)
     assert sorted(begun) == sorted(landed)
     assert not re.search(r"tcgen05\.(ld|wait)", text)     # only through the helpers
+
+
+def test_arrivals_at_another_block_release_for_the_cluster():
+    """An arrival without a scope is ordered for its own block alone, and so is a wait without one."""
+    remote = [s for s in statements(source("moe_tc.cuh")) if re.search(r"mbarrier\.arrive\S*shared::cluster", s)
+              and "tcgen05.commit" not in s]
+    assert remote
+    for s in remote:
+        code = "".join(re.findall(r'"((?:[^"\\]|\\.)*)"', s))
+        assert re.search(r"mbarrier\.arrive\.release\.cluster\.", code) or re.search(
+            r"fence\.(release\.sync_restrict::shared::cta|acq_rel)\.cluster;.*mbarrier\.arrive\.relaxed\.cluster\.", code), s
+    waits = [s for s in statements(source("moe_tc.cuh")) if "mbarrier.try_wait" in s]
+    assert any(re.search(r"try_wait\.parity\.(acquire\.cluster|relaxed\.cluster.*fence\.acquire\S*\.cluster)", s, re.S)
+               for s in waits)
+
+
+def test_waits_for_another_block_acquire_for_the_cluster():
+    """Of the products' barriers only `full` is signalled by the waiting block alone."""
+    waits = re.findall(r"bar_wait(<PAIR>)?\(&c\.(\w+)\[", source("moe_matmul.cu"))
+    assert {name for _, name in waits} == {"full", "done", "other", "sums", "read"}
+    for cluster, name in waits:
+        assert bool(cluster) == (name != "full"), name
