@@ -39,6 +39,7 @@
 #include <cuda_bf16.h>
 
 #include "moe_around.h"
+#include "moe_device.h"
 #include "moe_launch.h"
 #include "moe_matmul.cuh"
 #include "moe_tc.cuh"
@@ -599,6 +600,11 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 // ------------------------------------------------------------------ host
 
+int current_device() {
+    int dev = -1;
+    return cudaGetDevice(&dev) == cudaSuccess ? dev : -1;
+}
+
 bool encode(CUtensorMap *m, int dims, const void *p, const cuuint64_t *size, const cuuint64_t *stride,
             const cuuint32_t *box) {
     const cuuint32_t steps[5] = {1, 1, 1, 1, 1};
@@ -642,11 +648,12 @@ cudaError_t launch_t(const MatmulArgs &a, int grid, int cluster, cudaStream_t s)
     cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     if (err != cudaSuccess) return err;
     if (PAIR && !SPLIT && sizeof(TY) == 4) {   // the registers that its warps hand on have to be there
-        static const bool there = [k] {
+        static PerDevice registers;
+        const int have = registers.get(current_device(), [k] {
             cudaFuncAttributes at;
-            return cudaFuncGetAttributes(&at, k) == cudaSuccess && at.numRegs >= LAUNCH_REGS;
-        }();
-        if (!there) return cudaErrorInvalidConfiguration;
+            return cudaFuncGetAttributes(&at, k) == cudaSuccess ? at.numRegs : -1;
+        });
+        if (have < LAUNCH_REGS) return cudaErrorInvalidConfiguration;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
@@ -664,10 +671,11 @@ cudaError_t launch_t(const MatmulArgs &a, int grid, int cluster, cudaStream_t s)
     return cudaLaunchKernelEx(&cfg, k, mx, mx_less, mw, a);
 }
 
-// clusters of SIZE blocks that fit the GPU at once (its SMs come in groups, and a cluster lies within one); 0: not known
+// clusters of SIZE blocks that fit the GPU at once (its SMs come in groups, and a cluster lies within one); negative: not known
 template <int BT, bool PAIR, typename TY, int SIZE>
 int clusters_at_once() {
-    static const int n = [] {
+    static PerDevice clusters;
+    return clusters.get(current_device(), [] {
         auto *k = matmul_kernel<BT, PAIR, true, TY>;
         constexpr int smem = Shape<BT, PAIR>::SMEM;
         int n = 0;
@@ -684,11 +692,10 @@ int clusters_at_once() {
         if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
             cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess) {
             cudaGetLastError();   // this call goes on without
-            return 0;
+            return -1;
         }
         return n;
-    }();
-    return n;
+    });
 }
 // how many parts of the depth n tiles can have: every part with 4 blocks of depth and an SM (a pair: two) of its own, and all
 // clusters at once (16 of 8 blocks did not fit: 64 x 7168 by 2048 x 7168 18.8 us in 8 parts, 14.5 in 4; 64 x 8192 by
