@@ -635,8 +635,10 @@ moe_status moe_combine_grad(const void *dy, moe_dtype ydtype, const int32_t *pos
  * Errors: MOE_ERR_INVALID_ARG for limits, types, act, a NULL buffer, X < M without
  * rows, X == 0, offsets missing with G > 1, bias, residual or z where they have no
  * place, z missing, or x, w, y, z, residual not 16-byte aligned (bias, rows,
- * offsets: 4); MOE_ERR_UNSUPPORTED for K or N outside the rules above or more than
- * 2^30 tiles of 128 x 16; MOE_ERR_WORKSPACE for a missing, short or unaligned ws.
+ * offsets: 4); MOE_ERR_UNSUPPORTED for K or N outside the rules above, or for 2^30 or
+ * more tiles of 128 columns (gate and up counted) by 32 places, of which there are
+ * ceil(M / 32) a column tile, with offsets floor(M / 32) + min(G, M);
+ * MOE_ERR_WORKSPACE for a missing, short or unaligned ws.
  */
 moe_status moe_matmul(const void *x, int X, const int32_t *rows, int M, const int32_t *offsets, int G, const void *w,
                       int transposed, const float *bias, moe_act act, const void *residual, void *z, int N, int K,
