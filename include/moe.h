@@ -625,7 +625,8 @@ moe_status moe_combine_grad(const void *dy, moe_dtype ydtype, const int32_t *pos
  * sizes may add up in another order.  For fp32 results a running sum of the tensor
  * cores, which cut off below 24 bits, is at most 640 values long (their error is then
  * about 5e-7 of v); for bf16 it goes over the whole depth.  Activations are fp32, of
- * the unrounded v, with sigma by the machine's exp (off by (5 + 1.3 |v|) 2^-24 of itself).
+ * the unrounded v, with sigma by the machine's exp (off by (5 + 1.3 |v|) 2^-24 of itself;
+ * what lies below 2^-126, from about v = -87.3 down, counts as 0).
  * Row indexes and offsets outside their ranges are never followed (MOE_DEV_BAD_ROW);
  * the product of such a row is 0.  y and z must not overlap x, w or one another but
  * as stated.

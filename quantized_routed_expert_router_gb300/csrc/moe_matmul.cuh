@@ -26,7 +26,7 @@ struct MatmulArgs {
     int hold_copies, hold_products;
 };
 
-// 1 / (1 + exp(-v)) by the machine's exp and reciprocal: off by (5 + 1.3 |v|) 2^-24 of itself
+// 1 / (1 + exp(-v)) by the machine's exp and reciprocal: off by (5 + 1.3 |v|) 2^-24 of itself, 0 below 2^-126
 __device__ __forceinline__ float sigmoid(float v) {
     float e, r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.4426950408889634f));
