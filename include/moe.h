@@ -622,9 +622,11 @@ moe_status moe_combine_grad(const void *dy, moe_dtype ydtype, const int32_t *pos
  *              word, moe_read_device_status), zero-filled before its first use.
  *              Calls that overlap on the GPU may share it.
  * Sums are fp32, in one order for given sizes: equal calls give equal bits, other
- * sizes may add up in another order.  For fp32 results a running sum of the tensor
- * cores, which cut off below 24 bits, is at most 640 values long (their error is then
- * about 5e-7 of v); for bf16 it goes over the whole depth.  Activations are fp32, of
+ * sizes may add up in another order.  The tensor cores cut a running sum off below 24
+ * bits, towards zero.  For fp32 results it is at most 640 values long (over a matrix of
+ * results the error is about 5e-7 of them in the norm, and within 1e-6); for bf16 at
+ * most 8192 (about 2^-15 of itself where all terms have one sign, beside the rounding to
+ * bf16 by up to 2^-8).  Activations are fp32, of
  * the unrounded v, with sigma by the machine's exp (off by (5 + 1.3 |v|) 2^-24 of itself;
  * what lies below 2^-126, from about v = -87.3 down, counts as 0).
  * Row indexes and offsets outside their ranges are never followed (MOE_DEV_BAD_ROW);

@@ -31,10 +31,11 @@
 // splits the depth of a tile and adds its parts through distributed shared memory
 // in rank order.
 //
-// Sums.  The tensor cores cut off what they add below the 24 bits of a running sum, always towards
-// zero: over K values that is about K 2^-30 of the sum, 1.7e-6 at K = 2048.  Beside a rounding to bf16 it does
-// not count.  For fp32 results (TY = float) a running sum is at most 640 values of depth long and these are added
-// in fp32: 3e-7 to 6e-7, the more the larger a few channels of the rows are (768 long: 6e-7 to 9e-7).
+// Sums.  The tensor cores cut off what they add below the 24 bits of a running sum, always towards zero.  Over K values that
+// is about K 2^-30 of the results where terms have both signs (1.7e-6 at K = 2048), and more where they have one: 4e-6 at
+// 2048, 3.3e-5 at 8192, 1.8e-4 at 32768, 1.9e-3 at 262144.  So running sums are bounded and added up in fp32 (RUNS): for fp32
+// results 640 values long at most, which leaves 4e-7 to 8e-7 at any K, the more the larger a few channels of the rows
+// are (768 long: 6e-7 to 9e-7); for bf16 results, which are rounded by up to 2^-8, 8192 long, so that most have one.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -59,6 +60,7 @@ constexpr int LAUNCH_REGS = 168, FEED_REGS = 88, EPI_REGS = 208;
 // stages of a running sum of fp32 results: of a tile's first two, which the products can fill while the epilogue is busy with
 // the tile before, and of the others
 constexpr int FIRST_RUNS = 10, RUN = 8;
+constexpr int WHOLE = 128;   // of bf16 results
 
 template <int BT, bool PAIR>
 struct Shape {
@@ -213,13 +215,12 @@ __device__ __forceinline__ void clear_bad(const MatmulArgs &a, float (&v)[C], in
 // places of a tile that one of a pair's blocks loads (a product takes them in 32s)
 __device__ __forceinline__ int half_of(int rows) { return ((rows + 31) >> 5) << 4; }
 
-template <int BT, bool PAIR, bool SPLIT, typename TY>
+template <int BT, bool PAIR, bool SPLIT, bool RUNS, typename TY>
 __global__ void __launch_bounds__(THREADS, 1)
     matmul_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mx_less,
                   const __grid_constant__ CUtensorMap mw, const MatmulArgs a) {
     using S = Shape<BT, PAIR>;
     constexpr int STAGES = S::STAGES, NBUF = S::NBUF;
-    constexpr bool RUNS = sizeof(TY) == 4;
     extern __shared__ uint8_t raw[];
     __shared__ Ctl c;
     uint8_t *stages = raw + ((1024 - (sa(raw) & 1023)) & 1023);
@@ -296,10 +297,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int t0 = (int)blockIdx.x / size, dt = SPLIT ? total : (int)gridDim.x / size;
     const int kb0 = SPLIT ? part * a.KB / parts : 0, kb1 = SPLIT ? (part + 1) * a.KB / parts : a.KB;
     const auto run_end = [&](int kb) {   // of the running sum that starts with stage kb
-        return !RUNS ? kb1 : min(kb + (kb < kb0 + 2 * FIRST_RUNS ? FIRST_RUNS : RUN), kb1);
+        return !RUNS ? kb1 : min(kb + (sizeof(TY) == 2 ? WHOLE : kb < kb0 + 2 * FIRST_RUNS ? FIRST_RUNS : RUN), kb1);
     };
 
-    // Registers: the running sums of fp32 results take 128, beside 32 on their way.
+    // Registers: the running sums take 128, beside 32 on their way.
     constexpr bool MOVE = RUNS && PAIR && !SPLIT;
     static_assert(FEED_REGS * 32 * EPI_FIRST + EPI_REGS * 32 * EPI_WARPS <= LAUNCH_REGS * THREADS, "");
     if (warp < EPI_FIRST) {
@@ -635,7 +636,7 @@ bool encode_w(CUtensorMap *m, const MatmulArgs &a) {
     return encode(m, 3, a.w, size, stride, box);
 }
 
-template <int BT, bool PAIR, bool SPLIT, typename TY>
+template <int BT, bool PAIR, bool SPLIT, bool RUNS, typename TY>
 cudaError_t launch_t(const MatmulArgs &a, int grid, int cluster, cudaStream_t s) {
     using S = Shape<BT, PAIR>;
     CUtensorMap mx, mx_less, mw;
@@ -644,10 +645,10 @@ cudaError_t launch_t(const MatmulArgs &a, int grid, int cluster, cudaStream_t s)
     if (!encode_fn()) return cudaErrorSymbolNotFound;
     if (!encode(&mx, 2, a.x, size, stride, box) || !encode(&mx_less, 2, a.x, size, stride, less) || !encode_w(&mw, a))
         return cudaErrorInvalidValue;
-    auto *k = matmul_kernel<BT, PAIR, SPLIT, TY>;
+    auto *k = matmul_kernel<BT, PAIR, SPLIT, RUNS, TY>;
     cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     if (err != cudaSuccess) return err;
-    if (PAIR && !SPLIT && sizeof(TY) == 4) {   // the registers that its warps hand on have to be there
+    if (PAIR && !SPLIT && RUNS) {   // the registers that its warps hand on have to be there
         static PerDevice registers;
         const int have = registers.get(current_device(), [k] {
             cudaFuncAttributes at;
@@ -676,7 +677,7 @@ template <int BT, bool PAIR, typename TY, int SIZE>
 int clusters_at_once() {
     static PerDevice clusters;
     return clusters.get(current_device(), [] {
-        auto *k = matmul_kernel<BT, PAIR, true, TY>;
+        auto *k = matmul_kernel<BT, PAIR, true, sizeof(TY) == 4, TY>;   // (RUNS asks for the same threads and memory)
         constexpr int smem = Shape<BT, PAIR>::SMEM;
         int n = 0;
         cudaLaunchConfig_t cfg = {};
@@ -710,16 +711,24 @@ int parts_of(long long n, int KB) {
     if (PAIR || !room(MAX_SPLIT, clusters_at_once<BT, PAIR, TY, 8>())) return 4;
     return MAX_SPLIT;
 }
+template <int BT, bool PAIR, bool RUNS, typename TY>
+cudaError_t launch_tiles_t(const MatmulArgs &a, long long n, int parts, cudaStream_t s) {
+    constexpr int PER = PAIR ? 2 : 1;
+    if constexpr (!PAIR || BT == 256) {   // (of pairs with fewer places there are many)
+        if (parts > 1) return launch_t<BT, PAIR, true, RUNS, TY>(a, (int)n * parts * PER, parts * PER, s);
+    }
+    const long long most = num_sms() / PER;
+    return launch_t<BT, PAIR, false, RUNS, TY>(a, (int)(n < most ? n : most) * PER, PER, s);
+}
 template <int BT, bool PAIR, typename TY>
 cudaError_t launch_tiles(MatmulArgs a, int wide, long long n, int parts, cudaStream_t s) {
     constexpr int PER = PAIR ? 2 : 1;
     a.ntn = (wide + PER * BN - 1) / (PER * BN);
     a.whole = wide / (PER * BN);
-    if constexpr (!PAIR || BT == 256) {   // (of pairs with fewer places there are many)
-        if (parts > 1) return launch_t<BT, PAIR, true, TY>(a, (int)n * parts * PER, parts * PER, s);
+    if constexpr (sizeof(TY) == 2) {
+        if ((a.KB + parts - 1) / parts <= WHOLE) return launch_tiles_t<BT, PAIR, false, TY>(a, n, parts, s);
     }
-    const long long most = num_sms() / PER;
-    return launch_t<BT, PAIR, false, TY>(a, (int)(n < most ? n : most) * PER, PER, s);
+    return launch_tiles_t<BT, PAIR, true, TY>(a, n, parts, s);
 }
 
 template <typename TY>
