@@ -746,15 +746,18 @@ cudaError_t launch_matmul_t(const MatmulArgs &a, cudaStream_t s) {
     const int single = parts_of<128, false, TY>(n128, a.KB);
     if (a.offsets) {
         // Pairs where that leaves one of them for every other SM.  Few places a group: shorter stages, and more of them on
-        // their way (3108 rows over 32 of 2880 x 2880, 97 a group: 104.9 us, by 256 places 108.7).
+        // their way, until many groups take a second tile (us by 128, by 256 places: 70 places a group of 128 of 1536 x 2048
+        // 138.8, 144.4; 97 of 32 of 2880 x 2880 101.8, 106.5; 110 of 16 of 4096 x 4096 93.5, 101.7, of 64 of 2048 x 1408 72.4,
+        // 70.9; 128 108.1, 108.8 and 110.6, 103.1 and 77.5, 72.0; 160 140.2, 112.9 and 124.3, 104.9 and 99.4, 74.8).
         if (rows <= 64 || 2 * n256 < sms) return launch_tiles<128, false, TY>(a, wide, n128, single, s);
         return rows <= 110 ? launch_tiles<128, true, TY>(a, wide, tiles(128, 2 * BN), 1, s)
                            : launch_tiles<256, true, TY>(a, wide, n256, 1, s);
     }
     // One matrix: what takes fewer cycles.  A stage of either comes in about 560 (32 KB from L2); pairs have a longer start and
-    // end, and an exchange between parts its own.  us, by pairs and by one block a tile: 256 x 2048 by 7168 x 2048 16.8, 14.6;
-    // 512 18.7, 24.3; 2048 38.1, 59.6; 512 x 7168 by 2048 x 7168 26.9, 22.8; 1024 28.8, 35.0; 2048 x 1000 by 1000 x 1000
-    // 16.5, 12.6.
+    // end, and an exchange between parts its own.  us, by pairs and by one block a tile: 256 x 2048 by 7168 x 2048 16.2, 13.9;
+    // 512 17.9, 22.7; 2048 37.5, 58.1; 512 x 7168 by 2048 x 7168 26.1, 21.5; 1024 27.3, 33.6; 512 x 4096 by 4096 x 4096 22.4,
+    // 22.7; 1024 x 4096 by 1536 x 4096 19.5, 21.2; 512 x 2880 by 2880 x 2880 16.8, 16.2; 2048 x 4096 by 512 x 4096 19.0, 15.5;
+    // 256 x 1024 by 8192 x 1024 13.3, 9.3 (128 to 4096 rows by these seven matrices: the faster, or within 4% of it).
     const int both = parts_of<256, true, TY>(n256, a.KB);
     const auto cycles = [&](long long n, int parts, long long slots, int stage, int fixed, int exchange) {
         return (n + slots - 1) / slots * ((a.KB + parts - 1) / parts) * stage + fixed + (parts > 1 ? exchange : 0);

@@ -10,6 +10,11 @@
 // device: combine 8192 x 8 rows of 4096 in bf16 90.8 us (0.98 of the copy rate),
 // dispatch 4096 x 8 of 7168 78.5 (0.97), the gradient 8191 x 4 of 2880 65.7 (0.95;
 // 86.6 with blocks of 128 threads whose last round over a row was mostly empty).
+//   Narrow rows leave threads of a block idle, and rows that are no multiple of 8 values
+// go by pairs or single values: 65536 x 8 of 256 in bf16 dispatch 48.5, combine 59.2,
+// gradient 91.0 us (0.92, 0.76 and 0.93 of the copy rate), of 128 35.3, 54.5 and 68.6
+// (0.64, 0.42, 0.63); 32768 x 8 of 1026 142, 225 and 251 (0.63, 0.40, 0.67), of 1001 210,
+// 354 and 305 (0.42, 0.25, 0.54), of 1028 in fp32 199, 222 and 360 (0.90, 0.81, 0.94).
 #include <cuda_bf16.h>
 
 #include "moe_around.h"

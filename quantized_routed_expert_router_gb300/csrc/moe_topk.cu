@@ -12,13 +12,16 @@
 // (choose_exactly): two of the k + 1 largest that agree in their upper 22 bits (fp32
 // logits: about two rows in a hundred; bf16 ones are exact), or four of the chosen in
 // one lane (8 of 256: four rows in a thousand; 32 of 1024: half of them).
-// Issue slots bound it: 65536 rows of 256 in fp32, 8 chosen, take 26.2 us on the
-// device so (298 instructions a row, the integer pipe 63% busy), 63.6 when every round
-// looked through all values of its lane.  Many rows of up to 512, of which up to eight
-// are chosen, go four to a warp (topk_quad_kernel): x 512 28.3 us (38.9 with a warp a
-// row), x 256 19.9 (26.2), x 128 15.2 (19.3), x 64 12.2 (18.7); in bf16 19.6 (34.6),
-// 14.1 (23.7), 13.7 (16.8), 11.2 (16.8).  The gradient moves more and decides less:
-// 65536 x 128 in bf16 over all E 11.3 us (4.8 TB/s).
+// 65536 rows of 256 in fp32, 8 chosen, take 26.2 us on the device so (298 instructions
+// a row, the integer pipe 63% busy), 63.6 when every round looked through all values
+// of its lane.  Many rows of up to 512, of which up to eight are chosen, go four to a
+// warp (topk_quad_kernel): x 512 28.3 us (38.9 with a warp a row), x 256 19.9 (26.2),
+// x 128 15.2 (19.3), x 64 12.2 (18.7); in bf16 19.6 (34.6), 14.1 (23.7), 13.7 (16.8),
+// 11.2 (16.8).  No unit is full there (x 256 in fp32: 54% of the issue slots, the integer
+// pipe at 69%, DRAM at 39%): warps wait, most for the chosen pieces and then the chosen
+// logits, which are read again one behind the other.  The gradient moves more and decides
+// less: 65536 x 128 in bf16 over all E 12.1 us (4.5 TB/s), 60% of the issue slots; it
+// waits for shared memory, which it uses value by value.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -522,8 +525,9 @@ struct TopkGradArgs {
 };
 
 // ROW: the gradient reaches the whole row (softmax over all E); otherwise the chosen experts.  A row takes L lanes: two or
-// four rows share a warp where they fit, as most instructions do not depend on E (65536 rows of 128 in bf16, over all E: 18.5 us
-// with a row a warp, 12.4 with two, 11.3 with four; of 64, renormalised, 9.0 with two and 5.6 with four).  The next row's slots and logits are under way as in topk_kernel (a row is read before it is written, by the
+// four rows share a warp where they fit, as most instructions do not depend on E (calls that write the same rows, 65536 of 128
+// in bf16, over all E: 18.5 us with a row a warp, 12.4 with two, 11.3 with four; of 64, renormalised, 9.0 with two and 5.6
+// with four).  The next row's slots and logits are under way as in topk_kernel (a row is read before it is written, by the
 // warp that it belongs to: dlogits may be logits).
 template <typename T, int VEC, int J, bool ROW, int L>
 __global__ void __launch_bounds__(32 * kWarps, grad_blocks(VEC * J, ROW)) topk_grad_kernel(const TopkGradArgs a) {
